@@ -198,9 +198,11 @@ def _prepare_plan(case, seed):
     rnd.shuffle(order)
     old, new = [old[i] for i in order], [new[i] for i in order]
     m, page = case["m"], case["page"]
+    max_pages = max(-(-((o + n) // m) // page) for o, n in zip(old, new)) + 6
+    # up to four pages more in the past of every live request, by the seed: what is new stays as much
+    old = [o + m * page * rnd.randrange(5) if o + n else 0 for o, n in zip(old, new)]
     held = [-(-(o // m) // page) for o in old]
     need = [-(-((o + n) // m) // page) for o, n in zip(old, new)]
-    max_pages = max(max(need), 1) + 2
     n_pages = sum(need) + 64
     ids = torch.randperm(n_pages, generator=torch.Generator().manual_seed(seed), dtype=torch.int64).to(torch.int32)
     table = torch.full((case["batch"], max_pages), -1, dtype=torch.int32)
