@@ -375,6 +375,128 @@ int hca_attend_fp8kv(const uint16_t *q, const float *q_gain, const float *sinks,
                      float eps, uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Paged caches ("DeepSeek-V4-Pro - Model techniques map", KV-cache layout and
+ * pool rows: serving keeps the compressed entries of all requests in one pool
+ * of fixed-size pages; the pages give no format, the one used here follows).
+ *
+ *  * The pool holds n_pages pages of `page` rows (entries) each; entry j of
+ *    request b is row block_table[b][j / page] * page + j % page of the pool,
+ *    its slot.  A page may stand in several rows of the table (a shared prefix).
+ *  * The window rows of request b live in a ring of ring_rows rows: the row of
+ *    position u is ring row u % ring_rows, slot b * ring_rows + u % ring_rows.
+ *  * A row of the batch without a request (an empty slot) has lengths 0 in
+ *    csa_plan_pages and q_pos = -1 in the attention.
+ *
+ * csa_plan_pages -- block tables and slot maps of one step, from the requests'
+ * lengths, on the device.  Request b has old_len[b] tokens cached and appends
+ * new_len[b]; with e0 = floor(old / m) and e1 = floor((old + new) / m) entries
+ * before and after, it holds h = ceil(e0 / page) pages already (columns 0..h-1
+ * of its row) and takes p - h more, p = ceil(e1 / page), from the front of the
+ * free list, requests in order:
+ *   block_table[b][j] = free_pages[(pages taken by requests before b) + j - h]   h <= j < p
+ *   cu_tokens[b], cu_entries[b] = tokens / new entries of the requests before b
+ *   entry_slots[cu_entries[b] + i] = slot of entry e0 + i            0 <= i < e1 - e0
+ *   tok_pos[cu_tokens[b] + i]      = old + i                         0 <= i < new
+ *   win_slots[cu_tokens[b] + i]    = ring slot of position old + i; -1 where a
+ *                                    newer token of the step takes the same ring row
+ *   counts = { tokens, entries, pages taken, pages that could not be given }
+ * Other columns of the table are untouched.  A page past max_pages columns is
+ * not taken; a page that the free list lacks is noted as -1; both are counted
+ * in counts[3], and their entries' slots are -1.  Outputs past the totals
+ * (entry_slots up to max_entries, tok_pos and win_slots up to max_tokens) are
+ * -1; totals past max_entries / max_tokens are cut.  A request with a negative
+ * length, or old + new > 2^31 - 1, counts as an empty slot.  The call can be
+ * repeated: it reads only the columns below h, which it does not write.
+ *   old_len, new_len [batch] int32      free_pages [n_free] int32
+ *   block_table [batch][max_pages] int32 (in / out)
+ *   cu_tokens, cu_entries [batch + 1] int64   entry_slots [max_entries] int64
+ *   tok_pos [max_tokens] int32   win_slots [max_tokens] int64   counts [4] int64
+ * Requirements: batch >= 1, m >= 1, page >= 1, ring_rows >= 1, n_free >= 0,
+ * max_pages >= 1, max_entries >= 0, max_tokens >= 0; pointers aligned to their
+ * elements, and NULL only for an array of no elements (CSA_ERR_INVALID);
+ * batch <= 2^20, max_entries and max_tokens < 2^31 (CSA_ERR_UNSUPPORTED).
+ * Workspace: csa_plan_workspace_bytes(batch), 8-byte aligned
+ * (CSA_ERR_WORKSPACE; 0 bytes for batches up to 4096).
+ */
+size_t csa_plan_workspace_bytes(int batch);
+int csa_plan_pages(const int *old_len, const int *new_len, int batch, int m, int page, int ring_rows,
+                   const int *free_pages, long long n_free, int *block_table, int max_pages,
+                   long long *cu_tokens, long long *cu_entries, long long *entry_slots, long long max_entries,
+                   int *tok_pos, long long *win_slots, long long max_tokens, long long *counts, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * csa_paged_write -- stores packed rows through a slot map: for every i in
+ * [0, n) with 0 <= slots[i] < n_slots, row slots[i] of the pool becomes rows[i];
+ * other rows of the pool are untouched.  Serves the pool of entries
+ * (entry_slots, n_slots = n_pages * page) and the window rings (win_slots,
+ * n_slots = batch * ring_rows) alike.  The valid slots are distinct (as
+ * csa_plan_pages makes them): which row a slot named twice holds afterwards is
+ * not defined, and may be a mixture.
+ *   rows [n][d] bf16   slots [n] int64   pool [n_slots][d] bf16
+ * csa_paged_write_fp8kv -- the same into FP8 rows: codes [n_slots][d] and
+ * exps [n_slots][d/128] receive csa_quantize_fp8_kv's codes and exponents.
+ * Requirements: n >= 0, n_slots >= 1, d % 8 == 0, d >= 8 (FP8: d % 128 == 0);
+ * rows, pool and codes 16-byte, slots 8-byte aligned (CSA_ERR_INVALID).  rows
+ * and the pool do not overlap.
+ */
+int csa_paged_write(const uint16_t *rows, const long long *slots, long long n, int d, uint16_t *pool,
+                    long long n_slots, void *stream);
+int csa_paged_write_fp8kv(const uint16_t *rows, const long long *slots, long long n, int d, uint8_t *codes,
+                          uint8_t *exps, long long n_slots, void *stream);
+
+/*
+ * hca_attend_paged -- hca_attend over a paged cache, for a batch whose requests
+ * may share a long prefix.  The key set of the query at position t of request b:
+ *   J = { entry j of request b : 0 <= j < min(floor((t+1)/m), max_pages * page),
+ *         its page id in [0, n_pages) }
+ *       U { ring row u % ring_rows of request b : max(0, t-W+1) <= u <= t }
+ * with everything else (RMSNorm, gain, sinks, partial RoPE, scale) as
+ * csa_attend.  t < 0 (an empty slot of the batch) has no keys: its output rows
+ * are zero.  Rows of the pool and of the rings outside the key sets are never
+ * used, whatever they hold (unallocated pages may hold NaN).
+ *
+ * n_shared: the first n_shared entries are the same pages in every row of the
+ * table (a multiple of page; 0 = none).  They are read through row 0 of the
+ * table, once for all requests: the query rows of the whole batch are stacked
+ * into one product with the shared entries, and the result is merged with each
+ * request's own entries and window.  A query at t with floor((t+1)/m) <
+ * n_shared sees only the entries below that bound, as without sharing; shared
+ * entries it does not see must then hold finite numbers.
+ *   q [batch][nq][H][D] bf16      pool [n_pages][page][D] bf16
+ *   block_table [batch][max_pages] int32 (ids outside [0, n_pages): no entry)
+ *   ring [batch][ring_rows][D] bf16     q_pos [batch][nq] int32
+ *   out [batch][nq][H][D] bf16
+ * Requirements: those of hca_attend on the shared arguments; page % 16 == 0,
+ * n_pages >= 1, max_pages >= 1, 0 <= n_shared <= max_pages * page with n_shared
+ * % page == 0, ring_rows >= W + nq - 1 (the rings hold the windows of nq
+ * consecutive queries) (CSA_ERR_INVALID); n_pages * page and max_pages * page
+ * < 2^31 (CSA_ERR_UNSUPPORTED).  Workspace: csa_attend_paged_workspace_bytes,
+ * 16-byte aligned, with the same arguments (fp8 = 0).  Calls that may overlap
+ * on the device, replays of captured graphs among them, need workspaces of
+ * their own.
+ *
+ * hca_attend_paged_fp8kv -- the same over FP8 rows: pool8 [n_pages][page][D] and
+ * ring8 [batch][ring_rows][D] e4m3 codes with exponents [..][..][D/128]
+ * (csa_paged_write_fp8kv); the result is that of the bf16 call on the
+ * dequantised rows.  D in {128, 256, 512} (CSA_ERR_UNSUPPORTED otherwise).
+ * Workspace: with fp8 = 1.
+ */
+size_t csa_attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared,
+                                        int W, int fp8);
+int hca_attend_paged(const uint16_t *q, const float *q_gain, const float *sinks, const float *rope_cos,
+                     const float *rope_sin, long long rope_positions, const uint16_t *pool, long long n_pages,
+                     int page, const int *block_table, int max_pages, long long n_shared, int m,
+                     const uint16_t *ring, int ring_rows, int W, const int *q_pos, int batch, int nq, int H, int D,
+                     float scale, float eps, uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
+int hca_attend_paged_fp8kv(const uint16_t *q, const float *q_gain, const float *sinks, const float *rope_cos,
+                           const float *rope_sin, long long rope_positions, const uint8_t *pool8,
+                           const uint8_t *pool8_exp, long long n_pages, int page, const int *block_table,
+                           int max_pages, long long n_shared, int m, const uint8_t *ring8, const uint8_t *ring8_exp,
+                           int ring_rows, int W, const int *q_pos, int batch, int nq, int H, int D, float scale,
+                           float eps, uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * csa_sync_status -- synchronise `stream`, then read and clear the device
  * status word.  Returns CSA_ERR_TIMEOUT if a kernel gave up a bounded wait
  * since the last call, CSA_ERR_CUDA on a CUDA error, else CSA_OK.

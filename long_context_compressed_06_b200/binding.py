@@ -62,6 +62,15 @@ def load() -> ctypes.CDLL:
                              i32, i32, f32, f32, P, P, sz, P], i32),
         "csa_attend_noalloc": ([P, P, P, P, P, i64, P, i64, P, i32, P, i64, i64, i32, P, i32, i32, i32, i32, f32, f32, P, P],
                                i32),
+        "csa_plan_workspace_bytes": ([i32], sz),
+        "csa_plan_pages": ([P, P, i32, i32, i32, i32, P, i64, P, i32, P, P, P, i64, P, P, i64, P, P, sz, P], i32),
+        "csa_paged_write": ([P, P, i64, i32, P, i64, P], i32),
+        "csa_paged_write_fp8kv": ([P, P, i64, i32, P, P, i64, P], i32),
+        "csa_attend_paged_workspace_bytes": ([i32, i32, i32, i32, i32, i32, i64, i32, i32], sz),
+        "hca_attend_paged": ([P, P, P, P, P, i64, P, i64, i32, P, i32, i64, i32, P, i32, i32, P, i32, i32, i32, i32, f32,
+                              f32, P, P, sz, P], i32),
+        "hca_attend_paged_fp8kv": ([P, P, P, P, P, i64, P, P, i64, i32, P, i32, i64, i32, P, P, i32, i32, P, i32, i32,
+                                    i32, i32, f32, f32, P, P, sz, P], i32),
         "csa_sync_status": ([P], i32),
         "csa_set_wait_budget_ns": ([ctypes.c_ulonglong], None),
         "csa_selftest_wait_timeout": ([P], i32),
@@ -429,6 +438,132 @@ def csa_attend_noalloc(q, kv, idx, win, q_pos, W: int, scale: float, eps: float 
                                 rows, W,
                                 _p(q_pos), batch, nq, H, D, float(scale), float(eps), _p(out), _stream()),
            "csa_attend_noalloc")
+    return out
+
+
+def csa_plan_pages(old_len, new_len, free_pages, block_table, m: int, page: int, ring_rows: int, max_tokens: int,
+                   max_entries: int, out=None, workspace=None):
+    """Block tables and slot maps of one step from the requests' lengths: old_len, new_len [b] int32 tokens cached
+    and appended, free_pages [n] int32, block_table [b][max_pages] int32 (its new columns are written) ->
+    (cu_tokens [b+1], cu_entries [b+1], entry_slots [max_entries], tok_pos [max_tokens] int32,
+    win_slots [max_tokens], counts [4]), int64 unless noted, places past the totals -1.  out: those six tensors of
+    an earlier call, written again."""
+    L = load()
+    _need(old_len, torch.int32, "old_len", 1)
+    _need(new_len, torch.int32, "new_len", 1)
+    _need(free_pages, torch.int32, "free_pages", 1)
+    _need(block_table, torch.int32, "block_table", 2)
+    batch, max_pages = block_table.shape
+    if old_len.shape[0] != batch or new_len.shape[0] != batch:
+        raise ValueError("old_len, new_len and block_table must have one row per request")
+    shapes = ((batch + 1,), (batch + 1,), (max_entries,), (max_tokens,), (max_tokens,), (4,))
+    dtypes = (torch.int64, torch.int64, torch.int64, torch.int32, torch.int64, torch.int64)
+    if out is None:
+        if max_tokens < 0 or max_entries < 0:
+            raise ValueError("max_tokens and max_entries must not be negative")
+        out = tuple(torch.empty(s, dtype=t, device=old_len.device) for s, t in zip(shapes, dtypes))
+    else:
+        for x, s, t in zip(out, shapes, dtypes):
+            if _need(x, t, "out").shape != s:
+                raise ValueError("out must hold tensors of shapes %s" % (shapes,))
+    cu_t, cu_e, slots, pos, win, counts = out
+    ws, wsb = _workspace(int(L.csa_plan_workspace_bytes(batch)), old_len.device, workspace)
+    _check(L.csa_plan_pages(_p(old_len), _p(new_len), batch, m, page, ring_rows, _p(free_pages), free_pages.shape[0],
+                            _p(block_table), max_pages, _p(cu_t), _p(cu_e), _p(slots), max_entries, _p(pos), _p(win),
+                            max_tokens, _p(counts), _p(ws), wsb, _stream()), "csa_plan_pages")
+    return out
+
+
+def _write_rows(rows, slots, d):
+    _need(rows, torch.bfloat16, "rows", 2)
+    _need(slots, torch.int64, "slots", 1)
+    if rows.shape[1] != d or slots.shape[0] != rows.shape[0]:
+        raise ValueError("rows must be [n][%d] with one slot per row" % d)
+
+
+def csa_paged_write(rows, slots, pool):
+    """pool [..., d] bf16 (its leading dimensions are the slots): row slots[i] becomes rows[i] ([n][d] bf16) for
+    every slot (int64) inside the pool.  The slots inside are distinct."""
+    L = load()
+    _need(pool, torch.bfloat16, "pool")
+    d = pool.shape[-1]
+    _write_rows(rows, slots, d)
+    _check(L.csa_paged_write(_p(rows), _p(slots), rows.shape[0], d, _p(pool), pool.numel() // max(d, 1), _stream()),
+           "csa_paged_write")
+    return pool
+
+
+def csa_paged_write_fp8kv(rows, slots, codes, exps):
+    """csa_paged_write into FP8 rows: codes [..., d] u8 and exps [..., d/128] u8 (csa_quantize_fp8_kv's format)."""
+    L = load()
+    _need(codes, torch.uint8, "codes")
+    _need(exps, torch.uint8, "exps")
+    d = codes.shape[-1]
+    if exps.shape != codes.shape[:-1] + (d // 128,):
+        raise ValueError("exps must be [..., d/128]")
+    _write_rows(rows, slots, d)
+    _check(L.csa_paged_write_fp8kv(_p(rows), _p(slots), rows.shape[0], d, _p(codes), _p(exps),
+                                   codes.numel() // max(d, 1), _stream()), "csa_paged_write_fp8kv")
+    return codes, exps
+
+
+def attend_paged_workspace_bytes(batch: int, nq: int, H: int, D: int, page: int, max_pages: int, n_shared: int, W: int,
+                                 fp8: bool = False) -> int:
+    return int(load().csa_attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, W, int(fp8)))
+
+
+def _paged(q, block_table, q_pos, pool, ring, q_gain, out):
+    """The shape checks that both paged attention calls make -> (batch, nq, H, D, out)."""
+    _need(q, torch.bfloat16, "q", 4)
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(q_pos, torch.int32, "q_pos", 2)
+    batch, nq, H, D = q.shape
+    if pool.shape[2] != D or ring.shape[2] != D:
+        raise ValueError("pool and ring rows must hold D = %d channels" % D)
+    if block_table.shape[0] != batch or ring.shape[0] != batch or q_pos.shape != (batch, nq):
+        raise ValueError("block_table, ring and q_pos must have one row per sequence of q")
+    if q_gain is not None and _need(q_gain, torch.float32, "q_gain", 1).shape[0] != D:
+        raise ValueError("q_gain must hold D = %d values" % D)
+    if out is None:
+        out = torch.empty_like(q)
+    elif _need(out, torch.bfloat16, "out", 4).shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    return batch, nq, H, D, out
+
+
+def hca_attend_paged(q, pool, block_table, m: int, ring, q_pos, W: int, scale: float, eps: float = 1e-6, q_gain=None,
+                     out=None, workspace=None, n_shared: int = 0, sinks=None, rope=None):
+    """hca_attend over a paged cache: pool [n_pages][page][D], block_table [b][max_pages] int32, ring
+    [b][ring_rows][D] (position u at row u % ring_rows), q [b][nq][H][D], q_pos [b][nq] int32 (-1: an empty slot,
+    zero rows) -> out [b][nq][H][D] bf16.  n_shared: leading entries whose pages every row of the table shares
+    (a multiple of page); the batch's attention over them is computed as one product."""
+    L = load()
+    _need(pool, torch.bfloat16, "pool", 3)
+    _need(ring, torch.bfloat16, "ring", 3)
+    batch, nq, H, D, out = _paged(q, block_table, q_pos, pool, ring, q_gain, out)
+    n_pages, page, max_pages = pool.shape[0], pool.shape[1], block_table.shape[1]
+    ws, wsb = _workspace(attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, W), q.device, workspace)
+    _check(L.hca_attend_paged(_p(q), _p(q_gain), _sinks(sinks, H), *_rope(rope, D), _p(pool), n_pages, page,
+                              _p(block_table), max_pages, n_shared, m, _p(ring), ring.shape[1], W, _p(q_pos), batch,
+                              nq, H, D, float(scale), float(eps), _p(out), _p(ws), wsb, _stream()), "hca_attend_paged")
+    return out
+
+
+def hca_attend_paged_fp8kv(q, pool8, pool8_exp, block_table, m: int, ring8, ring8_exp, q_pos, W: int, scale: float,
+                           eps: float = 1e-6, q_gain=None, out=None, workspace=None, n_shared: int = 0, sinks=None,
+                           rope=None):
+    """hca_attend_paged over FP8 rows: pool8 / ring8 e4m3 codes, exponents [..][..][D/128] (csa_paged_write_fp8kv)."""
+    L = load()
+    _fp8_rows(pool8, pool8_exp, "pool8")
+    _fp8_rows(ring8, ring8_exp, "ring8")
+    batch, nq, H, D, out = _paged(q, block_table, q_pos, pool8, ring8, q_gain, out)
+    n_pages, page, max_pages = pool8.shape[0], pool8.shape[1], block_table.shape[1]
+    ws, wsb = _workspace(attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, W, True), q.device,
+                         workspace)
+    _check(L.hca_attend_paged_fp8kv(_p(q), _p(q_gain), _sinks(sinks, H), *_rope(rope, D), _p(pool8), _p(pool8_exp),
+                                    n_pages, page, _p(block_table), max_pages, n_shared, m, _p(ring8), _p(ring8_exp),
+                                    ring8.shape[1], W, _p(q_pos), batch, nq, H, D, float(scale), float(eps), _p(out),
+                                    _p(ws), wsb, _stream()), "hca_attend_paged_fp8kv")
     return out
 
 

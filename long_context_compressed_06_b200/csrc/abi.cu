@@ -37,6 +37,7 @@ bool ctx_for_launch(csa::DevCtx *ctx) {
 }
 
 inline bool al16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool al8(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 inline bool al4(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline cudaStream_t S(void *s) { return static_cast<cudaStream_t>(s); }
 
@@ -357,6 +358,106 @@ int hca_attend_fp8kv(const uint16_t *q, const float *q_gain, const float *sinks,
     return csa::launch_attend(q, q_gain, sinks, rope_cos, rope_sin, rope_positions, &f8, nullptr, N, m, nullptr, 0,
                               true, nullptr, win_pos0, win_rows, W, q_pos, batch, nq, H, D, scale, eps, out,
                               workspace, workspace_bytes, ctx, S(stream));
+}
+
+size_t csa_plan_workspace_bytes(int batch) { return batch < 1 ? 0 : csa::plan_workspace_bytes(batch); }
+
+int csa_plan_pages(const int *old_len, const int *new_len, int batch, int m, int page, int ring_rows,
+                   const int *free_pages, long long n_free, int *block_table, int max_pages, long long *cu_tokens,
+                   long long *cu_entries, long long *entry_slots, long long max_entries, int *tok_pos,
+                   long long *win_slots, long long max_tokens, long long *counts, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+    if (batch < 1 || m < 1 || page < 1 || ring_rows < 1 || n_free < 0 || max_pages < 1 || max_entries < 0 ||
+        max_tokens < 0)
+        return CSA_ERR_INVALID;
+    if (!al4(old_len) || !al4(new_len) || !al4(block_table) || !al8(cu_tokens) || !al8(cu_entries) || !al8(counts))
+        return CSA_ERR_INVALID;
+    if ((n_free > 0 && !al4(free_pages)) || (max_entries > 0 && !al8(entry_slots)) ||
+        (max_tokens > 0 && (!al4(tok_pos) || !al8(win_slots))))
+        return CSA_ERR_INVALID;
+    if (batch > (1 << 20) || max_entries > 0x7fffffffLL || max_tokens > 0x7fffffffLL) return CSA_ERR_UNSUPPORTED;
+    const size_t need = csa::plan_workspace_bytes(batch);
+    if (need > 0 && (!al8(workspace) || workspace_bytes < need)) return CSA_ERR_WORKSPACE;
+    csa::PlanArgs a = {};
+    a.old_len = old_len; a.new_len = new_len; a.batch = batch; a.m = m; a.page = page; a.ring = ring_rows;
+    a.free_pages = free_pages; a.n_free = n_free; a.table = block_table; a.max_pages = max_pages;
+    a.cu_tokens = cu_tokens; a.cu_entries = cu_entries; a.entry_slots = entry_slots; a.max_entries = max_entries;
+    a.tok_pos = tok_pos; a.win_slots = win_slots; a.max_tokens = max_tokens; a.counts = counts;
+    return csa::launch_plan_pages(a, workspace, S(stream));
+}
+
+int csa_paged_write(const uint16_t *rows, const long long *slots, long long n, int d, uint16_t *pool,
+                    long long n_slots, void *stream) {
+    if (n < 0 || n_slots < 1 || d < 8 || d % 8 != 0) return CSA_ERR_INVALID;
+    if (!al16(pool) || (n > 0 && (!al16(rows) || !al8(slots)))) return CSA_ERR_INVALID;
+    return csa::launch_paged_write(rows, slots, n, d, pool, nullptr, nullptr, n_slots, S(stream));
+}
+
+int csa_paged_write_fp8kv(const uint16_t *rows, const long long *slots, long long n, int d, uint8_t *codes,
+                          uint8_t *exps, long long n_slots, void *stream) {
+    if (n < 0 || n_slots < 1 || d < 128 || d % 128 != 0) return CSA_ERR_INVALID;
+    if (!al16(codes) || !exps || (n > 0 && (!al16(rows) || !al8(slots)))) return CSA_ERR_INVALID;
+    return csa::launch_paged_write(rows, slots, n, d, nullptr, codes, exps, n_slots, S(stream));
+}
+
+// The arguments of a paged attention call but its rows and its workspace.
+static int validate_paged(const csa::PagedArgs &a) {
+    if (!al16(a.q) || !al4(a.table) || !al4(a.q_pos) || !al16(a.out)) return CSA_ERR_INVALID;
+    if ((a.q_gain && !al4(a.q_gain)) || (a.sinks && !al4(a.sinks))) return CSA_ERR_INVALID;
+    if ((a.rope_cos == nullptr) != (a.rope_sin == nullptr)) return CSA_ERR_INVALID;
+    if (a.rope_cos && (!al4(a.rope_cos) || !al4(a.rope_sin) || a.rope_npos < 1)) return CSA_ERR_INVALID;
+    if (a.batch < 1 || a.nq < 1 || a.H < 1 || a.D < 1 || a.m < 1 || a.W < 1 || !(a.eps >= 0.f)) return CSA_ERR_INVALID;
+    if (a.page < 16 || a.page % 16 != 0 || a.n_pages < 1 || a.max_pages < 1) return CSA_ERR_INVALID;
+    const long long cap = (long long)a.max_pages * a.page;
+    if (a.n_shared < 0 || a.n_shared > cap || a.n_shared % a.page != 0) return CSA_ERR_INVALID;
+    if ((long long)a.ring_rows < (long long)a.W + a.nq - 1) return CSA_ERR_INVALID;
+    if (a.n_pages > 0x7fffffffLL / a.page || cap > 0x7fffffffLL) return CSA_ERR_UNSUPPORTED;
+    if (a.H > 128 || !(a.D == 64 || a.D == 128 || a.D == 256 || a.D == 512)) return CSA_ERR_UNSUPPORTED;
+    return CSA_OK;
+}
+
+static int run_paged(const csa::PagedArgs &a, void *workspace, size_t workspace_bytes, void *stream) {
+    const size_t need = csa::attend_paged_workspace_bytes(a.batch, a.nq, a.H, a.D, a.page, a.max_pages, a.n_shared, a.W,
+                                                          a.fp8.kv != nullptr);
+    if (need > 0 && (!al16(workspace) || workspace_bytes < need)) return CSA_ERR_WORKSPACE;
+    csa::DevCtx ctx;
+    if (!ctx_for_launch(&ctx)) return CSA_ERR_CUDA;
+    return csa::launch_attend_paged(a, workspace, workspace_bytes, ctx, S(stream));
+}
+
+size_t csa_attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared,
+                                        int W, int fp8) {
+    if (batch < 1 || nq < 1 || H < 1 || H > 128 || page < 1 || max_pages < 1 || n_shared < 0 || W < 1 ||
+        !(D == 64 || D == 128 || D == 256 || D == 512))
+        return 0;
+    return csa::attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, W, fp8 != 0);
+}
+
+int hca_attend_paged(const uint16_t *q, const float *q_gain, const float *sinks, const float *rope_cos,
+                     const float *rope_sin, long long rope_positions, const uint16_t *pool, long long n_pages,
+                     int page, const int *block_table, int max_pages, long long n_shared, int m, const uint16_t *ring,
+                     int ring_rows, int W, const int *q_pos, int batch, int nq, int H, int D, float scale, float eps,
+                     uint16_t *out, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!al16(pool) || !al16(ring)) return CSA_ERR_INVALID;
+    const csa::PagedArgs a = {q, q_gain, sinks, rope_cos, rope_sin, rope_positions, pool, {}, n_pages, page,
+                              block_table, max_pages, n_shared, m, ring, ring_rows, W, q_pos, batch, nq, H, D, scale,
+                              eps, out};
+    const int rc = validate_paged(a);
+    return rc != CSA_OK ? rc : run_paged(a, workspace, workspace_bytes, stream);
+}
+
+int hca_attend_paged_fp8kv(const uint16_t *q, const float *q_gain, const float *sinks, const float *rope_cos,
+                           const float *rope_sin, long long rope_positions, const uint8_t *pool8,
+                           const uint8_t *pool8_exp, long long n_pages, int page, const int *block_table,
+                           int max_pages, long long n_shared, int m, const uint8_t *ring8, const uint8_t *ring8_exp,
+                           int ring_rows, int W, const int *q_pos, int batch, int nq, int H, int D, float scale,
+                           float eps, uint16_t *out, void *workspace, size_t workspace_bytes, void *stream) {
+    const csa::PagedArgs a = {q, q_gain, sinks, rope_cos, rope_sin, rope_positions, nullptr,
+                              {pool8, pool8_exp, ring8, ring8_exp}, n_pages, page, block_table, max_pages, n_shared, m,
+                              nullptr, ring_rows, W, q_pos, batch, nq, H, D, scale, eps, out};
+    int rc = validate_paged(a);
+    if (rc == CSA_OK) rc = validate_fp8kv(pool8, pool8_exp, ring8, ring8_exp, D);
+    return rc != CSA_OK ? rc : run_paged(a, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -32,6 +32,14 @@ struct AttendArgs {
     const uint16_t *win;    // [batch][win_rows][D] stream-A rows of positions win_pos0..
     long long win_pos0, win_rows;
     int W;
+    // Paged cache (table set; kv / kv8 then hold [n_pages][page] rows): entry j of
+    // sequence b is row table[b][j / page] * page + j % page, the window is a ring
+    // of win_rows rows per sequence (position u at row u % win_rows), and the key
+    // set starts at entry e_first (the entries before it are another kernel's)
+    const int *table;       // [batch][max_pages] or null
+    int max_pages, page;
+    long long n_pages;
+    long long e_first;
     const int *q_pos;       // [n_bq]
     int nq;
     long long n_bq;         // batch * nq

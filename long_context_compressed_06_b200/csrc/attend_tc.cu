@@ -167,8 +167,18 @@ struct Keys {
     long long nsel, nsel4, nwin, u0, total;
 };
 
+template <bool PAGED>
 CSA_DEVINL Keys query_keys(const AttendArgs &a, long long t) {
     Keys k;
+    if constexpr (PAGED) {  // the visible entries from e_first on, then the ring rows t-W+1..t
+        const long long v = n_visible(t, a.m, a.N) - a.e_first;
+        k.nsel = v > 0 ? v : 0;
+        k.nsel4 = (k.nsel + 3) & ~3LL;
+        k.u0 = t - a.W + 1 > 0 ? t - a.W + 1 : 0;
+        k.nwin = t >= k.u0 ? t - k.u0 + 1 : 0;
+        k.total = k.nsel4 + k.nwin;
+        return k;
+    }
     k.nsel = a.dense ? n_visible(t, a.m, a.N) : a.k;
     k.nsel4 = (k.nsel + 3) & ~3LL;
     long long u0 = t - a.W + 1;
@@ -183,19 +193,37 @@ CSA_DEVINL Keys query_keys(const AttendArgs &a, long long t) {
 
 // The selection index of key e as stored (loaded only: the value is consumed
 // by key_row_index, so that the load can be issued a tile ahead).
+// Paged cache: the page that holds the entry (sequence b = bq / nq).
+template <bool PAGED>
 CSA_DEVINL int key_index_raw(const AttendArgs &a, const Keys &ks, long long bq, long long e, long long e_end) {
     if (e >= e_end) e = e_end - 1;
+    if constexpr (PAGED)
+        return e >= 0 && e < ks.nsel
+                   ? __ldg(a.table + bq / a.nq * a.max_pages + (uint32_t)(a.e_first + e) / (uint32_t)a.page)
+                   : -1;
     return (!a.dense && e >= 0 && e < ks.nsel) ? __ldg(a.idx + bq * a.k + e) : 0;
 }
 
 // Row of key e -- its index in kv (win == false) or in the window buffer --
 // and whether it takes part (keys past e_end, selection padding and
 // out-of-range indices read a valid row; their scores are masked).  jraw is
-// key_index_raw(e).
+// key_index_raw(e).  Paged cache: the row of a key that does not take part is
+// not read (its tile row is zero-filled), since nothing is known of what the
+// pages hold outside the entries.
+template <bool PAGED>
 CSA_DEVINL size_t key_row_index(const AttendArgs &a, const Keys &ks, long long b, long long e, long long e_end,
                                 int jraw, bool &valid, bool &win) {
     win = false;
     valid = e < e_end;
+    if constexpr (PAGED) {
+        if (e < ks.nsel4) {
+            const uint32_t j = (uint32_t)(a.e_first + e);
+            valid = valid && e < ks.nsel && jraw >= 0 && jraw < a.n_pages;
+            return valid ? (size_t)jraw * a.page + j % (uint32_t)a.page : 0;
+        }
+        win = true;
+        return valid ? (size_t)b * a.win_rows + (ks.u0 + (e - ks.nsel4)) % a.win_rows : 0;
+    }
     if (!valid) e = e_end - 1;  // e_end >= 1 whenever a tile exists
     if (e < ks.nsel4) {
         long long j = 0;
@@ -218,18 +246,25 @@ CSA_DEVINL size_t key_row_index(const AttendArgs &a, const Keys &ks, long long b
     return (size_t)b * a.win_rows + (ks.u0 - a.win_pos0) + w;
 }
 
+template <bool PAGED>
 CSA_DEVINL const uint16_t *key_slot(const AttendArgs &a, const Keys &ks, long long b, long long e, long long e_end,
                                     int jraw, bool &valid) {
     bool win;
-    const size_t r = key_row_index(a, ks, b, e, e_end, jraw, valid, win);
+    const size_t r = key_row_index<PAGED>(a, ks, b, e, e_end, jraw, valid, win);
+    if (PAGED && !valid) return nullptr;
     return (win ? a.win : a.kv) + r * a.D;
 }
 
 // FP8 rows: the codes of key e (the row's exponent bytes follow from the same index)
+template <bool PAGED>
 CSA_DEVINL const uint8_t *key_slot8(const AttendArgs &a, const Keys &ks, long long b, long long e, long long e_end,
                                     int jraw, bool &valid, const uint8_t *&exps) {
     bool win;
-    const size_t r = key_row_index(a, ks, b, e, e_end, jraw, valid, win);
+    const size_t r = key_row_index<PAGED>(a, ks, b, e, e_end, jraw, valid, win);
+    if (PAGED && !valid) {
+        exps = nullptr;
+        return nullptr;
+    }
     exps = (win ? a.win8e : a.kv8e) + r * (a.D / 128);
     return (win ? a.win8 : a.kv8) + r * a.D;
 }
@@ -333,6 +368,7 @@ struct Item {
     int split, head0, ntiles;
 };
 
+template <bool PAGED>
 CSA_DEVINL Item work_item(const AttTcParams &p, long long wi) {
     const AttendArgs &a = p.a;
     Item it;
@@ -342,7 +378,7 @@ CSA_DEVINL Item work_item(const AttTcParams &p, long long wi) {
     it.bq = rest / a.splits;
     it.b = it.bq / a.nq;
     it.head0 = hh * kHeads;
-    it.ks = query_keys(a, __ldg(a.q_pos + it.bq));
+    it.ks = query_keys<PAGED>(a, __ldg(a.q_pos + it.bq));
     const long long T = (it.ks.total + kTileKeys - 1) / kTileKeys;
     const long long t0 = T * it.split / a.splits, t1 = T * (it.split + 1) / a.splits;
     it.e0 = t0 * kTileKeys;
@@ -351,7 +387,13 @@ CSA_DEVINL Item work_item(const AttTcParams &p, long long wi) {
     return it;
 }
 
-template <int D, bool FP8>
+// 16-byte asynchronous copy; src == nullptr writes zeros (nothing is read)
+CSA_DEVINL void cp_async16_or_zero(uint32_t dst, const void *src, const void *any) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src ? src : any), "r"(src ? 16 : 0)
+                 : "memory");
+}
+
+template <int D, bool FP8, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap,
                      const AttTcParams p) {
@@ -495,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         for (long long wi = blockIdx.x; wi < p.n_work && ok; wi += gridDim.x) {
-            const Item it = work_item(p, wi);
+            const Item it = work_item<PAGED>(p, wi);
             // As a programmatic dependent (csa_decode_step) the selection is
             // complete only once the top-k grid is: wait before the first item
             // that reads selected slots (the query prologue and the window-only
@@ -510,8 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // iteration uses them.
             int nraw0 = 0, nraw1 = 0;
             if (it.ntiles > 0) {
-                nraw0 = key_index_raw(a, it.ks, it.bq, it.e0 + lane, it.e1);
-                nraw1 = key_index_raw(a, it.ks, it.bq, it.e0 + 32 + lane, it.e1);
+                nraw0 = key_index_raw<PAGED>(a, it.ks, it.bq, it.e0 + lane, it.e1);
+                nraw1 = key_index_raw<PAGED>(a, it.ks, it.bq, it.e0 + 32 + lane, it.e1);
             }
             for (int j = 0; j < it.ntiles; ++j) {
                 const long long g = jt + j;
@@ -519,18 +561,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const long long ebase = it.e0 + (long long)j * kTileKeys;
                 const int raw0 = nraw0, raw1 = nraw1;
                 if (j + 1 < it.ntiles) {
-                    nraw0 = key_index_raw(a, it.ks, it.bq, ebase + kTileKeys + lane, it.e1);
-                    nraw1 = key_index_raw(a, it.ks, it.bq, ebase + kTileKeys + 32 + lane, it.e1);
+                    nraw0 = key_index_raw<PAGED>(a, it.ks, it.bq, ebase + kTileKeys + lane, it.e1);
+                    nraw1 = key_index_raw<PAGED>(a, it.ks, it.bq, ebase + kTileKeys + 32 + lane, it.e1);
                 }
                 bool v0, v1;
                 const uint16_t *r0 = nullptr, *r1 = nullptr;
                 const uint8_t *c0 = nullptr, *c1 = nullptr, *x0 = nullptr, *x1 = nullptr;
                 if constexpr (FP8) {
-                    c0 = key_slot8(a, it.ks, it.b, ebase + lane, it.e1, raw0, v0, x0);
-                    c1 = key_slot8(a, it.ks, it.b, ebase + 32 + lane, it.e1, raw1, v1, x1);
+                    c0 = key_slot8<PAGED>(a, it.ks, it.b, ebase + lane, it.e1, raw0, v0, x0);
+                    c1 = key_slot8<PAGED>(a, it.ks, it.b, ebase + 32 + lane, it.e1, raw1, v1, x1);
                 } else {
-                    r0 = key_slot(a, it.ks, it.b, ebase + lane, it.e1, raw0, v0);
-                    r1 = key_slot(a, it.ks, it.b, ebase + 32 + lane, it.e1, raw1, v1);
+                    r0 = key_slot<PAGED>(a, it.ks, it.b, ebase + lane, it.e1, raw0, v0);
+                    r1 = key_slot<PAGED>(a, it.ks, it.b, ebase + 32 + lane, it.e1, raw1, v1);
                 }
                 const uint32_t mlo = __ballot_sync(0xffffffffu, v0), mhi = __ballot_sync(0xffffffffu, v1);
                 if (!warp_wait(smem_u32(s.kempty + st), (uint32_t)(((g / p.stages) & 1) ^ 1), p.ctx, s.abort_flag)) {
@@ -569,9 +611,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(key < 32 ? x0 : x1), key & 31));
                             if (lane < D / 16) {
                                 const uint32_t dst = stage + (lane >> 2) * (kTileKeys * 128) + key * 128 + (lane & 3) * 16;
-                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(crow + lane * 16)
-                                             : "memory");
-                                e_new[i] = __ldg(xrow + (lane >> 3));  // the block of 128 codes holding 16l..16l+15
+                                if constexpr (PAGED) {
+                                    cp_async16_or_zero(dst, crow ? crow + lane * 16 : nullptr, a.kv8);
+                                    if (crow) e_new[i] = __ldg(xrow + (lane >> 3));
+                                } else {
+                                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                                                 "l"(crow + lane * 16)
+                                                 : "memory");
+                                    e_new[i] = __ldg(xrow + (lane >> 3));  // the block of 128 codes holding 16l..16l+15
+                                }
                             }
                         }
                     }
@@ -592,8 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int u = lane; u < D / 8; u += 32) {  // 16-byte units of the row
                             const uint32_t dst = krow + (u >> 3) * (kTileKeys * 128) + (((u & 7) ^ (key & 7)) << 4);
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row + u * 8)
-                                         : "memory");
+                            if constexpr (PAGED)
+                                cp_async16_or_zero(dst, row ? row + u * 8 : nullptr, a.kv);
+                            else
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row + u * 8)
+                                             : "memory");
                         }
                     }
                     if (pw == 0) {  // the mask travels with the tile (release by lane 0's arrive)
@@ -637,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t n_items = 0;
         bool ok = true;
         for (long long wi = blockIdx.x; wi < p.n_work && ok; wi += gridDim.x, ++n_items) {
-            const Item it = work_item(p, wi);
+            const Item it = work_item<PAGED>(p, wi);
             // raw query rows of this item by TMA, once the previous item's QK MMAs are done with the tile
             if (n_items > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(s.qempty), (n_items - 1) & 1u, p.ctx,
                                                                  s.abort_flag)))
@@ -741,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t n_items = 0;
         bool ok = true;
         for (long long wi = blockIdx.x; wi < p.n_work && ok; wi += gridDim.x, ++n_items) {
-            const Item it = work_item(p, wi);
+            const Item it = work_item<PAGED>(p, wi);
             const int h = it.head0 + hl;
             if (!warp_wait(smem_u32(s.qfull), n_items & 1u, p.ctx, s.abort_flag)) break;
             const long long tq = __ldg(a.q_pos + it.bq);
@@ -927,7 +978,7 @@ constexpr uint32_t idesc_m64(int n, bool b_mn) {
            ((uint32_t)(64 >> 4) << 24);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool PAGED>
 int launch_d(const AttendArgs &a, const DevCtx &ctx, cudaStream_t st, bool pdl) {
     AttTcParams p = {};
     p.a = a;
@@ -941,7 +992,7 @@ int launch_d(const AttendArgs &a, const DevCtx &ctx, cudaStream_t st, bool pdl) 
     p.stages = stages;
     // at least 120 KiB so that one CTA owns an SM (it allocates all 512 TMEM columns)
     const size_t smem = std::max<size_t>(smem_bytes<D>(stages), 120 * 1024);
-    auto kern = attend_tc_kernel<D, FP8>;
+    auto kern = attend_tc_kernel<D, FP8, PAGED>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return CSA_ERR_CUDA;
     CUtensorMap qmap;
@@ -955,7 +1006,7 @@ int launch_d(const AttendArgs &a, const DevCtx &ctx, cudaStream_t st, bool pdl) 
     }
     CUtensorMap kvmap;
     memset(&kvmap, 0, sizeof(kvmap));
-    p.kv_tma = a.dense && !FP8 ? 1 : 0;
+    p.kv_tma = a.dense && !FP8 && !PAGED ? 1 : 0;
     if (p.kv_tma) {
         // kv [batch][N][D] bf16: boxes of 64 dims x 64 entries, 128-byte swizzle
         const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.N, (uint64_t)(a.n_bq / a.nq)};
@@ -1009,22 +1060,27 @@ void attend_tc_plan(long long n_bq, int H, long long max_keys, int *splits, long
     *kps = ((tiles + best - 1) / best) * kTileKeys;
 }
 
-int launch_attend_tc(AttendArgs a, const DevCtx &ctx, cudaStream_t st, bool pdl) {
+template <bool PAGED>
+static int launch_layout(const AttendArgs &a, const DevCtx &ctx, cudaStream_t st, bool pdl) {
     if (a.kv8) {  // FP8 rows: 128-channel scale blocks
         switch (a.D) {
-            case 128: return launch_d<128, true>(a, ctx, st, pdl);
-            case 256: return launch_d<256, true>(a, ctx, st, pdl);
-            case 512: return launch_d<512, true>(a, ctx, st, pdl);
+            case 128: return launch_d<128, true, PAGED>(a, ctx, st, pdl);
+            case 256: return launch_d<256, true, PAGED>(a, ctx, st, pdl);
+            case 512: return launch_d<512, true, PAGED>(a, ctx, st, pdl);
             default: return CSA_ERR_UNSUPPORTED;
         }
     }
     switch (a.D) {
-        case 64: return launch_d<64, false>(a, ctx, st, pdl);
-        case 128: return launch_d<128, false>(a, ctx, st, pdl);
-        case 256: return launch_d<256, false>(a, ctx, st, pdl);
-        case 512: return launch_d<512, false>(a, ctx, st, pdl);
+        case 64: return launch_d<64, false, PAGED>(a, ctx, st, pdl);
+        case 128: return launch_d<128, false, PAGED>(a, ctx, st, pdl);
+        case 256: return launch_d<256, false, PAGED>(a, ctx, st, pdl);
+        case 512: return launch_d<512, false, PAGED>(a, ctx, st, pdl);
         default: return CSA_ERR_UNSUPPORTED;
     }
+}
+
+int launch_attend_tc(AttendArgs a, const DevCtx &ctx, cudaStream_t st, bool pdl) {
+    return a.table ? launch_layout<true>(a, ctx, st, pdl) : launch_layout<false>(a, ctx, st, pdl);
 }
 
 }  // namespace csa

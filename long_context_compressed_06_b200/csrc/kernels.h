@@ -69,6 +69,56 @@ int launch_attend(const uint16_t *q, const float *q_gain, const float *sinks, co
                   int batch, int nq, int H, int D, float scale, float eps, uint16_t *out,
                   void *ws, size_t ws_bytes, const DevCtx &ctx, cudaStream_t st, bool pdl = false);
 
+// Attention over a paged cache (csa_paged / hca_attend_paged): the arguments
+// of one call, bf16 rows (pool, ring) or FP8 rows (fp8: kv / win fields).
+struct PagedArgs {
+    const uint16_t *q;
+    const float *q_gain, *sinks, *rope_cos, *rope_sin;
+    long long rope_npos;
+    const uint16_t *pool;  // [n_pages][page][D]
+    Fp8Kv fp8;             // or its codes and exponents (fp8.kv set)
+    long long n_pages;
+    int page;
+    const int *table;      // [batch][max_pages]
+    int max_pages;
+    long long n_shared;    // leading entries that every row of the table shares
+    int m;
+    const uint16_t *ring;  // [batch][ring_rows][D]
+    int ring_rows, W;
+    const int *q_pos;
+    int batch, nq, H, D;
+    float scale, eps;
+    uint16_t *out;
+};
+
+size_t attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared, int W,
+                                    bool fp8);
+int launch_attend_paged(const PagedArgs &a, void *ws, size_t ws_bytes, const DevCtx &ctx, cudaStream_t st);
+
+// Block tables and slot maps (csa_plan_pages); the pointers' shapes are the ABI's.
+struct PlanArgs {
+    const int *old_len, *new_len;
+    int batch, m, page, ring;
+    const int *free_pages;
+    long long n_free;
+    int *table;
+    int max_pages;
+    long long *cu_tokens, *cu_entries, *cu_pages;  // cu_pages: workspace (large batches)
+    long long *entry_slots;
+    long long max_entries;
+    int *tok_pos;
+    long long *win_slots;
+    long long max_tokens;
+    long long *counts;
+};
+
+size_t plan_workspace_bytes(int batch);
+int launch_plan_pages(PlanArgs a, void *ws, cudaStream_t st);
+
+// rows [n][d] to rows slots[i] of pool (bf16) or of codes / exps (FP8 rows, codes set)
+int launch_paged_write(const uint16_t *rows, const long long *slots, long long n, int d, uint16_t *pool, uint8_t *codes,
+                       uint8_t *exps, long long n_slots, cudaStream_t st);
+
 int launch_selftest_wait(const DevCtx &ctx, cudaStream_t st);
 
 // Host-side argument checks of csa_attend (everything but the workspace).

@@ -1,0 +1,321 @@
+// paged.cu -- the bookkeeping of a paged cache of compressed entries:
+// csa_plan_pages (block tables and slot maps from the requests' lengths) and
+// csa_paged_write / csa_paged_write_fp8kv (rows stored through a slot map).
+//
+// csa_plan_pages.  With e0 = old / m, e1 = (old + new) / m entries before and
+// after the step, request b holds ceil(e0 / page) pages and takes the next
+// ceil(e1 / page) - ceil(e0 / page) ids of the free list, requests in order; three
+// prefix sums over the batch (tokens, entries, pages) place everything else.
+// The kernel is bound by latency (a decode step) or by the 8 bytes per entry
+// and 12 per token that it writes (a prompt).
+//
+// Up to kFusedBatch requests one launch does it all: every block forms the
+// three prefix sums over the whole batch in its shared memory (the lengths are
+// 8 bytes a request, read from L2) and fills its own range of the outputs;
+// above that a one-block launch writes the sums to global memory first and the
+// filling blocks search them there.
+#include "common.cuh"
+#include "kernels.h"
+#include "quant_fp8.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kFusedBatch = 4096;  // three int64 sums per request: 96 KiB of shared memory
+constexpr int kPlanItems = 2048;   // outputs per filling block
+
+struct Req {
+    long long o, n, e0, e1, held, fresh;  // tokens, entries, pages before, pages taken
+};
+
+CSA_DEVINL Req request(const PlanArgs &a, int b) {
+    Req r;
+    r.o = __ldg(a.old_len + b);
+    r.n = __ldg(a.new_len + b);
+    if (r.o < 0 || r.n < 0 || r.o + r.n > 0x7fffffffLL) r.o = r.n = 0;  // an empty slot of the batch
+    r.e0 = (uint32_t)r.o / (uint32_t)a.m;
+    r.e1 = (uint32_t)(r.o + r.n) / (uint32_t)a.m;
+    // ceil, without passing 32 bits
+    const uint32_t pg = (uint32_t)a.page;
+    const long long h = (uint32_t)r.e0 / pg + ((uint32_t)r.e0 % pg ? 1 : 0);
+    const long long p = (uint32_t)r.e1 / pg + ((uint32_t)r.e1 % pg ? 1 : 0);
+    r.held = h < a.max_pages ? h : a.max_pages;
+    r.fresh = (p < a.max_pages ? p : a.max_pages) - r.held;
+    return r;
+}
+
+// pages that the table has no column for
+CSA_DEVINL long long pages_cut(const PlanArgs &a, const Req &r) {
+    const uint32_t pg = (uint32_t)a.page;
+    const long long p = (uint32_t)r.e1 / pg + ((uint32_t)r.e1 % pg ? 1 : 0);
+    const long long h = (uint32_t)r.e0 / pg + ((uint32_t)r.e0 % pg ? 1 : 0);
+    return p - h - r.fresh;
+}
+
+struct Sums {
+    long long t, e, p, cut;
+};
+
+CSA_DEVINL Sums operator+(const Sums &x, const Sums &y) { return {x.t + y.t, x.e + y.e, x.p + y.p, x.cut + y.cut}; }
+
+CSA_DEVINL Sums shfl_up(const Sums &v, int d) {
+    return {__shfl_up_sync(0xffffffffu, v.t, d), __shfl_up_sync(0xffffffffu, v.e, d),
+            __shfl_up_sync(0xffffffffu, v.p, d), __shfl_up_sync(0xffffffffu, v.cut, d)};
+}
+
+// Exclusive prefix sums over the batch into cu_* ([batch + 1] each), by one
+// block; every thread returns the totals.  A thread owns consecutive requests.
+CSA_DEVINL Sums scan_batch(const PlanArgs &a, long long *cu_t, long long *cu_e, long long *cu_p) {
+    __shared__ Sums warp_tot[kPlanThreads / 32];
+    const int per = (a.batch + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = (int)min((long long)threadIdx.x * per, (long long)a.batch), b1 = min(b0 + per, a.batch);
+    Sums mine = {0, 0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+        const Req r = request(a, b);
+        mine = mine + Sums{r.n, r.e1 - r.e0, r.fresh, pages_cut(a, r)};
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sums inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const Sums up = shfl_up(inc, d);
+        if (lane >= d) inc = inc + up;
+    }
+    if (lane == 31) warp_tot[warp] = inc;
+    __syncthreads();
+    Sums base = {0, 0, 0, 0}, total = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w == warp) base = total;
+        total = total + warp_tot[w];
+    }
+    Sums at = {base.t + inc.t - mine.t, base.e + inc.e - mine.e, base.p + inc.p - mine.p, 0};
+    for (int b = b0; b < b1; ++b) {
+        const Req r = request(a, b);
+        cu_t[b] = at.t;
+        cu_e[b] = at.e;
+        cu_p[b] = at.p;
+        at = at + Sums{r.n, r.e1 - r.e0, r.fresh, 0};
+    }
+    if (threadIdx.x == 0) {
+        cu_t[a.batch] = total.t;
+        cu_e[a.batch] = total.e;
+        cu_p[a.batch] = total.p;
+    }
+    return total;
+}
+
+CSA_DEVINL void write_counts(const PlanArgs &a, const Sums &total) {
+    const long long lacking = total.p > a.n_free ? total.p - a.n_free : 0;
+    a.counts[0] = total.t;
+    a.counts[1] = total.e;
+    a.counts[2] = total.p;
+    a.counts[3] = total.cut + lacking;
+}
+
+// the request whose range of the prefix sums holds item i < cu[batch]
+CSA_DEVINL int owner(const long long *cu, int batch, long long i) {
+    int lo = 0, hi = batch;  // cu[lo] <= i < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Fills one range of kPlanItems outputs: blocks [0, entry_blocks) the entry
+// slots (and the table's new columns, by the thread of a page's first new
+// entry), the others the token outputs.
+CSA_DEVINL void fill(const PlanArgs &a, int block, int entry_blocks, const long long *cu_t, const long long *cu_e,
+                     const long long *cu_p) {
+    if (block < entry_blocks) {
+        const long long total = cu_e[a.batch];
+        // every entry of the batch has its page noted, also those past the slot map's room
+        const long long all = total > a.max_entries ? total : a.max_entries;
+        for (long long s = (long long)block * kPlanItems; s < all; s += (long long)entry_blocks * kPlanItems) {
+            for (int k = threadIdx.x; k < kPlanItems; k += kPlanThreads) {
+                const long long i = s + k;
+                if (i >= all) break;
+                long long slot = -1;
+                if (i < total) {
+                    const int b = owner(cu_e, a.batch, i);
+                    const Req r = request(a, b);
+                    const long long c0 = cu_e[b];
+                    const uint32_t e = (uint32_t)(r.e0 + (i - c0)), j = e / (uint32_t)a.page, off = e % (uint32_t)a.page;
+                    if (j < (uint32_t)a.max_pages) {
+                        int *cell = a.table + (size_t)b * a.max_pages + j;
+                        int id;
+                        if (j < r.held) {
+                            id = *cell;
+                        } else {
+                            const long long f = cu_p[b] + (j - r.held);
+                            id = f < a.n_free ? __ldg(a.free_pages + f) : -1;
+                            if (off == 0) *cell = id;
+                        }
+                        if (id >= 0) slot = (long long)id * a.page + off;
+                    }
+                }
+                if (i < a.max_entries) a.entry_slots[i] = slot;
+            }
+        }
+        return;
+    }
+    const long long total = cu_t[a.batch], s = (long long)(block - entry_blocks) * kPlanItems;
+    for (int k = threadIdx.x; k < kPlanItems; k += kPlanThreads) {
+        const long long i = s + k;
+        if (i >= a.max_tokens) return;
+        int pos = -1;
+        long long slot = -1;
+        if (i < total) {
+            const int b = owner(cu_t, a.batch, i);
+            const long long p = (long long)__ldg(a.old_len + b) + (i - cu_t[b]);
+            pos = (int)p;
+            // of tokens that share a ring row only the newest is kept
+            if (p >= (long long)__ldg(a.old_len + b) + __ldg(a.new_len + b) - a.ring)
+                slot = (long long)b * a.ring + (uint32_t)p % (uint32_t)a.ring;
+        }
+        a.tok_pos[i] = pos;
+        a.win_slots[i] = slot;
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_fused_kernel(const PlanArgs a, int entry_blocks) {
+    extern __shared__ long long cu[];
+    long long *cu_t = cu, *cu_e = cu + (a.batch + 1), *cu_p = cu + 2 * (a.batch + 1);
+    const Sums total = scan_batch(a, cu_t, cu_e, cu_p);
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int b = threadIdx.x; b <= a.batch; b += kPlanThreads) {
+            a.cu_tokens[b] = cu_t[b];
+            a.cu_entries[b] = cu_e[b];
+        }
+        if (threadIdx.x == 0) write_counts(a, total);
+    }
+    fill(a, blockIdx.x, entry_blocks, cu_t, cu_e, cu_p);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Sums total = scan_batch(a, a.cu_tokens, a.cu_entries, a.cu_pages);
+    if (threadIdx.x == 0) write_counts(a, total);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_fill_kernel(const PlanArgs a, int entry_blocks) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums of plan_scan_kernel
+    fill(a, blockIdx.x, entry_blocks, a.cu_tokens, a.cu_entries, a.cu_pages);
+}
+
+// ---------------------------------------------------------------- writes
+constexpr int kWriteThreads = 256;
+constexpr int kWriteUnits = 4;  // 16-byte units per thread, all in flight before the first store
+
+// Unit u (8 elements) of the packed rows goes to row slots[u / upr] of the pool.
+__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const uint4 *__restrict__ rows, uint32_t upr,
+                                                                    long long units,
+                                                                    const long long *__restrict__ slots,
+                                                                    long long n_slots, uint4 *__restrict__ pool) {
+    const long long u0 = (long long)blockIdx.x * (kWriteThreads * kWriteUnits) + threadIdx.x;
+    uint4 v[kWriteUnits];
+    long long dst[kWriteUnits];
+#pragma unroll
+    for (int k = 0; k < kWriteUnits; ++k) {
+        const long long u = u0 + k * kWriteThreads;
+        dst[k] = -1;
+        if (u < units) {
+            v[k] = ldg_stream(rows + u);
+            const long long row = u / upr, s = __ldg(slots + row);
+            if (s >= 0 && s < n_slots) dst[k] = s * upr + (u - row * upr);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kWriteUnits; ++k)
+        if (dst[k] >= 0) pool[dst[k]] = v[k];
+}
+
+// The same with the rows quantised on the way (csa_quantize_fp8_kv's codes and
+// exponents): the 16 units of a 128-channel block are 16 consecutive lanes.
+__global__ void __launch_bounds__(kWriteThreads)
+    paged_write_fp8_kernel(const uint4 *__restrict__ rows, uint32_t upr, long long units,
+                           const long long *__restrict__ slots, long long n_slots, uint2 *__restrict__ codes,
+                           uint8_t *__restrict__ exps) {
+    const long long u0 = (long long)blockIdx.x * (kWriteThreads * kWriteUnits) + threadIdx.x;
+    uint4 v[kWriteUnits];
+    long long dst[kWriteUnits];
+#pragma unroll
+    for (int k = 0; k < kWriteUnits; ++k) {
+        const long long u = u0 + k * kWriteThreads;
+        dst[k] = -1;
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (u < units) {
+            v[k] = ldg_stream(rows + u);
+            const long long row = u / upr, s = __ldg(slots + row);
+            if (s >= 0 && s < n_slots) dst[k] = s * upr + (u - row * upr);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kWriteUnits; ++k) {
+        float f[8];
+        unpack8(v[k], f);
+        int e;
+        const uint2 w = quantize_fp8_unit(f, e);  // every lane (shuffles)
+        if (dst[k] >= 0) {
+            codes[dst[k]] = w;
+            if ((dst[k] & 15) == 0) exps[dst[k] >> 4] = (uint8_t)(e + 127);
+        }
+    }
+}
+
+}  // namespace
+
+size_t plan_workspace_bytes(int batch) {
+    return batch > kFusedBatch ? (size_t)(batch + 1) * sizeof(long long) : 0;
+}
+
+int launch_plan_pages(PlanArgs a, void *ws, cudaStream_t st) {
+    const long long eb = (a.max_entries + kPlanItems - 1) / kPlanItems;
+    const long long tb = (a.max_tokens + kPlanItems - 1) / kPlanItems;
+    // one entry block at least: the new columns are noted also without a slot map
+    const int entry_blocks = (int)(eb < 1 ? 1 : eb);
+    const unsigned blocks = (unsigned)(entry_blocks + tb);
+    if (a.batch <= kFusedBatch) {
+        const size_t smem = 3 * (size_t)(a.batch + 1) * sizeof(long long);
+        if (cudaFuncSetAttribute(plan_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(3 * (kFusedBatch + 1) * sizeof(long long))) != cudaSuccess)
+            return CSA_ERR_CUDA;
+        plan_fused_kernel<<<blocks, kPlanThreads, smem, st>>>(a, entry_blocks);
+        return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    }
+    a.cu_pages = static_cast<long long *>(ws);
+    plan_scan_kernel<<<1, kPlanThreads, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return CSA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, plan_fill_kernel, a, entry_blocks) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
+int launch_paged_write(const uint16_t *rows, const long long *slots, long long n, int d, uint16_t *pool, uint8_t *codes,
+                       uint8_t *exps, long long n_slots, cudaStream_t st) {
+    const long long units = n * (d / 8);
+    if (units == 0) return CSA_OK;
+    const long long blocks = (units + kWriteThreads * kWriteUnits - 1) / (kWriteThreads * kWriteUnits);
+    if (blocks > 0x7fffffffLL) return CSA_ERR_UNSUPPORTED;
+    const uint4 *src = reinterpret_cast<const uint4 *>(rows);
+    if (codes)
+        paged_write_fp8_kernel<<<(unsigned)blocks, kWriteThreads, 0, st>>>(src, (uint32_t)(d / 8), units, slots, n_slots,
+                                                                           reinterpret_cast<uint2 *>(codes), exps);
+    else
+        paged_write_kernel<<<(unsigned)blocks, kWriteThreads, 0, st>>>(src, (uint32_t)(d / 8), units, slots, n_slots,
+                                                                       reinterpret_cast<uint4 *>(pool));
+    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
+}  // namespace csa

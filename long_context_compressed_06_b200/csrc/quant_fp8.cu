@@ -14,26 +14,12 @@
 // 2 bytes and writes 1 + 1/128 bytes per element: HBM bound.
 #include "common.cuh"
 #include "kernels.h"
+#include "quant_fp8.cuh"
 
 namespace csa {
 namespace {
 
 constexpr int kThreads = 256;
-
-// two floats -> two e4m3 codes (lo in the low byte), RNE, saturating
-CSA_DEVINL uint32_t e4m3x2_rn_sat(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// a code of -0 (0x80) becomes +0
-CSA_DEVINL uint32_t plus_zero(uint32_t w) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (((w >> (8 * i)) & 0xffu) == 0x80u) w &= ~(0xffu << (8 * i));
-    return w;
-}
 
 __global__ void __launch_bounds__(kThreads) quantize_fp8_kv_kernel(const uint16_t *__restrict__ x, long long n8,
                                                                    uint8_t *__restrict__ codes,
@@ -47,29 +33,10 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kv_kernel(const uint16_
 #pragma unroll
         for (int q = 0; q < 8; ++q) f[q] = 0.f;
     }
-    float amax = 0.f;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) amax = fmaxf(amax, fabsf(f[q]));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // smallest k with amax <= 448 * 2^k = 1.75 * 2^(8 + k), from amax's bit fields
-    int k = 0;
-    if (amax > 0.f) {
-        const uint32_t bits = __float_as_uint(amax);
-        const int ef = (int)((bits >> 23) & 0xffu);
-        if (ef == 0) {
-            k = -124;  // subnormal absmax: far below the floor
-        } else {
-            const int E = ef - 127;
-            k = (bits & 0x7fffffu) <= 0x600000u ? E - 8 : E - 7;  // mantissa <= 1.75 or above
-        }
-        k = k < -124 ? -124 : (k > 119 ? 119 : k);
-    }
-    const float inv = __uint_as_float((uint32_t)(127 - k) << 23);  // 2^-k, exact
-    const uint32_t w0 = plus_zero(e4m3x2_rn_sat(f[0] * inv, f[1] * inv) | (e4m3x2_rn_sat(f[2] * inv, f[3] * inv) << 16));
-    const uint32_t w1 = plus_zero(e4m3x2_rn_sat(f[4] * inv, f[5] * inv) | (e4m3x2_rn_sat(f[6] * inv, f[7] * inv) << 16));
+    int k;
+    const uint2 w = quantize_fp8_unit(f, k);
     if (active) {
-        *reinterpret_cast<uint2 *>(codes + t * 8) = make_uint2(w0, w1);
+        *reinterpret_cast<uint2 *>(codes + t * 8) = w;
         if ((t & 15) == 0) exps[t >> 4] = (uint8_t)(k + 127);
     }
 }
