@@ -49,6 +49,8 @@ struct AttendArgs {
     uint16_t *part_o;       // [splits][n_bq][H][D] bf16 partial outputs, each divided by its own sum
     int part_perm;          // part_o rows of one (split, query) in warp-store order (see attend_combine)
     float2 *part_ml;        // [splits][n_bq][H] (running max in log2 units, sum)
+    float *part_f;          // paged: [splits][n_bq][H][D] fp32 partial outputs, not divided, part_perm as
+                            // for part_o (null: the one split's output rows are final)
     int splits;
     long long keys_per_split;
 };
@@ -62,5 +64,42 @@ CSA_DEVINL float2 rope_cs(const AttendArgs &a, long long t, int i) {
 }
 
 int launch_attend_combine(const AttendArgs &a, cudaStream_t st);
+
+// The part of hca_attend_paged over the shared entries (attend_prefix.cu): the
+// query rows of the whole batch, [rows = n_bq * H][D], against entries
+// [0, n_shared) read through the table's row 0.  Rows are tiled by 128 and
+// entries by 128; the row_tiles * key_tiles products ("units", key tiles
+// fastest) are dealt to `pairs` CTA pairs in balanced contiguous ranges, and a
+// pair writes one partial per row tile that its range meets: partial p + r for
+// pair p and row tile r, [rank 2][DP / 16 pieces][128 threads][8] fp32 with
+// (running max in log2 units, sum) per row in ml.  O is not divided by the sum.
+struct PrefixPlan {
+    int row_tiles, key_tiles, pairs;
+    CSA_HOSTDEV long long units() const { return (long long)row_tiles * key_tiles; }
+    CSA_HOSTDEV int partials() const { return pairs + row_tiles; }
+    // pair p owns units [first(p), first(p + 1))
+    CSA_HOSTDEV long long first(int p) const { return units() * p / pairs; }
+    // the pair that owns unit u
+    CSA_HOSTDEV int pair_of(long long u) const { return (int)(((u + 1) * pairs - 1) / units()); }
+};
+
+constexpr int kPrefixRows = 128, kPrefixKeys = 128;
+CSA_HOSTDEV inline int prefix_dims(int D) { return D < 128 ? 128 : D; }  // a row's dims in the kernel (zero-padded)
+
+struct PrefixArgs {
+    AttendArgs a;        // q, gain, rope tables, table / page / n_pages, q_pos, sizes
+    PrefixPlan plan;
+    long long n_shared;
+    const uint16_t *keys;  // the entries' rows: the pool, or (linear) rows 0..n_shared-1 in order
+    bool linear;
+    float *part;         // [partials][128][DP], see above
+    float2 *ml;          // [partials][128]
+};
+
+PrefixPlan prefix_plan(long long rows, long long n_shared);
+// entries 0..n_shared-1 of an FP8 pool, in order, as bf16 rows
+int launch_prefix_rows(const uint8_t *codes, const uint8_t *exps, const int *table, int page, long long n_pages, int D,
+                       long long n_shared, uint16_t *out, cudaStream_t st);
+int launch_attend_prefix(const PrefixArgs &p, const DevCtx &ctx, cudaStream_t st);
 
 }  // namespace csa

@@ -47,6 +47,7 @@
 #include "attend_common.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "quant_fp8.cuh"
 #include "tc.cuh"
 
 namespace csa {
@@ -267,24 +268,6 @@ CSA_DEVINL const uint8_t *key_slot8(const AttendArgs &a, const Keys &ks, long lo
     }
     exps = (win ? a.win8e : a.kv8e) + r * (a.D / 128);
     return (win ? a.win8 : a.kv8) + r * a.D;
-}
-
-// 8 e4m3 codes times 2^(e - 127) -> 8 bf16, exactly: e4m3 -> f16 is exact, the
-// power-of-two scale is exact in fp32, and the product has at most 4
-// significant bits inside bf16's range (the quantiser keeps e in [3, 246]).
-CSA_DEVINL uint4 e4m3x8_bf16x8(uint2 raw, uint32_t e) {
-    const float sc = __uint_as_float(e << 23);
-    const uint32_t w[2] = {raw.x, raw.y};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
-        const float lo = __half2float(__ushort_as_half((unsigned short)(h & 0xffffu))) * sc;
-        const float hi = __half2float(__ushort_as_half((unsigned short)(h >> 16))) * sc;
-        o[i] = pack_bf16x2(lo, hi);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Warp-uniform bounded wait.  Every lane polls and the outcome is voted: a
@@ -916,11 +899,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // one split: normalise here, the head's sink logit (natural units ->
             // log2 units) joining the denominator; several: each split's rows are
             // divided by its own sum and the merge weighs them (and adds the sink)
-            const float L = a.splits == 1
+            const bool direct = PAGED ? a.part_f == nullptr : a.splits == 1;
+            const float L = direct
                                 ? l + ((a.sinks && h < a.H) ? exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - m_run) : 0.f)
                                 : l;
-            const float inv = L > 0.f ? 1.0f / L : 0.f;
-            const int orow = (int)(a.splits == 1 ? it.bq : (long long)it.split * a.n_bq + it.bq);
+            const float inv = PAGED && !direct ? 1.0f : (L > 0.f ? 1.0f / L : 0.f);
+            const int orow = (int)(direct ? it.bq : (long long)it.split * a.n_bq + it.bq);
             for (int c = 0; c < D; c += 64) {
                 float v[32];
                 if (it.ntiles > 0) {
@@ -932,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= inv;
-                if (a.splits == 1 && a.rope_cos && c == D - kRopeDim) {
+                if (direct && a.rope_cos && c == D - kRopeDim) {
                     // conjugate rotation of the rotated slice (this 64-column slab):
                     // column i pairs with i + 32, held by the head's other thread
                     // (with several splits the merge rotates the merged row)
@@ -944,7 +928,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         v[i] = first ? v[i] * cs.x + pv * cs.y : v[i] * cs.x - pv * cs.y;
                     }
                 }
-                if (a.splits > 1 && a.part_perm) {
+                if (PAGED && !direct) {
+                    // fp32, not divided: the merge weighs the partials of this kernel and of
+                    // the shared entries' kernel alike.  Warp-store order (part_perm) or rows.
+                    float4 *dst = reinterpret_cast<float4 *>(a.part_f + (size_t)orow * a.H * D);
+                    int step = 1;
+                    if (a.part_perm) {
+                        dst += ((size_t)(it.head0 / kHeads) * (D / 64) + c / 64) * 1024 + sp * 256 + lane;
+                        step = 32;
+                    } else {
+                        dst += ((size_t)h * D + c + 32 * kh) / 4;
+                    }
+                    if (h < a.H) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j * step] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    }
+                } else if (a.splits > 1 && a.part_perm) {
                     // split partials in warp-store order (the merge reads them so): this
                     // warp's 16 heads x 64 columns of the slab as one 2 KiB block, piece
                     // j * 32 + lane, so that every store writes whole sectors
@@ -953,17 +953,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) reinterpret_cast<uint4 *>(blk)[j * 32 + lane] = pack8(v + 8 * j);
                 } else if (h < a.H) {
-                    uint16_t *dst = (a.splits == 1 ? a.out : a.part_o) + ((size_t)orow * a.H + h) * D + c + 32 * kh;
+                    uint16_t *dst = (direct ? a.out : a.part_o) + ((size_t)orow * a.H + h) * D + c + 32 * kh;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) reinterpret_cast<uint4 *>(dst)[j] = pack8(v + 8 * j);
                 }
             }
-            if (h < a.H && a.splits > 1 && kh == 0)
+            if (h < a.H && !direct && kh == 0)
                 a.part_ml[((size_t)it.split * a.n_bq + it.bq) * a.H + h] =
                     it.ntiles > 0 ? make_float2(m_run, l) : make_float2(-INFINITY, 0.f);
             jt += it.ntiles;
         }
     }
+    // paged: the merge waits for this grid only, so this grid ends after the
+    // shared entries' kernel before it (a no-op for an ordinary launch)
+    if constexpr (PAGED) asm volatile("griddepcontrol.wait;" ::: "memory");
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 0) {
@@ -1028,6 +1031,7 @@ int launch_d(const AttendArgs &a, const DevCtx &ctx, cudaStream_t st, bool pdl) 
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, kern, qmap, kvmap, p) != cudaSuccess) return CSA_ERR_CUDA;
+    if (PAGED) return CSA_OK;  // the caller merges
     return a.splits > 1 ? launch_attend_combine(a, st) : CSA_OK;
 }
 

@@ -1,7 +1,9 @@
 // quant_fp8.cuh -- one 8-element unit of the FP8 KV-row format (e4m3 codes with
-// a UE8M0 exponent byte per 128 channels), shared by the row quantiser and the
-// paged FP8 write.
+// a UE8M0 exponent byte per 128 channels): its quantisation, shared by the row
+// quantiser and the paged FP8 write, and its expansion in the attention kernels.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 
@@ -47,6 +49,24 @@ CSA_DEVINL uint2 quantize_fp8_unit(const float (&f)[8], int &k) {
     const float inv = __uint_as_float((uint32_t)(127 - k) << 23);  // 2^-k, exact
     return make_uint2(plus_zero(e4m3x2_rn_sat(f[0] * inv, f[1] * inv) | (e4m3x2_rn_sat(f[2] * inv, f[3] * inv) << 16)),
                       plus_zero(e4m3x2_rn_sat(f[4] * inv, f[5] * inv) | (e4m3x2_rn_sat(f[6] * inv, f[7] * inv) << 16)));
+}
+
+// 8 e4m3 codes times 2^(e - 127) -> 8 bf16, exactly: e4m3 -> f16 is exact, the
+// power-of-two scale is exact in fp32, and the product has at most 4
+// significant bits inside bf16's range (the quantiser keeps e in [3, 246]).
+CSA_DEVINL uint4 e4m3x8_bf16x8(uint2 raw, uint32_t e) {
+    const float sc = __uint_as_float(e << 23);
+    const uint32_t w[2] = {raw.x, raw.y};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
+        const float lo = __half2float(__ushort_as_half((unsigned short)(h & 0xffffu))) * sc;
+        const float hi = __half2float(__ushort_as_half((unsigned short)(h >> 16))) * sc;
+        o[i] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 }  // namespace csa
