@@ -53,8 +53,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Merge
         np = g.plan.pair_of((long long)(rt + 1) * g.plan.key_tiles - 1) - p0 + 1;
         pml = g.ml + (size_t)(p0 + rt) * kPrefixRows + rr;
         // dim d0 of row rr: [rank][piece of 8 columns][lane half x 64 rows][8]
-        const int pvn = DP < 256 ? DP : 256, half = pvn / 2;
-        const int i = d0 / pvn, rem = d0 % pvn, hf = rem / half, col = i * half + rem % half;
+        const int hf = d0 / (DP / 2), col = d0 % (DP / 2);
         psrc = reinterpret_cast<const float4 *>(g.part) +
                (((size_t)(p0 + rt) * 2 + (rr >> 6)) * (DP / 16) * 128 + (size_t)(col / 8) * 128 + hf * 64 + (rr & 63)) * 2;
     }

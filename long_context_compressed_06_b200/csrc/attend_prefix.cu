@@ -14,6 +14,7 @@
 // two lane halves of each SM's tensor memory, so that O at D = 512 fits in 256
 // columns beside two S buffers.  One SM alone would have to run at M = 64, half
 // the tensor rate (128 rows x 512 fp32 columns fill its tensor memory).
+// Column c of lane half f of O is dim f * DP / 2 + c.
 // The price is that each SM loads 64 of a tile's 128 entries whole (its half of
 // K's rows) and all 128 entries by half their dims (its half of V's columns):
 // 128 KiB per SM and tile at D = 512, 1.33 times what one copy would be.
@@ -39,7 +40,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kSoftWarp0 = 4, kSoftWarps = 8;
 constexpr int kSlots = 8;
-constexpr uint32_t kSlotBytes = 16384;  // K: 64 keys x 128 dims, V: 128 keys x 64 dims
+constexpr uint32_t kSlotBytes = 16384;  // K: 64 keys x 128 dims, V: 16384 / DP keys x DP / 2 dims
 constexpr uint32_t kPBytes = 16384;     // 64 rows x 128 keys, bf16
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kSCols = 256;        // first column of the S buffers (64 columns each)
@@ -48,9 +49,9 @@ template <int DP>
 struct Layout {
     static constexpr int kPieces = DP / 128;              // slots of a K tile, and of a V tile, per SM
     static constexpr int kPvN = DP < 256 ? DP : 256;      // N of one P.V MMA
-    static constexpr int kHalf = kPvN / 2;                // its columns per SM
-    static constexpr int kPvMmas = DP / kPvN;
-    static constexpr int kPvSlots = kHalf / 64;           // slots (64 dims) of one P.V MMA per SM
+    static constexpr int kPvMmas = DP / kPvN;             // MMAs per 16 keys
+    static constexpr int kVKeys = 16384 / DP;             // keys of a V slot
+    static constexpr int kVChunks = DP / 128;             // its 64-dim chunks (this SM's half of V's columns)
     static constexpr uint32_t kQBytes = 64 * DP * 2;      // [DP/64][64 rows][128 B]
 };
 
@@ -59,7 +60,8 @@ struct Params {
     PrefixPlan plan;
     int n_shared;
     int linear;
-    int box;          // rows of one key box: 16, 32 or 64
+    int box;          // entries that one copy brings at most (none crosses a page): 16, 32 or 64
+    int vbox;         // those of a V copy: at most one slot's
     float *part;
     float2 *ml;
     uint32_t idesc_qk, idesc_pv;
@@ -71,6 +73,7 @@ struct Smem {
     uint64_t *full, *empty, *sfull, *sempty, *pfull, *pvdone, *qland, *qready, *qempty, *vfix;
     uint16_t *xmax;  // [2][4][64] the upper halves of the row maxima of a tile's four threads per row
     float *xsum;     // [4][64], the same memory
+    int *rows;       // [2][8] first rows of a tile's key groups (producer)
     uint32_t *tmem_slot;
     int *abort_flag;
 };
@@ -94,14 +97,15 @@ CSA_DEVINL Smem carve(uint8_t *raw) {
     s.qready = s.qland + 1;
     s.qempty = s.qready + 1;
     s.vfix = s.qempty + 1;
-    s.tmem_slot = reinterpret_cast<uint32_t *>(s.vfix + 1);
+    s.rows = reinterpret_cast<int *>(s.vfix + 1);
+    s.tmem_slot = reinterpret_cast<uint32_t *>(s.rows + 16);
     s.abort_flag = reinterpret_cast<int *>(s.tmem_slot + 1);
     return s;
 }
 
 template <int DP>
 constexpr size_t smem_bytes() {
-    return 1024 + Layout<DP>::kQBytes + kSlots * kSlotBytes + 2 * kPBytes + 1024 + (2 * kSlots + 12) * 8 + 16;
+    return 1024 + Layout<DP>::kQBytes + kSlots * kSlotBytes + 2 * kPBytes + 1024 + (2 * kSlots + 12) * 8 + 64 + 16;
 }
 static_assert(smem_bytes<512>() <= 227 * 1024, "shared memory of one CTA");
 
@@ -185,7 +189,7 @@ CSA_DEVINL float query_units(const AttendArgs &a, uint8_t *q, int r, int q4, lon
 template <int DP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                         const Params p) {
+                         const __grid_constant__ CUtensorMap vmap, const Params p) {
     using Lt = Layout<DP>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const Smem s = carve<DP>(smem_raw);
@@ -213,6 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         tc::prefetch_tmap(&qmap);
         tc::prefetch_tmap(&kmap);
+        tc::prefetch_tmap(&vmap);
     }
     if (warp == 2) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
     tc::fence_before_sync();
@@ -225,10 +230,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
+        // One thread issues, inside an elect_one branch (a copy issued by every lane under a
+        // guard, or a diverged lane, took ~200 cycles each: more than the MMAs that it feeds).
         if (p.linear) asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' copy
-        const uint32_t full0 = tc::map_to_rank(smem_u32(s.full), 0);
-        const int box = p.box, groups = kPrefixKeys / box;
-        uint32_t it = 0, nq = 0, nfix = 0;
+        const uint32_t full0 = tc::map_to_rank(smem_u32(s.full), 0), slots = smem_u32(s.slots);
+        const uint32_t qland = tc::map_to_rank(smem_u32(s.qland), rank), vfix = tc::map_to_rank(smem_u32(s.vfix), rank);
+        uint32_t it0 = 0, nq = 0, nfix = 0;
         bool ok = true;
         for (long long u = u0; u < u1 && ok;) {
             const Range rg = range_at(p, u, u1);
@@ -236,67 +243,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (rg.n == 0) continue;
             if (!(ok = warp_wait(smem_u32(s.qempty), (nq & 1u) ^ 1u, p.ctx, s.abort_flag))) break;
             ++nq;
-            mbar_arrive_expect_tx(smem_u32(s.qland), Lt::kQBytes, lane == 0);
-            for (int c = 0; c < DP / 64; ++c)
-                tc::tma_load_2d_2sm(smem_u32(s.q) + c * 8192, &qmap, smem_u32(s.qland), c * 64,
-                                    rg.rt * kPrefixRows + rank * 64, lane == 0);
-            int prev = 0;  // row of key group `lane` of the tile before
+            if (tc::elect_one()) {
+                mbar_arrive_expect_tx_cluster(qland, Lt::kQBytes);
+                for (int c = 0; c < DP / 64; c += 2)
+                    tc::tma_load_3d_2sm(smem_u32(s.q) + c * 8192, &qmap, qland, 0, rg.rt * kPrefixRows + rank * 64, c);
+            }
+            // row of 16 entries `lane` of tile j: below 0 (which reads as zeros) where no row
+            // sees them or their page does not exist
+            const auto tile_rows = [&](int j) {
+                const int key = (rg.k0 + j) * kPrefixKeys + lane * 16;
+                if (lane < 8) {
+                    int row = -kPrefixKeys;
+                    if (key < rg.vmax) {
+                        if (p.linear) {
+                            row = key;
+                        } else {
+                            const int id = __ldg(a.table + (uint32_t)key / (uint32_t)a.page);
+                            if (id >= 0 && id < a.n_pages) row = id * a.page + (int)((uint32_t)key % (uint32_t)a.page);
+                        }
+                    }
+                    s.rows[(j & 1) * 8 + lane] = row;
+                }
+                __syncwarp();
+            };
+            tile_rows(0);
             for (int j = 0; j <= rg.n && ok; ++j) {
-                // the pool row of key group `lane` (box entries); a row below 0 reads as zeros:
-                // groups that no row sees or whose page does not exist
-                int cur = -64;
-                const int key = (rg.k0 + j) * kPrefixKeys + lane * box;
-                if (j < rg.n && lane < groups && key < rg.vmax) {
-                    if (p.linear) {
-                        cur = key;
-                    } else {
-                        const int id = __ldg(a.table + (uint32_t)key / (uint32_t)a.page);
-                        if (id >= 0 && id < a.n_pages) cur = id * a.page + (int)((uint32_t)key % (uint32_t)a.page);
+                // entries of V's tile that count; the others' weights are zero, their values
+                // (anything, in memory) are cleared where a copy brings them
+                const int end = rg.vmax - (rg.k0 + j - 1) * kPrefixKeys;
+                const bool fix = j > 0 && end < kPrefixKeys && end % p.vbox != 0;
+                bool good = true;
+                if (tc::elect_one()) {
+                    uint32_t it = it0;
+                    if (j < rg.n) {
+                        const int *rows = s.rows + (j & 1) * 8 + rank * 4;
+                        for (int w = 0; w < Lt::kPieces && good; ++w, ++it) {
+                            const uint32_t sl = it % kSlots, dst = slots + sl * kSlotBytes, bar = full0 + sl * 8;
+                            if (!(good = mbar_wait(smem_u32(s.empty + sl), ((it / kSlots) & 1u) ^ 1u, p.ctx, s.abort_flag)))
+                                break;
+                            mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
+                            if (p.box == 64) {
+                                tc::tma_load_3d_2sm(dst, &kmap, bar, 0, rows[0], 2 * w);
+                            } else {
+                                for (int x = 0; x < 64; x += p.box) {
+                                    const int row = rows[x / 16];
+                                    tc::tma_load_3d_2sm(dst + x * 128, &kmap, bar, 0, row, 2 * w);
+                                    tc::tma_load_3d_2sm(dst + 8192 + x * 128, &kmap, bar, 0, row, 2 * w + 1);
+                                }
+                            }
+                        }
                     }
-                }
-                if (j < rg.n) {
-                    for (int w = 0; w < Lt::kPieces; ++w, ++it) {
-                        const int sl = it % kSlots;
-                        if (!(ok = warp_wait(smem_u32(s.empty + sl), ((it / kSlots) & 1u) ^ 1u, p.ctx, s.abort_flag)))
-                            break;
-                        mbar_arrive_expect_tx_cluster(full0 + sl * 8, kSlotBytes, lane == 0);
-                        for (int i = 0; i < groups / 2; ++i) {
-                            const int row = __shfl_sync(0xffffffffu, cur, rank * (groups / 2) + i);
-                            for (int c = 0; c < 2; ++c)
-                                tc::tma_load_2d_2sm(smem_u32(s.slots) + sl * kSlotBytes + c * 8192 + i * box * 128, &kmap,
-                                                    full0 + sl * 8, (2 * w + c) * 64, row, lane == 0);
+                    if (j > 0 && !fix) {
+                        const int *rows = s.rows + ((j - 1) & 1) * 8;
+                        for (int w = 0; w < Lt::kPieces && good; ++w, ++it) {
+                            const uint32_t sl = it % kSlots, dst = slots + sl * kSlotBytes, bar = full0 + sl * 8;
+                            if (!(good = mbar_wait(smem_u32(s.empty + sl), ((it / kSlots) & 1u) ^ 1u, p.ctx, s.abort_flag)))
+                                break;
+                            mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
+                            for (int x = 0; x < Lt::kVKeys; x += p.vbox)
+                                tc::tma_load_3d_2sm(dst + x * (Lt::kVChunks * 128), &vmap, bar, 0,
+                                                    rows[(w * Lt::kVKeys + x) / 16], rank * Lt::kVChunks);
                         }
                     }
                 }
-                if (j > 0 && ok) {
-                    // entries that no row sees are multiplied by zero weights: their values
-                    // (anything, in memory) are cleared where a box holds them
-                    const int end = rg.vmax - (rg.k0 + j - 1) * kPrefixKeys;  // entries of the tile that count
-                    const bool fix = end < kPrefixKeys && end % box != 0;
-                    for (int w = 0; w < Lt::kPieces; ++w, ++it) {
-                        const int sl = it % kSlots;
-                        if (!(ok = warp_wait(smem_u32(s.empty + sl), ((it / kSlots) & 1u) ^ 1u, p.ctx, s.abort_flag)))
-                            break;
-                        const int chunk = (w / Lt::kPvSlots) * (Lt::kPvN / 64) + rank * (Lt::kHalf / 64) + w % Lt::kPvSlots;
-                        const uint32_t slot = smem_u32(s.slots) + sl * kSlotBytes;
-                        const uint32_t bar = fix ? smem_u32(s.vfix) : full0 + sl * 8;
-                        mbar_arrive_expect_tx_cluster(fix ? tc::map_to_rank(bar, rank) : bar, kSlotBytes, lane == 0);
-                        for (int i = 0; i < groups; ++i)
-                            tc::tma_load_2d_2sm(slot + i * box * 128, &kmap, fix ? tc::map_to_rank(bar, rank) : bar, chunk * 64,
-                                                __shfl_sync(0xffffffffu, prev, i), lane == 0);
-                        if (fix) {
-                            if (!(ok = warp_wait(smem_u32(s.vfix), nfix & 1u, p.ctx, s.abort_flag))) break;
-                            ++nfix;
-                            uint4 *rows = reinterpret_cast<uint4 *>(s.slots + sl * kSlotBytes);
-                            for (int x = end * 8 + lane; x < (end + box - end % box) * 8; x += 32)
-                                rows[x] = make_uint4(0u, 0u, 0u, 0u);
-                            tc::fence_proxy_async_smem();
-                            __syncwarp();
-                            mbar_arrive_cluster(full0 + sl * 8, lane == 0);
+                __syncwarp();
+                ok = good && !*(volatile int *)s.abort_flag;
+                ok = __all_sync(0xffffffffu, ok);
+                it0 += j < rg.n ? Lt::kPieces : 0;
+                if (fix) {
+                    const int *rows = s.rows + ((j - 1) & 1) * 8;
+                    for (int w = 0; w < Lt::kPieces && ok; ++w) {
+                        const uint32_t it = it0 + w, sl = it % kSlots, dst = slots + sl * kSlotBytes;
+                        if (!(ok = warp_wait(smem_u32(s.empty + sl), ((it / kSlots) & 1u) ^ 1u, p.ctx, s.abort_flag))) break;
+                        if (tc::elect_one()) {
+                            mbar_arrive_expect_tx_cluster(vfix, kSlotBytes);
+                            for (int x = 0; x < Lt::kVKeys; x += p.vbox)
+                                tc::tma_load_3d_2sm(dst + x * (Lt::kVChunks * 128), &vmap, vfix, 0,
+                                                    rows[(w * Lt::kVKeys + x) / 16], rank * Lt::kVChunks);
                         }
+                        __syncwarp();
+                        if (!(ok = warp_wait(smem_u32(s.vfix), nfix & 1u, p.ctx, s.abort_flag))) break;
+                        ++nfix;
+                        // entry e of the slot, chunk c: [e / vbox][c][e % vbox][128 B]
+                        uint8_t *slot = s.slots + sl * kSlotBytes;
+                        for (int x = lane; x < (Lt::kVKeys * Lt::kVChunks) * 8; x += 32) {
+                            const int row = x >> 3, e = row / (Lt::kVChunks * p.vbox) * p.vbox + row % p.vbox;
+                            if (w * Lt::kVKeys + e >= end) reinterpret_cast<uint4 *>(slot)[x] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        mbar_arrive_cluster(full0 + sl * 8, lane == 0);
                     }
                 }
-                prev = cur;
+                it0 += j > 0 ? Lt::kPieces : 0;
+                if (j + 1 < rg.n) tile_rows(j + 1);
             }
         }
         if (!ok) {  // given up: copies may still be in flight to this shared memory
@@ -307,7 +347,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ MMA issuer (one thread)
         const uint64_t qdesc = tc::smem_desc(smem_u32(s.q), 1024, tc::kLayoutSw128);
         const uint64_t kdesc = tc::smem_desc(smem_u32(s.slots), 1024, tc::kLayoutSw128);
-        const uint64_t vdesc = tc::smem_desc_lbo(smem_u32(s.slots), kSlotBytes, 1024, tc::kLayoutSw128);
+        // V as stored, [keys][dims] (MN-major): 64-dim chunks vbox * 128 bytes apart, 8-key groups 1024
+        const uint64_t vdesc = tc::smem_desc_lbo(smem_u32(s.slots), p.vbox * 128, 1024, tc::kLayoutSw128);
         const uint64_t pdesc = tc::smem_desc(smem_u32(s.p), 1024, tc::kLayoutSw128);
         uint32_t it0 = 0, g0 = 0, nq = 0;
         for (long long u = u0; u < u1;) {
@@ -316,14 +357,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (rg.n == 0) continue;
             if (tc::elect_one()) {
                 uint32_t it = it0;
-                bool ok = mbar_wait_cluster(smem_u32(s.qready), nq & 1u, p.ctx, s.abort_flag);
+                bool ok = mbar_wait(smem_u32(s.qready), nq & 1u, p.ctx, s.abort_flag);
                 for (int j = 0; j <= rg.n && ok; ++j) {
                     if (j < rg.n) {
                         const uint32_t g = g0 + j, b = g & 1u;
-                        if (!(ok = mbar_wait_cluster(smem_u32(s.sempty + b), ((g >> 1) & 1u) ^ 1u, p.ctx, s.abort_flag))) break;
+                        if (!(ok = mbar_wait(smem_u32(s.sempty + b), ((g >> 1) & 1u) ^ 1u, p.ctx, s.abort_flag))) break;
                         for (int w = 0; w < Lt::kPieces; ++w, ++it) {
                             const uint32_t sl = it % kSlots;
-                            if (!(ok = mbar_wait_cluster(smem_u32(s.full + sl), (it / kSlots) & 1u, p.ctx, s.abort_flag))) break;
+                            if (!(ok = mbar_wait(smem_u32(s.full + sl), (it / kSlots) & 1u, p.ctx, s.abort_flag))) break;
                             tc::fence_after_sync();
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {  // 16 dims each: chunk 2 w + k / 4
@@ -339,20 +380,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     if (j > 0) {
                         const uint32_t g = g0 + j - 1, b = g & 1u;
-                        if (!(ok = mbar_wait_cluster(smem_u32(s.pfull + b), (g >> 1) & 1u, p.ctx, s.abort_flag))) break;
-                        for (int i = 0; i < Lt::kPvMmas; ++i) {
+                        if (!(ok = mbar_wait(smem_u32(s.pfull + b), (g >> 1) & 1u, p.ctx, s.abort_flag))) break;
+                        for (int w = 0; w < Lt::kPieces; ++w, ++it) {
                             const uint32_t sl = it % kSlots;
-                            for (int w = 0; w < Lt::kPvSlots && ok; ++w)
-                                ok = mbar_wait_cluster(smem_u32(s.full + sl + w), (it / kSlots) & 1u, p.ctx, s.abort_flag);
-                            if (!ok) break;
+                            if (!(ok = mbar_wait(smem_u32(s.full + sl), (it / kSlots) & 1u, p.ctx, s.abort_flag))) break;
                             tc::fence_after_sync();
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)  // 16 keys each
-                                tc::mma_f16_2sm(tmem + i * Lt::kHalf,
-                                                pdesc + ((b * kPBytes + (k >> 2) * 8192 + (k & 3) * 32) >> 4),
-                                                vdesc + ((sl * kSlotBytes + k * 2048) >> 4), p.idesc_pv, (j > 1 || k) ? 1u : 0u);
-                            for (int w = 0; w < Lt::kPvSlots; ++w) tc::mma_commit_2sm(smem_u32(s.empty + sl + w));
-                            it += Lt::kPvSlots;
+                            for (int k = 0; k < Lt::kVKeys / 16; ++k) {  // 16 keys each
+                                const uint32_t kt = w * (Lt::kVKeys / 16) + k;
+                                const uint32_t x = k * 16, voff = x / p.vbox * (Lt::kVChunks * p.vbox * 128) + x % p.vbox * 128;
+#pragma unroll
+                                for (int i = 0; i < Lt::kPvMmas; ++i)
+                                    tc::mma_f16_2sm(tmem + i * (Lt::kPvN / 2),
+                                                    pdesc + ((b * kPBytes + (kt >> 2) * 8192 + (kt & 3) * 32) >> 4),
+                                                    vdesc + ((sl * kSlotBytes + voff + i * 2 * p.vbox * 128) >> 4), p.idesc_pv,
+                                                    (j > 1 || kt) ? 1u : 0u);
+                            }
+                            tc::mma_commit_2sm(smem_u32(s.empty + sl));
                         }
                         if (!ok) break;
                         tc::mma_commit_2sm(smem_u32(s.pvdone + b));
@@ -404,6 +448,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const long long row = (long long)rg.rt * kPrefixRows + rank * 64 + r;
             const long long t = row < n_rows ? __ldg(a.q_pos + row / a.H) : -1;
             const int vis = (int)n_visible(t, a.m, p.n_shared);
+            // entries of a tile need a mask only past the fewest that a row of this warp sees,
+            // or where a page is missing
+            const int vis_min = __reduce_min_sync(0xffffffffu, vis);
+            bool holes = false;
+            for (int pg = rg.k0 * kPrefixKeys / a.page + lane; (long long)pg * a.page < rg.vmax; pg += 32) {
+                const int id = __ldg(a.table + pg);
+                holes |= id < 0 || id >= a.n_pages;
+            }
+            holes = __any_sync(0xffffffffu, holes);
             warp_wait(smem_u32(s.qland), nq & 1u, p.ctx, s.abort_flag);
             ++nq;
             s.xsum[q4 * 64 + r] = query_units<DP>(a, s.q, r, q4, t, q_rw);
@@ -420,17 +473,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float m_run = -INFINITY, l = 0.f;
             for (int j = 0; j < rg.n; ++j, ++g) {
                 const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
-                // which of this thread's 32 entries take part
                 const int key = (rg.k0 + j) * kPrefixKeys + hf * 64 + wg * 32;
-                const int lim = vis - key;
-                uint32_t mask = lim >= 32 ? 0xffffffffu : (lim <= 0 ? 0u : (1u << lim) - 1u);
+                const bool whole = !holes && key + 32 <= vis_min;
+                uint32_t mask = 0xffffffffu;  // which of this thread's 32 entries take part
+                if (!whole) {
+                    const int lim = vis - key;
+                    mask = lim >= 32 ? 0xffffffffu : (lim <= 0 ? 0u : (1u << lim) - 1u);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (lim > 16 * h) {
-                        const int id = __ldg(a.table + (uint32_t)(key + 16 * h) / (uint32_t)a.page);
-                        if (id < 0 || id >= a.n_pages) mask &= h ? 0x0000ffffu : 0xffff0000u;
-                    }
-                const bool whole = __all_sync(0xffffffffu, mask == 0xffffffffu);
+                    for (int h = 0; h < 2; ++h)
+                        if (lim > 16 * h) {
+                            const int id = __ldg(a.table + (uint32_t)(key + 16 * h) / (uint32_t)a.page);
+                            if (id < 0 || id >= a.n_pages) mask &= h ? 0x0000ffffu : 0xffff0000u;
+                        }
+                }
                 warp_wait(smem_u32(s.sfull + b), ph, p.ctx, s.abort_flag);
                 tc::fence_after_sync();
                 float sc[32];
@@ -439,13 +494,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 mbar_arrive_cluster(sempty0 + b * 8, lane == 0);
-                float mt = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    sc[i] *= rq;
-                    if (!whole) sc[i] = (mask >> i) & 1u ? sc[i] : -INFINITY;
-                    mt = fmaxf(mt, sc[i]);
+                for (int i = 0; i < 32; ++i) sc[i] *= rq;
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sc[i] = (mask >> i) & 1u ? sc[i] : -INFINITY;
                 }
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], sc[i]);
+                float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 // the row's maximum over its four threads, each rounded to 16 bits towards zero
                 // (any reference near the maximum serves, as long as the four agree)
                 s.xmax[(b * 4 + q4) * 64 + r] = (uint16_t)(__float_as_uint(mt) >> 16);
@@ -475,15 +533,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (m_run == -INFINITY) m_run = mt;
                 const float mref = m_run == -INFINITY ? 0.f : m_run;
-                float ps = 0.f;
+                float ps[2] = {0.f, 0.f};
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const float p0 = exp2f(sc[i] - mref), p1 = exp2f(sc[i + 1] - mref);
-                    ps += p0 + p1;
+                    const float p0 = exp2_ftz(sc[i] - mref), p1 = exp2_ftz(sc[i + 1] - mref);
+                    ps[0] += p0;
+                    ps[1] += p1;
                     pk[i / 2] = pack_bf16x2(p0, p1);
                 }
-                l += ps;
+                l += ps[0] + ps[1];
                 // P buffer b was read by the P.V of tile g - 2
                 warp_wait(smem_u32(s.pvdone + b), ph ^ 1u, p.ctx, s.abort_flag);
                 uint8_t *prow = s.p + b * kPBytes + hf * 8192 + r * 128;
@@ -566,22 +625,24 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     p.ctx = ctx;
     p.idesc_qk = idesc(kPrefixKeys, false);
     p.idesc_pv = idesc(Layout<DP>::kPvN, true);
-    // the largest box of key rows that never crosses a page
     p.box = x.linear || x.a.page % 64 == 0 ? 64 : (x.a.page % 32 == 0 ? 32 : 16);
+    p.vbox = std::min(p.box, Layout<DP>::kVKeys);
     auto kern = attend_prefix_kernel<DP>;
     constexpr size_t smem = smem_bytes<DP>();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return CSA_ERR_CUDA;
-    const uint64_t D = (uint64_t)x.a.D, stride = D * 2;
-    CUtensorMap qmap, kmap;
-    const uint64_t qdims[2] = {D, (uint64_t)(x.a.n_bq * x.a.H)};
-    const uint32_t qbox[2] = {64, 64};
-    const uint64_t kdims[2] = {D, (uint64_t)(x.linear ? x.n_shared : x.a.n_pages * x.a.page)};
-    const uint32_t kbox[2] = {64, (uint32_t)p.box};
-    if (!encode_tensor_map(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x.a.q, qdims, &stride, qbox,
-                           CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tensor_map(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x.keys, kdims, &stride, kbox,
-                           CU_TENSOR_MAP_SWIZZLE_128B))
+    // [64-dim chunk][row][64]: one copy brings several chunks of its rows (past D: zeros)
+    const auto encode = [&](CUtensorMap *map, const uint16_t *base, long long rows, int box_rows, int chunks) {
+        const uint64_t dims[3] = {64, (uint64_t)rows, (uint64_t)(x.a.D / 64)};
+        const uint64_t strides[2] = {(uint64_t)x.a.D * 2, 128};
+        const uint32_t box[3] = {64, (uint32_t)box_rows, (uint32_t)chunks};
+        return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+                                 CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    const long long key_rows = x.linear ? x.n_shared : x.a.n_pages * x.a.page;
+    CUtensorMap qmap, kmap, vmap;
+    if (!encode(&qmap, x.a.q, x.a.n_bq * x.a.H, 64, 2) || !encode(&kmap, x.keys, key_rows, p.box, p.box == 64 ? 2 : 1) ||
+        !encode(&vmap, x.keys, key_rows, p.vbox, Layout<DP>::kVChunks))
         return CSA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * x.plan.pairs));
@@ -593,7 +654,7 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = x.linear ? 1 : 0;  // a dependent of the rows' copy
-    return cudaLaunchKernelEx(&cfg, kern, qmap, kmap, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, qmap, kmap, vmap, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 }  // namespace

@@ -153,12 +153,11 @@ CSA_DEVINL void mma_commit_2sm(uint32_t bar) {
 }
 // TMA load into this CTA's shared memory that reports its bytes to `bar`, a
 // shared::cluster address that may lie in the pair's other CTA
-CSA_DEVINL void tma_load_2d_2sm(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, bool pred) {
+CSA_DEVINL void tma_load_3d_2sm(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
     asm volatile(
-        "{\n\t.reg .pred g;\n\tsetp.ne.b32 g, %5, 0;\n\t"
-        "@g cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-        "[%2];\n\t}"
-        ::"r"(dst), "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"((int)pred)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
 CSA_DEVINL uint32_t cluster_rank() {
