@@ -34,12 +34,10 @@ struct AttendArgs {
     int W;
     // Paged cache (table set; kv / kv8 then hold [n_pages][page] rows): entry j of
     // sequence b is row table[b][j / page] * page + j % page, the window is a ring
-    // of win_rows rows per sequence (position u at row u % win_rows), and the key
-    // set starts at entry e_first (the entries before it are another kernel's)
+    // of win_rows rows per sequence (position u at row u % win_rows)
     const int *table;       // [batch][max_pages] or null
     int max_pages, page;
     long long n_pages;
-    long long e_first;
     const int *q_pos;       // [n_bq]
     int nq;
     long long n_bq;         // batch * nq
@@ -65,38 +63,44 @@ CSA_DEVINL float2 rope_cs(const AttendArgs &a, long long t, int i) {
 
 int launch_attend_combine(const AttendArgs &a, cudaStream_t st);
 
-// The part of hca_attend_paged over the shared entries (attend_prefix.cu): the
-// query rows of the whole batch, [rows = n_bq * H][D], against entries
-// [0, n_shared) read through the table's row 0.  Rows are tiled by 128 and
-// entries by 128; the row_tiles * key_tiles products ("units", key tiles
-// fastest) are dealt to `pairs` CTA pairs in balanced contiguous ranges, and a
-// pair writes one partial per row tile that its range meets: partial p + r for
-// pair p and row tile r, [rank 2][DP / 16 pieces][128 threads][8] fp32 with
-// (running max in log2 units, sum) per row in ml.  O is not divided by the sum.
+// Paged attention of a batch with a shared prefix (attend_prefix.cu): the query
+// rows of the whole batch, [rows = n_bq * H][D], by tiles of 128, against tiles
+// of 128 keys.  A row tile's units are the tiles of shared entries (read through
+// the table's row 0) and of its requests' own keys; the units of all row tiles
+// are dealt to `active` CTA pairs in balanced contiguous ranges, and a pair
+// writes one partial per row tile that its range meets: partial p + r for pair p
+// and row tile r, [rank 2][DP / 8 pieces][128 threads][4] fp32 with (running max
+// in log2 units, sum) per row in ml.  O is not divided by the sum.
 struct PrefixPlan {
-    int row_tiles, key_tiles, pairs;
-    CSA_HOSTDEV long long units() const { return (long long)row_tiles * key_tiles; }
+    int row_tiles, pairs;
     CSA_HOSTDEV int partials() const { return pairs + row_tiles; }
-    // pair p owns units [first(p), first(p + 1))
-    CSA_HOSTDEV long long first(int p) const { return units() * p / pairs; }
+    // pairs that `units` units are dealt to: pair p owns [units p / active, units (p + 1) / active)
+    CSA_HOSTDEV int active(long long units) const {
+        const long long most = (units + kMinUnits - 1) / kMinUnits;
+        return (int)(most < 1 ? 1 : (most < pairs ? most : pairs));
+    }
     // the pair that owns unit u
-    CSA_HOSTDEV int pair_of(long long u) const { return (int)(((u + 1) * pairs - 1) / units()); }
+    CSA_HOSTDEV int pair_of(long long u, long long units) const {
+        return (int)(((u + 1) * active(units) - 1) / units);
+    }
+    static constexpr int kMinUnits = 1;
 };
 
 constexpr int kPrefixRows = 128, kPrefixKeys = 128;
 CSA_HOSTDEV inline int prefix_dims(int D) { return D < 128 ? 128 : D; }  // a row's dims in the kernel (zero-padded)
 
 struct PrefixArgs {
-    AttendArgs a;        // q, gain, rope tables, table / page / n_pages, q_pos, sizes
+    AttendArgs a;          // of the whole call
     PrefixPlan plan;
     long long n_shared;
     const uint16_t *keys;  // the entries' rows: the pool, or (linear) rows 0..n_shared-1 in order
     bool linear;
-    float *part;         // [partials][128][DP], see above
-    float2 *ml;          // [partials][128]
+    float *part;           // [partials][128][DP], see above
+    float2 *ml;            // [partials][128]
+    long long *first;      // [row_tiles + 1] first unit of every row tile, and the units of all (out)
 };
 
-PrefixPlan prefix_plan(long long rows, long long n_shared);
+PrefixPlan prefix_plan(long long rows);
 // entries 0..n_shared-1 of an FP8 pool, in order, as bf16 rows
 int launch_prefix_rows(const uint8_t *codes, const uint8_t *exps, const int *table, int page, long long n_pages, int D,
                        long long n_shared, uint16_t *out, cudaStream_t st);

@@ -1,13 +1,17 @@
-// attend_prefix.cu -- attention of a whole batch over the entries that all its
-// requests share, as one product (the n_shared part of hca_attend_paged).
+// attend_prefix.cu -- hca_attend_paged for a batch whose requests share a long
+// prefix: the query rows of the whole batch as one product with the shared
+// entries, and each request's own entries and window beside it.
 //
 // With the query rows of every request stacked, Q is [R = batch * nq * H][D]
 // and the shared entries X [n_shared][D] are keys and values of all of them:
 //   S = scale / RMS(q) * Q X^T,   P = exp2(S - m),   O = P X
-// with the running maximum m and sum l of every row kept per tile of 128
-// entries (m raised only when it grows by more than 2^8, so that O in tensor
-// memory is rarely rescaled).  O, m and l of a tile range go out in 32 bits and
-// are merged with each request's own entries and window.
+// with the running maximum m and sum l of every row kept per tile of 128 keys
+// (m raised only when it grows by more than 2^8, so that O in tensor memory is
+// rarely rescaled).  A tile of 128 rows continues with the own keys of each of
+// its requests, 128 at a time, the rows of other requests masked: with H = 128
+// heads a row tile is one request and nothing is wasted, and a batch of small
+// heads shares the tile's tensor work that the mask throws away.  O, m and l of
+// a range of tiles go out in 32 bits and are merged (attend_paged.cu).
 //
 // A pair of SMs owns 128 rows (cta_group::2, M = 128): every MMA reads half of
 // its B operand from each SM, and an accumulator takes 64 rows x N/2 columns x
@@ -15,16 +19,23 @@
 // columns beside two S buffers.  One SM alone would have to run at M = 64, half
 // the tensor rate (128 rows x 512 fp32 columns fill its tensor memory).
 // Column c of lane half f of O is dim f * DP / 2 + c.
-// The price is that each SM loads 64 of a tile's 128 entries whole (its half of
-// K's rows) and all 128 entries by half their dims (its half of V's columns):
+// The price is that each SM loads 64 of a tile's 128 keys whole (its half of
+// K's rows) and all 128 keys by half their dims (its half of V's columns):
 // 128 KiB per SM and tile at D = 512, 1.33 times what one copy would be.
 // The tensor cores' operand reads (224 KiB), these loads and P share the
 // 128 B/cycle of shared memory, which bounds the kernel at D = 512.
 //
-// Warps: 0 TMA producer, 1 MMA issuer (the pair's leader), 2 tensor memory and
-// the query tile's hand-over, 4..11 softmax (four threads per row: lane half x
+// Warps: 0..3 producers of K and V, 4 MMA issuer (the pair's leader), 5 tensor
+// memory and the query tile, 6..13 softmax (four threads per row: lane half x
 // 32-column half).  16 KiB slots form one ring for both operands, in the order
-// the MMAs consume them (K0, K1, V0, K2, V1, ...).  Work: see PrefixPlan.
+// the MMAs consume them (K0, K1, V0, K2, V1, ...); the producers take its
+// positions in turn, whatever they hold: shared entries by TMA, own keys (rows
+// of any page and of the ring) by 16-byte asynchronous copies, FP8 rows expanded
+// on the way.  (A producer per kind would pass over the other kind's positions,
+// and a slot's phase bit cannot tell it how far the ring is.)
+//
+// The tiles of all row tiles ("units") are counted on the device from the
+// positions and dealt to the pairs in balanced contiguous ranges.
 #include <algorithm>
 #include <cstring>
 
@@ -37,8 +48,8 @@
 namespace csa {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kSoftWarp0 = 4, kSoftWarps = 8;
+constexpr int kThreads = 448;
+constexpr int kProducers = 4, kMmaWarp = 4, kQueryWarp = 5, kSoftWarp0 = 6, kSoftWarps = 8;
 constexpr int kSlots = 8;
 constexpr uint32_t kSlotBytes = 16384;  // K: 64 keys x 128 dims, V: 16384 / DP keys x DP / 2 dims
 constexpr uint32_t kPBytes = 16384;     // 64 rows x 128 keys, bf16
@@ -60,6 +71,7 @@ struct Params {
     PrefixPlan plan;
     int n_shared;
     int linear;
+    long long *first; // [row_tiles + 1] first unit of a row tile; the units of all
     int box;          // entries that one copy brings at most (none crosses a page): 16, 32 or 64
     int vbox;         // those of a V copy: at most one slot's
     float *part;
@@ -73,7 +85,8 @@ struct Smem {
     uint64_t *full, *empty, *sfull, *sempty, *pfull, *pvdone, *qland, *qready, *qempty, *vfix;
     uint16_t *xmax;  // [2][4][64] the upper halves of the row maxima of a tile's four threads per row
     float *xsum;     // [4][64], the same memory
-    int *rows;       // [2][8] first rows of a tile's key groups (producer)
+    long long *left; // this pair's units
+    int *start;      // its first row tile, and the first unit's number within it
     uint32_t *tmem_slot;
     int *abort_flag;
 };
@@ -97,42 +110,198 @@ CSA_DEVINL Smem carve(uint8_t *raw) {
     s.qready = s.qland + 1;
     s.qempty = s.qready + 1;
     s.vfix = s.qempty + 1;
-    s.rows = reinterpret_cast<int *>(s.vfix + 1);
-    s.tmem_slot = reinterpret_cast<uint32_t *>(s.rows + 16);
+    s.left = reinterpret_cast<long long *>(s.vfix + kProducers);
+    s.start = reinterpret_cast<int *>(s.left + 1);
+    s.tmem_slot = reinterpret_cast<uint32_t *>(s.start + 2);
     s.abort_flag = reinterpret_cast<int *>(s.tmem_slot + 1);
     return s;
 }
 
 template <int DP>
 constexpr size_t smem_bytes() {
-    return 1024 + Layout<DP>::kQBytes + kSlots * kSlotBytes + 2 * kPBytes + 1024 + (2 * kSlots + 12) * 8 + 64 + 16;
+    return 1024 + Layout<DP>::kQBytes + kSlots * kSlotBytes + 2 * kPBytes + 1024 + (2 * kSlots + 11 + kProducers) * 8 + 32;
 }
 static_assert(smem_bytes<512>() <= 227 * 1024, "shared memory of one CTA");
 
-// A pair's part of one row tile: tiles [k0, k0 + n) of 128 entries, vmax the
-// most entries that any row of the tile sees.  Tiles past vmax are left out.
-struct Range {
-    int rt, k0, n, vmax;
-    long long next;  // first unit after the range
+// ---------------------------------------------------------------- units
+// The tiles of row tile rt, in order: the shared entries that any of its rows
+// sees, then request by request the own keys of its queries in the row tile.
+CSA_DEVINL int visible(const Params &p, int t, int cap) {
+    const uint32_t v = t < 0 ? 0u : ((uint32_t)t + 1u) / (uint32_t)p.a.m;
+    return v < (uint32_t)cap ? (int)v : cap;
+}
+
+// The own keys of queries [q0, q1] of one request: entries n_shared..n_shared + n_own - 1,
+// then the window rows of positions u0..u0 + (total - n_own) - 1.
+struct Own {
+    int n_own, u0;
+    long long total;
+    CSA_DEVINL int tiles() const { return (int)((total + kPrefixKeys - 1) / kPrefixKeys); }
 };
 
-// warp-collective
-CSA_DEVINL Range range_at(const Params &p, long long u, long long u1) {
-    Range r;
-    const int KT = p.plan.key_tiles;
-    r.rt = (int)(u / KT);
-    r.k0 = (int)(u - (long long)r.rt * KT);
-    const int k1 = (int)std::min<long long>(KT, r.k0 + (u1 - u));
-    r.next = u + (k1 - r.k0);
-    const long long row0 = (long long)r.rt * kPrefixRows;
-    const long long b0 = row0 / p.a.H, b1 = std::min(p.a.n_bq - 1, (row0 + kPrefixRows - 1) / p.a.H);
-    int v = 0;
-    for (long long b = b0 + (threadIdx.x & 31); b <= b1; b += 32)
-        v = std::max(v, (int)n_visible(__ldg(p.a.q_pos + b), p.a.m, p.n_shared));
-    r.vmax = __reduce_max_sync(0xffffffffu, v);
-    r.n = std::max(0, std::min(k1, (r.vmax + kPrefixKeys - 1) / kPrefixKeys) - r.k0);
+CSA_DEVINL Own own_keys(const Params &p, int q0, int q1) {
+    int vis = 0, u0 = 0x7fffffff, u1 = -1;
+    for (int q = q0; q <= q1; ++q) {
+        const int t = __ldg(p.a.q_pos + q);
+        if (t < 0) continue;
+        vis = std::max(vis, visible(p, t, (int)p.a.N));
+        u0 = std::min(u0, std::max(0, t - p.a.W + 1));
+        u1 = std::max(u1, t);
+    }
+    Own o;
+    o.n_own = std::max(0, vis - p.n_shared);
+    o.u0 = u0;
+    o.total = o.n_own + (u1 >= 0 ? (long long)u1 - u0 + 1 : 0);
+    return o;
+}
+
+// Queries (rows of q_pos) bq0..bq1 of row tile rt.
+struct Queries {
+    int bq0, bq1;
+};
+
+CSA_DEVINL Queries queries_of(const Params &p, int rt) {
+    Queries r;
+    const uint32_t row0 = (uint32_t)rt * kPrefixRows, H = (uint32_t)p.a.H;
+    r.bq0 = (int)(row0 / H);
+    r.bq1 = (int)std::min<uint32_t>((uint32_t)p.a.n_bq - 1, (row0 + kPrefixRows - 1) / H);
     return r;
 }
+
+// units of row tile rt, by one thread
+CSA_DEVINL int count_units(const Params &p, int rt) {
+    const Queries r = queries_of(p, rt);
+    int vmax = 0, n = 0;
+    for (int q = r.bq0; q <= r.bq1;) {
+        const int e = std::min(r.bq1, q / p.a.nq * p.a.nq + p.a.nq - 1);
+        n += own_keys(p, q, e).tiles();
+        for (; q <= e; ++q) vmax = std::max(vmax, visible(p, __ldg(p.a.q_pos + q), p.n_shared));
+    }
+    return n + (vmax + kPrefixKeys - 1) / kPrefixKeys;
+}
+
+// Which units are this pair's, by one warp; pair 0 writes where the row tiles begin.
+CSA_DEVINL void deal_units(const Params &p, const Smem &s, int pair, bool write) {
+    const int lane = threadIdx.x & 31, RT = p.plan.row_tiles;
+    long long total = 0;
+    int n = 0;
+    for (int r0 = 0; r0 < RT; r0 += 32) {
+        n = r0 + lane < RT ? count_units(p, r0 + lane) : 0;
+        int inc = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += up;
+        }
+        if (write && r0 + lane < RT) p.first[r0 + lane] = total + inc - n;
+        total += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (write && lane == 0) p.first[RT] = total;
+    const int P = p.plan.active(total);
+    const long long u0 = pair < P ? total * pair / P : 0, u1 = pair < P ? total * (pair + 1) / P : 0;
+    if (lane == 0) *s.left = u1 - u0;
+    if (u1 == u0) return;
+    long long base = 0;
+    for (int r0 = 0; r0 < RT; r0 += 32) {
+        if (RT > 32) n = r0 + lane < RT ? count_units(p, r0 + lane) : 0;
+        int inc = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += up;
+        }
+        if (base + inc - n <= u0 && u0 < base + inc) {
+            s.start[0] = r0 + lane;
+            s.start[1] = (int)(u0 - (base + inc - n));
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+        if (base > u0) break;
+    }
+}
+
+// A pair's part of one row tile: n of its tiles from number x on.
+struct Range {
+    int rt, x, n;
+    int vmax, shared;  // shared entries that any of its rows sees, and their tiles
+    Queries q;
+};
+
+// One of a range's tiles: 128 shared entries (own.total < 0) or packed own keys, from `first` on.
+struct Tile {
+    long long first;
+    int b;  // the request
+    Own own;
+    CSA_DEVINL bool shared() const { return own.total < 0; }
+};
+
+// Walks a pair's ranges and the tiles of each; every role does so by itself, whole warps together.
+struct Walk {
+    long long left;
+    int rt, x;
+    CSA_DEVINL explicit Walk(const Smem &s) : left(*s.left), rt(s.start[0]), x(s.start[1]) {}
+
+    CSA_DEVINL bool next(const Params &p, Range &r) {
+        const int lane = threadIdx.x & 31;
+        while (left > 0) {
+            r.rt = rt;
+            r.x = x;
+            r.q = queries_of(p, rt);
+            int v = 0, n = 0;
+            for (int q = r.q.bq0 + lane; q <= r.q.bq1; q += 32) v = std::max(v, visible(p, __ldg(p.a.q_pos + q), p.n_shared));
+            const int b0 = r.q.bq0 / p.a.nq, b1 = r.q.bq1 / p.a.nq;
+            for (int b = b0 + lane; b <= b1; b += 32)
+                n += own_keys(p, std::max(r.q.bq0, b * p.a.nq), std::min(r.q.bq1, b * p.a.nq + p.a.nq - 1)).tiles();
+            r.vmax = __reduce_max_sync(0xffffffffu, v);
+            r.shared = (r.vmax + kPrefixKeys - 1) / kPrefixKeys;
+            n = __reduce_add_sync(0xffffffffu, n) + r.shared - x;
+            ++rt;
+            x = 0;
+            if (n <= 0) continue;
+            r.n = (int)std::min<long long>(n, left);
+            left -= r.n;
+            return true;
+        }
+        return false;
+    }
+};
+
+struct Tiles {
+    Tile t;
+    int x;
+
+    CSA_DEVINL void request(const Params &p, const Range &r, int b) {
+        t.b = b;
+        t.own = own_keys(p, std::max(r.q.bq0, b * p.a.nq), std::min(r.q.bq1, b * p.a.nq + p.a.nq - 1));
+    }
+    CSA_DEVINL Tiles(const Params &p, const Range &r) {
+        x = r.x;
+        t.own.total = -1;
+        t.own.n_own = t.own.u0 = t.b = 0;
+        t.first = (long long)x * kPrefixKeys;
+        if (x >= r.shared) {
+            long long y = x - r.shared;
+            request(p, r, r.q.bq0 / p.a.nq);
+            while (y >= t.own.tiles()) {
+                y -= t.own.tiles();
+                request(p, r, t.b + 1);
+            }
+            t.first = y * kPrefixKeys;
+        }
+    }
+    CSA_DEVINL void next(const Params &p, const Range &r) {
+        ++x;
+        t.first += kPrefixKeys;
+        if (x < r.shared) return;
+        if (x == r.shared) {
+            t.first = 0;
+            request(p, r, r.q.bq0 / p.a.nq);
+        }
+        while (t.first >= t.own.total) {
+            t.first = 0;
+            request(p, r, t.b + 1);
+        }
+    }
+};
 
 CSA_DEVINL bool warp_wait(uint32_t bar, uint32_t parity, const DevCtx &ctx, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctx, abort));
@@ -186,7 +355,123 @@ CSA_DEVINL float query_units(const AttendArgs &a, uint8_t *q, int r, int q4, lon
     return ss;
 }
 
-template <int DP>
+CSA_DEVINL uint32_t low_bits(long long n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (int)n) - 1u); }
+
+// Which of keys off..off + 31 of a tile the row of a query at t (of request
+// b_row, seeing vis shared entries) takes.
+CSA_DEVINL uint32_t key_mask(const Params &p, const Tile &tile, int off, int t, int vis, int b_row) {
+    const AttendArgs &a = p.a;
+    const long long k0 = tile.first + off;  // entry, or packed own key
+    const int *table = a.table;
+    long long ent, e0 = k0;  // entries from e0 on: the first `ent` of the 32 keys are the row's
+    uint32_t mask;
+    if (tile.shared()) {
+        ent = vis - k0;
+        mask = low_bits(ent);
+    } else {
+        if (t < 0 || b_row != tile.b) return 0u;
+        ent = std::max(0, visible(p, t, (int)a.N) - p.n_shared) - k0;
+        // positions t-W+1..t, key n_own + (u - u0)
+        const long long lo = tile.own.n_own + (long long)std::max(0, t - a.W + 1) - tile.own.u0 - k0;
+        const long long hi = tile.own.n_own + (long long)t - tile.own.u0 - k0;
+        mask = low_bits(ent) | (low_bits(hi + 1) & ~low_bits(lo));
+        table += (size_t)tile.b * a.max_pages;
+        e0 += p.n_shared;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (ent > 16 * h) {  // 16 entries of one page (n_shared, k0 and the page are multiples of 16)
+            const int id = __ldg(table + (uint32_t)(e0 + 16 * h) / (uint32_t)a.page);
+            if (id < 0 || id >= a.n_pages) mask &= ~(low_bits(std::min(ent - 16 * h, 16LL)) << (16 * h));
+        }
+    return mask;
+}
+
+// One slot of an own tile, by one warp: K (V = false): the CTA's 64 keys x dims
+// [128 w, 128 w + 128), V: keys [w kVKeys, ..) x the CTA's half of the dims, in
+// the layouts that the TMA copies of shared tiles make.  Keys that do not exist
+// are zeros (no weight is on them, and nothing is known of their memory).
+template <int DP, bool FP8, bool V>
+CSA_DEVINL void gather_slot(const Params &p, const Tile &t, int rank, int w, uint32_t dst) {
+    using Lt = Layout<DP>;
+    const AttendArgs &a = p.a;
+    const int lane = threadIdx.x & 31;
+    constexpr int kKeys = V ? Lt::kVKeys : 64, kPer = kKeys / 32, kUnits = V ? Lt::kVChunks * 8 : 16;  // 8-dim units per key
+    const int key0 = V ? w * kKeys : rank * 64, dim0 = V ? rank * (DP / 2) : w * 128;
+    // rows of keys key0 + lane, + 32, ..: index, ~index in the rings, or none
+    constexpr long long kNone = 0x7fffffffffffffffLL;
+    long long row[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const long long k = t.first + key0 + i * 32 + lane;
+        row[i] = kNone;
+        if (k < t.own.n_own) {
+            const uint32_t e = (uint32_t)(p.n_shared + k);
+            const int id = __ldg(a.table + (size_t)t.b * a.max_pages + e / (uint32_t)a.page);
+            if (id >= 0 && id < a.n_pages) row[i] = (long long)id * a.page + e % (uint32_t)a.page;
+        } else if (k < t.own.total) {
+            const uint32_t u = (uint32_t)(t.own.u0 + (int)(k - t.own.n_own));
+            row[i] = ~((long long)t.b * a.win_rows + u % (uint32_t)a.win_rows);
+        }
+    }
+    // shared-memory address of 16-byte unit u of key k (both within the slot)
+    const auto at = [&](int k, int u) {
+        const uint32_t base = V ? (uint32_t)(k / p.vbox * (Lt::kVChunks * p.vbox) + (u >> 3) * p.vbox + k % p.vbox) * 128
+                                : (uint32_t)(u >> 3) * 8192 + k * 128;
+        return dst + base + (((u & 7) ^ (k & 7)) << 4);
+    };
+    if constexpr (FP8) {
+        constexpr int kU2 = kUnits / 2;  // 16 codes each
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+#pragma unroll
+            for (int c0 = 0; c0 < kU2; c0 += 8) {  // 32 * kU2 units of these 32 keys, 8 loads in flight
+                uint4 v[8];
+                uint32_t e[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const int q = (c0 + c) * 32 + lane, k = q / kU2, d = dim0 + (q % kU2) * 16;
+                    const long long r = __shfl_sync(0xffffffffu, row[i], k);
+                    v[c] = make_uint4(0u, 0u, 0u, 0u);
+                    e[c] = 0u;
+                    if (r != kNone) {
+                        const size_t ri = (size_t)(r < 0 ? ~r : r);
+                        v[c] = ldg16((r < 0 ? a.win8 : a.kv8) + ri * a.D + d);
+                        e[c] = __ldg((r < 0 ? a.win8e : a.kv8e) + ri * (a.D / 128) + d / 128);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const int q = (c0 + c) * 32 + lane, k = i * 32 + q / kU2, u = (q % kU2) * 2;
+                    const uint4 lo = e4m3x8_bf16x8(make_uint2(v[c].x, v[c].y), e[c]);
+                    const uint4 hi = e4m3x8_bf16x8(make_uint2(v[c].z, v[c].w), e[c]);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(k, u)), "r"(lo.x), "r"(lo.y), "r"(lo.z),
+                                 "r"(lo.w)
+                                 : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(k, u + 1)), "r"(hi.x), "r"(hi.y),
+                                 "r"(hi.z), "r"(hi.w)
+                                 : "memory");
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+#pragma unroll 8
+            for (int c = 0; c < kUnits; ++c) {
+                const int q = c * 32 + lane, k = q / kUnits, u = q % kUnits, d = dim0 + u * 8;
+                const long long r = __shfl_sync(0xffffffffu, row[i], k);
+                const bool there = r != kNone && d < a.D;
+                const uint16_t *src = (r < 0 ? a.win + (size_t)~r * a.D : a.kv + (size_t)r * a.D) + d;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(i * 32 + k, u)),
+                             "l"(there ? src : a.win), "r"(there ? 16 : 0)
+                             : "memory");
+            }
+        }
+    }
+}
+
+template <int DP, bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const Params p) {
@@ -212,138 +497,156 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(s.qland, 1);
         mbar_init(s.qready, q_rw ? 2 * kSoftWarps : 2);  // leader
         mbar_init(s.qempty, 1 + kSoftWarps);
-        mbar_init(s.vfix, 1);
+        for (int i = 0; i < kProducers; ++i) mbar_init(s.vfix + i, 1);
         *s.abort_flag = 0;
         fence_mbar_init();
         tc::prefetch_tmap(&qmap);
         tc::prefetch_tmap(&kmap);
         tc::prefetch_tmap(&vmap);
     }
-    if (warp == 2) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
+    if (warp == kQueryWarp) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
+    if (warp == kSoftWarp0) deal_units(p, s, pair, blockIdx.x == 0);
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_sync();  // both CTAs' barriers exist
     tc::fence_after_sync();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = *s.tmem_slot;
-    const long long u0 = p.plan.first(pair), u1 = p.plan.first(pair + 1);
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        // One thread issues, inside an elect_one branch (a copy issued by every lane under a
-        // guard, or a diverged lane, took ~200 cycles each: more than the MMAs that it feeds).
+    if (warp < kProducers) {
+        // ------------------------------------------------------------ producers
+        // The copies of an own slot are in flight while the warp's next slot is issued (unless
+        // that one is not free yet).  TMA copies are issued by one thread inside an elect_one
+        // branch (one issued by every lane under a guard, or by a diverged lane, took ~200
+        // cycles: more than the MMAs that it feeds).
         if (p.linear) asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' copy
         const uint32_t full0 = tc::map_to_rank(smem_u32(s.full), 0), slots = smem_u32(s.slots);
-        const uint32_t qland = tc::map_to_rank(smem_u32(s.qland), rank), vfix = tc::map_to_rank(smem_u32(s.vfix), rank);
-        uint32_t it0 = 0, nq = 0, nfix = 0;
+        const uint32_t vfix = tc::map_to_rank(smem_u32(s.vfix + warp), rank);
+        uint32_t it = 0, nfix = 0;
+        int pending = -1;
         bool ok = true;
-        for (long long u = u0; u < u1 && ok;) {
-            const Range rg = range_at(p, u, u1);
-            u = rg.next;
-            if (rg.n == 0) continue;
-            if (!(ok = warp_wait(smem_u32(s.qempty), (nq & 1u) ^ 1u, p.ctx, s.abort_flag))) break;
-            ++nq;
-            if (tc::elect_one()) {
-                mbar_arrive_expect_tx_cluster(qland, Lt::kQBytes);
-                for (int c = 0; c < DP / 64; c += 2)
-                    tc::tma_load_3d_2sm(smem_u32(s.q) + c * 8192, &qmap, qland, 0, rg.rt * kPrefixRows + rank * 64, c);
+        const auto flush = [&] {
+            if (pending < 0) return;
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            mbar_arrive_cluster(full0 + pending * 8, lane == 0);
+            pending = -1;
+        };
+        // ring position `it`: slot w of a tile's K or V
+        const auto fill = [&](bool v, uint32_t w, const Tile &t, const Range &rg) {
+            if (!ok || (it & (kProducers - 1)) != (uint32_t)warp) return;
+            const uint32_t sl = it % kSlots, par = ((it / kSlots) & 1u) ^ 1u, empty = smem_u32(s.empty + sl);
+            const uint32_t dst = slots + sl * kSlotBytes;
+            if (!__all_sync(0xffffffffu, mbar_test_wait(empty, par))) {
+                flush();
+                if (!(ok = warp_wait(empty, par, p.ctx, s.abort_flag))) return;
             }
-            // row of 16 entries `lane` of tile j: below 0 (which reads as zeros) where no row
+            if (!t.shared()) {
+                if (v) gather_slot<DP, FP8, true>(p, t, rank, w, dst);
+                else gather_slot<DP, FP8, false>(p, t, rank, w, dst);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                const int before = pending;
+                pending = (int)sl;
+                if (FP8) {
+                    flush();
+                } else if (before >= 0) {
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    mbar_arrive_cluster(full0 + before * 8, lane == 0);
+                }
+                return;
+            }
+            // row of 16 entries `lane` of the tile: below 0 (which reads as zeros) where no row
             // sees them or their page does not exist
-            const auto tile_rows = [&](int j) {
-                const int key = (rg.k0 + j) * kPrefixKeys + lane * 16;
-                if (lane < 8) {
-                    int row = -kPrefixKeys;
-                    if (key < rg.vmax) {
-                        if (p.linear) {
-                            row = key;
-                        } else {
-                            const int id = __ldg(a.table + (uint32_t)key / (uint32_t)a.page);
-                            if (id >= 0 && id < a.n_pages) row = id * a.page + (int)((uint32_t)key % (uint32_t)a.page);
-                        }
-                    }
-                    s.rows[(j & 1) * 8 + lane] = row;
+            const int key = (int)t.first + lane * 16;
+            int row = -kPrefixKeys;
+            if (lane < 8 && key < rg.vmax) {
+                if (p.linear) {
+                    row = key;
+                } else {
+                    const int id = __ldg(a.table + (uint32_t)key / (uint32_t)a.page);
+                    if (id >= 0 && id < a.n_pages) row = id * a.page + (int)((uint32_t)key % (uint32_t)a.page);
                 }
-                __syncwarp();
-            };
-            tile_rows(0);
-            for (int j = 0; j <= rg.n && ok; ++j) {
-                // entries of V's tile that count; the others' weights are zero, their values
-                // (anything, in memory) are cleared where a copy brings them
-                const int end = rg.vmax - (rg.k0 + j - 1) * kPrefixKeys;
-                const bool fix = j > 0 && end < kPrefixKeys && end % p.vbox != 0;
-                bool good = true;
+            }
+            if (!v) {
+                const int g0 = rank * 4, r0 = __shfl_sync(0xffffffffu, row, g0), r1 = __shfl_sync(0xffffffffu, row, g0 + 1);
+                const int r2 = __shfl_sync(0xffffffffu, row, g0 + 2), r3 = __shfl_sync(0xffffffffu, row, g0 + 3);
                 if (tc::elect_one()) {
-                    uint32_t it = it0;
-                    if (j < rg.n) {
-                        const int *rows = s.rows + (j & 1) * 8 + rank * 4;
-                        for (int w = 0; w < Lt::kPieces && good; ++w, ++it) {
-                            const uint32_t sl = it % kSlots, dst = slots + sl * kSlotBytes, bar = full0 + sl * 8;
-                            if (!(good = mbar_wait(smem_u32(s.empty + sl), ((it / kSlots) & 1u) ^ 1u, p.ctx, s.abort_flag)))
-                                break;
-                            mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
-                            if (p.box == 64) {
-                                tc::tma_load_3d_2sm(dst, &kmap, bar, 0, rows[0], 2 * w);
-                            } else {
-                                for (int x = 0; x < 64; x += p.box) {
-                                    const int row = rows[x / 16];
-                                    tc::tma_load_3d_2sm(dst + x * 128, &kmap, bar, 0, row, 2 * w);
-                                    tc::tma_load_3d_2sm(dst + 8192 + x * 128, &kmap, bar, 0, row, 2 * w + 1);
-                                }
-                            }
-                        }
-                    }
-                    if (j > 0 && !fix) {
-                        const int *rows = s.rows + ((j - 1) & 1) * 8;
-                        for (int w = 0; w < Lt::kPieces && good; ++w, ++it) {
-                            const uint32_t sl = it % kSlots, dst = slots + sl * kSlotBytes, bar = full0 + sl * 8;
-                            if (!(good = mbar_wait(smem_u32(s.empty + sl), ((it / kSlots) & 1u) ^ 1u, p.ctx, s.abort_flag)))
-                                break;
-                            mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
-                            for (int x = 0; x < Lt::kVKeys; x += p.vbox)
-                                tc::tma_load_3d_2sm(dst + x * (Lt::kVChunks * 128), &vmap, bar, 0,
-                                                    rows[(w * Lt::kVKeys + x) / 16], rank * Lt::kVChunks);
+                    const uint32_t bar = full0 + sl * 8;
+                    mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
+                    if (p.box == 64) {
+                        tc::tma_load_3d_2sm(dst, &kmap, bar, 0, r0, 2 * w);
+                    } else {
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t d = dst + c * 8192;
+                            tc::tma_load_3d_2sm(d, &kmap, bar, 0, r0, 2 * w + c);
+                            if (p.box == 16) tc::tma_load_3d_2sm(d + 16 * 128, &kmap, bar, 0, r1, 2 * w + c);
+                            tc::tma_load_3d_2sm(d + 32 * 128, &kmap, bar, 0, r2, 2 * w + c);
+                            if (p.box == 16) tc::tma_load_3d_2sm(d + 48 * 128, &kmap, bar, 0, r3, 2 * w + c);
                         }
                     }
                 }
                 __syncwarp();
-                ok = good && !*(volatile int *)s.abort_flag;
-                ok = __all_sync(0xffffffffu, ok);
-                it0 += j < rg.n ? Lt::kPieces : 0;
-                if (fix) {
-                    const int *rows = s.rows + ((j - 1) & 1) * 8;
-                    for (int w = 0; w < Lt::kPieces && ok; ++w) {
-                        const uint32_t it = it0 + w, sl = it % kSlots, dst = slots + sl * kSlotBytes;
-                        if (!(ok = warp_wait(smem_u32(s.empty + sl), ((it / kSlots) & 1u) ^ 1u, p.ctx, s.abort_flag))) break;
-                        if (tc::elect_one()) {
-                            mbar_arrive_expect_tx_cluster(vfix, kSlotBytes);
-                            for (int x = 0; x < Lt::kVKeys; x += p.vbox)
-                                tc::tma_load_3d_2sm(dst + x * (Lt::kVChunks * 128), &vmap, vfix, 0,
-                                                    rows[(w * Lt::kVKeys + x) / 16], rank * Lt::kVChunks);
-                        }
-                        __syncwarp();
-                        if (!(ok = warp_wait(smem_u32(s.vfix), nfix & 1u, p.ctx, s.abort_flag))) break;
-                        ++nfix;
-                        // entry e of the slot, chunk c: [e / vbox][c][e % vbox][128 B]
-                        uint8_t *slot = s.slots + sl * kSlotBytes;
-                        for (int x = lane; x < (Lt::kVKeys * Lt::kVChunks) * 8; x += 32) {
-                            const int row = x >> 3, e = row / (Lt::kVChunks * p.vbox) * p.vbox + row % p.vbox;
-                            if (w * Lt::kVKeys + e >= end) reinterpret_cast<uint4 *>(slot)[x] = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        tc::fence_proxy_async_smem();
-                        __syncwarp();
-                        mbar_arrive_cluster(full0 + sl * 8, lane == 0);
-                    }
+                return;
+            }
+            // V: entries of the tile that do not count have zero weights; their values (anything, in
+            // memory) are cleared where a copy brings them
+            const int end = rg.vmax - (int)t.first - (int)w * Lt::kVKeys;  // entries of the slot that count
+            const bool fix = end > 0 && end < Lt::kVKeys && end % p.vbox != 0;
+            constexpr int kGroups = Lt::kVKeys / 16;
+            int r[kGroups];
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) r[i] = __shfl_sync(0xffffffffu, row, w * kGroups + i);
+            if (tc::elect_one()) {
+                const uint32_t bar = fix ? vfix : full0 + sl * 8;
+                mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i)
+                    if (i * 16 % p.vbox == 0)
+                        tc::tma_load_3d_2sm(dst + i * 16 * (Lt::kVChunks * 128), &vmap, bar, 0, r[i], rank * Lt::kVChunks);
+            }
+            __syncwarp();
+            if (fix) {
+                if (!(ok = warp_wait(smem_u32(s.vfix + warp), nfix & 1u, p.ctx, s.abort_flag))) return;
+                ++nfix;
+                // entry e of the slot, chunk c: [e / vbox][c][e % vbox][128 B]
+                uint4 *slot = reinterpret_cast<uint4 *>(s.slots + sl * kSlotBytes);
+                for (int y = lane; y < Lt::kVKeys * Lt::kVChunks * 8; y += 32) {
+                    const int line = y >> 3, e = line / (Lt::kVChunks * p.vbox) * p.vbox + line % p.vbox;
+                    if (e >= end) slot[y] = make_uint4(0u, 0u, 0u, 0u);
                 }
-                it0 += j > 0 ? Lt::kPieces : 0;
-                if (j + 1 < rg.n) tile_rows(j + 1);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                mbar_arrive_cluster(full0 + sl * 8, lane == 0);
+            }
+        };
+        Range rg;
+        for (Walk wk(s); ok && wk.next(p, rg);) {
+            Tiles k(p, rg);
+            Tile v = k.t;
+            for (int j = 0; j <= rg.n && ok; ++j) {
+                if (j < rg.n) {
+                    if (j > 0) {
+                        v = k.t;
+                        k.next(p, rg);
+                    }
+                    for (uint32_t w = 0; w < Lt::kPieces; ++w, ++it) fill(false, w, k.t, rg);
+                } else {
+                    v = k.t;
+                }
+                if (j > 0)
+                    for (uint32_t w = 0; w < Lt::kPieces; ++w, ++it) fill(true, w, v, rg);
             }
         }
-        if (!ok) {  // given up: copies may still be in flight to this shared memory
+        if (ok) flush();
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok) {  // given up: TMA copies may still be in flight to this shared memory
             const uint64_t t0 = global_timer_ns();
             while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
         }
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == kMmaWarp && rank == 0) {
         // ------------------------------------------------------------ MMA issuer (one thread)
         const uint64_t qdesc = tc::smem_desc(smem_u32(s.q), 1024, tc::kLayoutSw128);
         const uint64_t kdesc = tc::smem_desc(smem_u32(s.slots), 1024, tc::kLayoutSw128);
@@ -351,10 +654,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t vdesc = tc::smem_desc_lbo(smem_u32(s.slots), p.vbox * 128, 1024, tc::kLayoutSw128);
         const uint64_t pdesc = tc::smem_desc(smem_u32(s.p), 1024, tc::kLayoutSw128);
         uint32_t it0 = 0, g0 = 0, nq = 0;
-        for (long long u = u0; u < u1;) {
-            const Range rg = range_at(p, u, u1);
-            u = rg.next;
-            if (rg.n == 0) continue;
+        Range rg;
+        for (Walk wk(s); wk.next(p, rg);) {
             if (tc::elect_one()) {
                 uint32_t it = it0;
                 bool ok = mbar_wait(smem_u32(s.qready), nq & 1u, p.ctx, s.abort_flag);
@@ -409,19 +710,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             g0 += rg.n;
             ++nq;
         }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ query tile -> MMA issuer
-        if (!q_rw) {
-            const uint32_t qready0 = tc::map_to_rank(smem_u32(s.qready), 0);
-            uint32_t nq = 0;
-            for (long long u = u0; u < u1;) {
-                const Range rg = range_at(p, u, u1);
-                u = rg.next;
-                if (rg.n == 0) continue;
-                if (!warp_wait(smem_u32(s.qland), nq & 1u, p.ctx, s.abort_flag)) break;
-                mbar_arrive_cluster(qready0, lane == 0);
-                ++nq;
+    } else if (warp == kQueryWarp) {
+        // ------------------------------------------------------------ query tiles
+        const uint32_t qland = tc::map_to_rank(smem_u32(s.qland), rank), qready0 = tc::map_to_rank(smem_u32(s.qready), 0);
+        uint32_t nq = 0;
+        bool ok = true;
+        Range rg;
+        for (Walk wk(s); wk.next(p, rg); ++nq) {
+            if (!(ok = warp_wait(smem_u32(s.qempty), (nq & 1u) ^ 1u, p.ctx, s.abort_flag))) break;
+            if (tc::elect_one()) {
+                mbar_arrive_expect_tx_cluster(qland, Lt::kQBytes);
+                for (int c = 0; c < DP / 64; c += 2)
+                    tc::tma_load_3d_2sm(smem_u32(s.q) + c * 8192, &qmap, qland, 0, rg.rt * kPrefixRows + rank * 64, c);
             }
+            __syncwarp();
+            if (!(ok = warp_wait(smem_u32(s.qland), nq & 1u, p.ctx, s.abort_flag))) break;
+            if (!q_rw) mbar_arrive_cluster(qready0, lane == 0);  // else the softmax warps rewrite the tile first
+        }
+        if (!ok) {  // as above
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
         }
     } else if (warp >= kSoftWarp0) {
         // ------------------------------------------------------------ softmax, partial rows
@@ -435,27 +743,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t sempty0 = tc::map_to_rank(smem_u32(s.sempty), 0), pfull0 = tc::map_to_rank(smem_u32(s.pfull), 0);
         const uint32_t qready0 = tc::map_to_rank(smem_u32(s.qready), 0);
-        const long long n_rows = a.n_bq * a.H;
+        const int n_rows = (int)(a.n_bq * a.H);
         uint32_t g = 0, nq = 0;
-        for (long long u = u0; u < u1;) {
-            const Range rg = range_at(p, u, u1);
-            u = rg.next;
+        Range rg;
+        for (Walk wk(s); wk.next(p, rg);) {
             const size_t pi = (size_t)pair + rg.rt;
-            if (rg.n == 0) {
-                if (q4 == 0) p.ml[pi * kPrefixRows + rank * 64 + r] = make_float2(-INFINITY, 0.f);
-                continue;
-            }
-            const long long row = (long long)rg.rt * kPrefixRows + rank * 64 + r;
-            const long long t = row < n_rows ? __ldg(a.q_pos + row / a.H) : -1;
-            const int vis = (int)n_visible(t, a.m, p.n_shared);
-            // entries of a tile need a mask only past the fewest that a row of this warp sees,
-            // or where a page is missing
+            const int row = rg.rt * kPrefixRows + rank * 64 + r;
+            const int bq = row < n_rows ? row / a.H : 0, b_row = bq / a.nq;
+            const int t = row < n_rows ? __ldg(a.q_pos + bq) : -1;
+            const int vis = visible(p, t, p.n_shared);
+            // shared entries need a mask only past the fewest that a row of this warp sees, or
+            // where a page is missing
             const int vis_min = __reduce_min_sync(0xffffffffu, vis);
             bool holes = false;
-            for (int pg = rg.k0 * kPrefixKeys / a.page + lane; (long long)pg * a.page < rg.vmax; pg += 32) {
-                const int id = __ldg(a.table + pg);
-                holes |= id < 0 || id >= a.n_pages;
-            }
+            if (rg.x < rg.shared)
+                for (int pg = rg.x * kPrefixKeys / a.page + lane; (long long)pg * a.page < rg.vmax; pg += 32) {
+                    const int id = __ldg(a.table + pg);
+                    holes |= id < 0 || id >= a.n_pages;
+                }
             holes = __any_sync(0xffffffffu, holes);
             warp_wait(smem_u32(s.qland), nq & 1u, p.ctx, s.abort_flag);
             ++nq;
@@ -471,20 +776,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float rq = (1.0f / sqrtf(ss / (float)a.D + a.eps)) * a.scale * 1.4426950408889634f;
 
             float m_run = -INFINITY, l = 0.f;
+            Tiles tile(p, rg);
             for (int j = 0; j < rg.n; ++j, ++g) {
                 const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
-                const int key = (rg.k0 + j) * kPrefixKeys + hf * 64 + wg * 32;
-                const bool whole = !holes && key + 32 <= vis_min;
-                uint32_t mask = 0xffffffffu;  // which of this thread's 32 entries take part
+                if (j > 0) tile.next(p, rg);
+                const Tile &tl_ = tile.t;
+                const int off = hf * 64 + wg * 32;
+                uint32_t mask = 0xffffffffu;  // which of this thread's 32 keys take part
+                bool whole = tl_.shared() && !holes && (int)tl_.first + off + 32 <= vis_min;
                 if (!whole) {
-                    const int lim = vis - key;
-                    mask = lim >= 32 ? 0xffffffffu : (lim <= 0 ? 0u : (1u << lim) - 1u);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (lim > 16 * h) {
-                            const int id = __ldg(a.table + (uint32_t)(key + 16 * h) / (uint32_t)a.page);
-                            if (id < 0 || id >= a.n_pages) mask &= h ? 0x0000ffffu : 0xffff0000u;
-                        }
+                    mask = key_mask(p, tl_, off, t, vis, b_row);
+                    whole = __all_sync(0xffffffffu, mask == 0xffffffffu);
                 }
                 warp_wait(smem_u32(s.sfull + b), ph, p.ctx, s.abort_flag);
                 tc::fence_after_sync();
@@ -564,15 +866,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 p.ml[pi * kPrefixRows + rank * 64 + r] =
                     make_float2(m_run, (s.xsum[r] + s.xsum[64 + r]) + (s.xsum[128 + r] + s.xsum[192 + r]));
             group_sync(bar_id);
-            float4 *dst = reinterpret_cast<float4 *>(p.part) + ((pi * 2 + rank) * (DP / 16) * 128 + tl) * 2;
+            float4 *dst = reinterpret_cast<float4 *>(p.part) + (pi * 2 + rank) * (DP / 8) * 128 + tl;
             for (int c = wg * (DP / 4); c < (wg + 1) * (DP / 4); c += 32) {
                 float v[32];
                 tc::tmem_ld32(tmem + lane_base + c, v);
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    dst[(size_t)(c / 8 + i / 2) * 256 + (i & 1)] =
-                        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    dst[(size_t)(c / 4 + i) * 128] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
             tc::fence_before_sync();  // O is read before the next range's first P.V (through pfull)
         }
@@ -581,7 +882,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_sync();  // no arrival of the other CTA is outstanding
-    if (warp == 2) {
+    if (warp == kQueryWarp) {
         tc::fence_after_sync();
         tc::tmem_dealloc_2sm(tmem, 512);
     }
@@ -613,7 +914,7 @@ __global__ void __launch_bounds__(256)
 // kind::f16 instruction descriptor: bf16 operands, fp32 accumulate, M = 128
 constexpr uint32_t idesc(int n, bool b_mn) { return tc::idesc_f16(n, true) | (b_mn ? (1u << 16) : 0u); }
 
-template <int DP>
+template <int DP, bool FP8>
 int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     Params p = {};
     p.a = x.a;
@@ -622,12 +923,13 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     p.linear = x.linear ? 1 : 0;
     p.part = x.part;
     p.ml = x.ml;
+    p.first = x.first;
     p.ctx = ctx;
     p.idesc_qk = idesc(kPrefixKeys, false);
     p.idesc_pv = idesc(Layout<DP>::kPvN, true);
     p.box = x.linear || x.a.page % 64 == 0 ? 64 : (x.a.page % 32 == 0 ? 32 : 16);
     p.vbox = std::min(p.box, Layout<DP>::kVKeys);
-    auto kern = attend_prefix_kernel<DP>;
+    auto kern = attend_prefix_kernel<DP, FP8>;
     constexpr size_t smem = smem_bytes<DP>();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return CSA_ERR_CUDA;
@@ -659,11 +961,10 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
 
 }  // namespace
 
-PrefixPlan prefix_plan(long long rows, long long n_shared) {
+PrefixPlan prefix_plan(long long rows) {
     PrefixPlan pl;
     pl.row_tiles = (int)((rows + kPrefixRows - 1) / kPrefixRows);
-    pl.key_tiles = (int)((n_shared + kPrefixKeys - 1) / kPrefixKeys);
-    pl.pairs = (int)std::min<long long>(std::max(num_sms() / 2, 1), pl.units());
+    pl.pairs = std::max(num_sms() / 2, 1);
     return pl;
 }
 
@@ -676,10 +977,11 @@ int launch_prefix_rows(const uint8_t *codes, const uint8_t *exps, const int *tab
 }
 
 int launch_attend_prefix(const PrefixArgs &p, const DevCtx &ctx, cudaStream_t st) {
+    const bool fp8 = p.a.kv8 != nullptr;
     switch (prefix_dims(p.a.D)) {
-        case 128: return launch_d<128>(p, ctx, st);
-        case 256: return launch_d<256>(p, ctx, st);
-        case 512: return launch_d<512>(p, ctx, st);
+        case 128: return fp8 ? launch_d<128, true>(p, ctx, st) : launch_d<128, false>(p, ctx, st);
+        case 256: return fp8 ? launch_d<256, true>(p, ctx, st) : launch_d<256, false>(p, ctx, st);
+        case 512: return fp8 ? launch_d<512, true>(p, ctx, st) : launch_d<512, false>(p, ctx, st);
         default: return CSA_ERR_UNSUPPORTED;
     }
 }

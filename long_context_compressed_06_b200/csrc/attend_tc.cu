@@ -171,9 +171,8 @@ struct Keys {
 template <bool PAGED>
 CSA_DEVINL Keys query_keys(const AttendArgs &a, long long t) {
     Keys k;
-    if constexpr (PAGED) {  // the visible entries from e_first on, then the ring rows t-W+1..t
-        const long long v = n_visible(t, a.m, a.N) - a.e_first;
-        k.nsel = v > 0 ? v : 0;
+    if constexpr (PAGED) {  // the visible entries, then the ring rows t-W+1..t
+        k.nsel = n_visible(t, a.m, a.N);
         k.nsel4 = (k.nsel + 3) & ~3LL;
         k.u0 = t - a.W + 1 > 0 ? t - a.W + 1 : 0;
         k.nwin = t >= k.u0 ? t - k.u0 + 1 : 0;
@@ -200,7 +199,7 @@ CSA_DEVINL int key_index_raw(const AttendArgs &a, const Keys &ks, long long bq, 
     if (e >= e_end) e = e_end - 1;
     if constexpr (PAGED)
         return e >= 0 && e < ks.nsel
-                   ? __ldg(a.table + bq / a.nq * a.max_pages + (uint32_t)(a.e_first + e) / (uint32_t)a.page)
+                   ? __ldg(a.table + bq / a.nq * a.max_pages + (uint32_t)e / (uint32_t)a.page)
                    : -1;
     return (!a.dense && e >= 0 && e < ks.nsel) ? __ldg(a.idx + bq * a.k + e) : 0;
 }
@@ -218,7 +217,7 @@ CSA_DEVINL size_t key_row_index(const AttendArgs &a, const Keys &ks, long long b
     valid = e < e_end;
     if constexpr (PAGED) {
         if (e < ks.nsel4) {
-            const uint32_t j = (uint32_t)(a.e_first + e);
+            const uint32_t j = (uint32_t)e;
             valid = valid && e < ks.nsel && jraw >= 0 && jraw < a.n_pages;
             return valid ? (size_t)jraw * a.page + j % (uint32_t)a.page : 0;
         }
@@ -929,8 +928,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (PAGED && !direct) {
-                    // fp32, not divided: the merge weighs the partials of this kernel and of
-                    // the shared entries' kernel alike.  Warp-store order (part_perm) or rows.
+                    // fp32, not divided (the paged merge rounds once, to the output).
+                    // Warp-store order (part_perm) or rows.
                     float4 *dst = reinterpret_cast<float4 *>(a.part_f + (size_t)orow * a.H * D);
                     int step = 1;
                     if (a.part_perm) {
@@ -964,9 +963,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             jt += it.ntiles;
         }
     }
-    // paged: the merge waits for this grid only, so this grid ends after the
-    // shared entries' kernel before it (a no-op for an ordinary launch)
-    if constexpr (PAGED) asm volatile("griddepcontrol.wait;" ::: "memory");
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 0) {

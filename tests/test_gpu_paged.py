@@ -346,6 +346,14 @@ CASES = {
     "none_seen": dict(ts=[[2], [1]], H=8, D=64, m=4, page=16, n_shared=64, Wn=16),
     "all_empty": dict(ts=[[-1], [-1]], H=8, D=64, m=4, page=16, n_shared=64, Wn=16),
     "row_tiles": dict(ts=[[900 + 3 * i] for i in range(37)], H=8, D=64, m=4, page=16, n_shared=208, Wn=16),
+    # several row tiles per pair of SMs, shared and own tiles in turn
+    "many_ranges_64": dict(ts=[[790 + 7 * i] for i in range(150)], H=64, D=64, m=2, page=16, n_shared=384, Wn=40),
+    "many_ranges_128": dict(ts=[[790 + 7 * (i % 50)] for i in range(250)], H=40, D=128, m=2, page=32, n_shared=352, Wn=16),
+    "many_ranges_256": dict(ts=[[700 + 9 * i] for i in range(80)], H=128, D=256, m=4, page=64, n_shared=128, Wn=30),
+    "many_ranges_512": dict(ts=[[700 + 9 * i] for i in range(80)], H=128, D=512, m=4, page=16, n_shared=160, Wn=30),
+    "many_ranges_fp8": dict(ts=[[700 + 9 * i] for i in range(80)], H=128, D=512, m=4, page=64, n_shared=128, Wn=30,
+                            fp8=True),
+    "long_own": dict(ts=[[1200], [9000], [300]], H=128, D=128, m=2, page=64, n_shared=128, Wn=128),
     "many_units": dict(ts=[[30000 + 100 * i] for i in range(3)], H=4, D=64, m=2, page=64, n_shared=14976, Wn=16),
     "many_units_128": dict(ts=[[25000 + 100 * i] for i in range(5)], H=64, D=128, m=8, page=16, n_shared=3056, Wn=16),
     "pages_missing": dict(ts=[[700], [690], [650]], H=16, D=128, m=2, page=16, n_shared=304, Wn=8,
