@@ -369,12 +369,6 @@ CSA_DEVINL Item work_item(const AttTcParams &p, long long wi) {
     return it;
 }
 
-// 16-byte asynchronous copy; src == nullptr writes zeros (nothing is read)
-CSA_DEVINL void cp_async16_or_zero(uint32_t dst, const void *src, const void *any) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src ? src : any), "r"(src ? 16 : 0)
-                 : "memory");
-}
-
 template <int D, bool FP8, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap,

@@ -62,6 +62,12 @@ CSA_DEVINL uint4 ldg_stream(const void *p) {
 
 CSA_DEVINL uint4 ldg16(const void *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
 
+// 16-byte asynchronous copy; src == nullptr writes zeros (nothing is read)
+CSA_DEVINL void cp_async16_or_zero(uint32_t dst, const void *src, const void *any) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src ? src : any), "r"(src ? 16 : 0)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- misc
 CSA_DEVINL long long n_visible(long long t, int m, long long N) {
     long long v = (t + 1) / m;
