@@ -470,8 +470,8 @@ int csa_paged_write_fp8kv(const uint16_t *rows, const long long *slots, long lon
  * Requirements: those of hca_attend on the shared arguments; page % 16 == 0,
  * n_pages >= 1, max_pages >= 1, 0 <= n_shared <= max_pages * page with n_shared
  * % page == 0, ring_rows >= W + nq - 1 (the rings hold the windows of nq
- * consecutive queries) (CSA_ERR_INVALID); n_pages * page and max_pages * page
- * < 2^31 (CSA_ERR_UNSUPPORTED).  Workspace: csa_attend_paged_workspace_bytes,
+ * consecutive queries) (CSA_ERR_INVALID); n_pages * page, max_pages * page and
+ * batch * ring_rows < 2^31 (CSA_ERR_UNSUPPORTED).  Workspace: csa_attend_paged_workspace_bytes,
  * 16-byte aligned, with the same arguments (fp8 = 0).  Calls that may overlap
  * on the device, replays of captured graphs among them, need workspaces of
  * their own.

@@ -411,7 +411,8 @@ static int validate_paged(const csa::PagedArgs &a) {
     const long long cap = (long long)a.max_pages * a.page;
     if (a.n_shared < 0 || a.n_shared > cap || a.n_shared % a.page != 0) return CSA_ERR_INVALID;
     if ((long long)a.ring_rows < (long long)a.W + a.nq - 1) return CSA_ERR_INVALID;
-    if (a.n_pages > 0x7fffffffLL / a.page || cap > 0x7fffffffLL) return CSA_ERR_UNSUPPORTED;
+    if (a.n_pages > 0x7fffffffLL / a.page || cap > 0x7fffffffLL || (long long)a.batch * a.ring_rows > 0x7fffffffLL)
+        return CSA_ERR_UNSUPPORTED;
     if (a.H > 128 || !(a.D == 64 || a.D == 128 || a.D == 256 || a.D == 512)) return CSA_ERR_UNSUPPORTED;
     return CSA_OK;
 }

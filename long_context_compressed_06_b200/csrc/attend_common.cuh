@@ -74,14 +74,20 @@ int launch_attend_combine(const AttendArgs &a, cudaStream_t st);
 struct PrefixPlan {
     int row_tiles, pairs;
     CSA_HOSTDEV int partials() const { return pairs + row_tiles; }
-    // pairs that `units` units are dealt to: pair p owns [units p / active, units (p + 1) / active)
-    CSA_HOSTDEV int active(long long units) const {
-        const long long most = (units + kMinUnits - 1) / kMinUnits;
-        return (int)(most < 1 ? 1 : (most < pairs ? most : pairs));
+    // pairs that `units` units are dealt to
+    CSA_HOSTDEV int active(int units) const {
+        const int most = (units + kMinUnits - 1) / kMinUnits;
+        return most < 1 ? 1 : (most < pairs ? most : pairs);
+    }
+    // pair p owns units [begin(p), begin(p + 1)): units / active of them, the first pairs one more
+    CSA_HOSTDEV int begin(int p, int units) const {
+        const int n = active(units), more = units % n;
+        return p >= n ? units : units / n * p + (p < more ? p : more);
     }
     // the pair that owns unit u
-    CSA_HOSTDEV int pair_of(long long u, long long units) const {
-        return (int)(((u + 1) * active(units) - 1) / units);
+    CSA_HOSTDEV int pair_of(int u, int units) const {
+        const int n = active(units), each = units / n, more = units % n;
+        return u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each;
     }
     static constexpr int kMinUnits = 1;
 };
@@ -97,7 +103,7 @@ struct PrefixArgs {
     bool linear;
     float *part;           // [partials][128][DP], see above
     float2 *ml;            // [partials][128]
-    long long *first;      // [row_tiles + 1] first unit of every row tile, and the units of all (out)
+    int *first;            // [row_tiles + 1] first unit of every row tile, and the units of all (out)
 };
 
 PrefixPlan prefix_plan(long long rows);

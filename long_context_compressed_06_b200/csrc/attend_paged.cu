@@ -27,7 +27,7 @@ struct MergeArgs {
     PrefixPlan plan;  // pairs > 0: the partials of attend_prefix.cu, else the splits of attend_tc.cu
     const float *part;
     const float2 *ml;
-    const long long *first;
+    const int *first;
 };
 
 // A warp: 4 rows x 64 dims, a thread 8 dims of one row: two 16-byte pieces of each partial.
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Merge
     if (!active) {
     } else if (g.plan.pairs > 0) {
         const int DP = prefix_dims(a.D), rt = (int)(row / kPrefixRows), rr = (int)(row % kPrefixRows);
-        const long long u0 = g.first[rt], u1 = g.first[rt + 1], units = g.first[g.plan.row_tiles];
+        const int u0 = g.first[rt], u1 = g.first[rt + 1], units = g.first[g.plan.row_tiles];
         if (u1 > u0) {
             const int p0 = g.plan.pair_of(u0, units);
             np = g.plan.pair_of(u1 - 1, units) - p0 + 1;
@@ -139,7 +139,7 @@ PagedPlan paged_plan(long long n_bq, int H, int D, int page, int max_pages, long
         if (fp8) pl.keys = take(at, (size_t)n_shared * D * sizeof(uint16_t));
         pl.part = take(at, (size_t)pl.prefix.partials() * kPrefixRows * prefix_dims(D) * sizeof(float));
         pl.ml = take(at, (size_t)pl.prefix.partials() * kPrefixRows * sizeof(float2));
-        pl.first = take(at, (size_t)(pl.prefix.row_tiles + 1) * sizeof(long long));
+        pl.first = take(at, (size_t)(pl.prefix.row_tiles + 1) * sizeof(int));
     } else {
         attend_tc_plan(n_bq, H, cap + W, &pl.splits, &pl.keys_per_split);
         if (pl.splits > 1) {
@@ -178,6 +178,9 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     g.a = a;
     int rc;
     if (pl.prefix.pairs > 0) {
+        // the units are counted in 32 bits
+        const long long requests = 1 + kPrefixRows / a.H, own = (a.N - p.n_shared + a.win_rows) / kPrefixKeys + 2;
+        if ((p.n_shared / kPrefixKeys + 1 + requests * own) > 0x7fffffffLL / pl.prefix.row_tiles) return CSA_ERR_UNSUPPORTED;
         PrefixArgs x = {};
         x.a = a;
         x.plan = g.plan = pl.prefix;
@@ -192,7 +195,7 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
         }
         g.part = x.part = reinterpret_cast<float *>(w + pl.part);
         g.ml = x.ml = reinterpret_cast<float2 *>(w + pl.ml);
-        g.first = x.first = reinterpret_cast<long long *>(w + pl.first);
+        g.first = x.first = reinterpret_cast<int *>(w + pl.first);
         rc = launch_attend_prefix(x, ctx, st);
         if (rc != CSA_OK) return rc;
     } else {

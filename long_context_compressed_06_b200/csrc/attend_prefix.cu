@@ -28,18 +28,20 @@
 // Warps: 0 and 1 producers of K, 2 and 3 of V, 4 and 5 MMA issuers of Q K^T and of
 // P V on the pair's leader (one thread for both was busy for longer than the
 // tensor cores: a satisfied barrier wait takes ~140 cycles, an MMA ~20), 6
-// tensor memory and the query tiles, 7 the planner, 8..15 softmax (four threads
-// per row: lane half x 32-column half).
+// tensor memory and the query tiles, 7 the planner, 8..15 softmax: two groups of
+// four warps take the tiles in turn, two threads per row (64 keys each), so that
+// the waits and exchanges of one tile overlap the exponentials of the next (all
+// eight warps on one tile took ~2500 cycles a tile, most of it latency).
 // The planner walks the pair's tiles a few ahead of everyone, describes each in
 // shared memory (struct Tile) and brings own rows into L2 (the producers are one
 // tile ahead at D = 512).  Each role's code is kept small on purpose: unrolled
-// loops that run once per row tile cost more in instruction misses than in work
-// (14K cycles per row tile, measured, for a prologue of ~3K instructions).
+// loops that run once per row tile cost more in instruction misses than in work.
 // K and V have a ring of 16 KiB slots each; every tile passes through both, and
-// two producer warps take a ring's positions in turn, whatever they hold: shared
-// entries by TMA, own keys (rows of any page and of the window rings) by 16-byte
-// asynchronous copies, FP8 rows expanded on the way.  (A slot's phase bit tells
-// its use from the one before only: whoever waits on a ring passes every use.)
+// two producer warps take a ring's positions in turn.  Rows arrive by TMA,
+// entries in boxes that never cross a page, window rows 16 at a time in the
+// order of the ring; FP8 own rows are expanded by the producers.  (A slot's
+// phase bit tells its use from the one before only: whoever waits on a ring
+// passes every use.)
 //
 // The tiles of all row tiles ("units") are counted on the device from the
 // positions and dealt to the pairs in balanced contiguous ranges.
@@ -58,11 +60,12 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kProducers = 4, kQkWarp = 4, kPvWarp = 5, kQueryWarp = 6, kPlanWarp = 7, kSoftWarp0 = 8, kSoftWarps = 8;
 constexpr int kSlots = 4;  // of each ring
-constexpr int kDescs = 8;  // tiles described ahead
+constexpr int kDescs = 6;  // tiles described ahead
 constexpr uint32_t kSlotBytes = 16384;  // K: 64 keys x 128 dims, V: 16384 / DP keys x DP / 2 dims
 constexpr uint32_t kPBytes = 16384;     // 64 rows x 128 keys, bf16
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kSCols = 256;        // first column of the S buffers (64 columns each)
+constexpr int kSBufs = 4;
 
 template <int DP>
 struct Layout {
@@ -79,7 +82,7 @@ struct Params {
     PrefixPlan plan;
     int n_shared;
     int linear;
-    long long *first; // [row_tiles + 1] first unit of a row tile; the units of all
+    int *first;       // [row_tiles + 1] first unit of a row tile; the units of all
     int box;          // entries that one copy brings at most (none crosses a page): 16, 32 or 64
     int vbox;         // those of a V copy: at most one slot's
     float *part;
@@ -89,26 +92,29 @@ struct Params {
 };
 
 // One tile of 128 keys, as the planner describes it.
-enum : int { kShared = 1, kFirst = 2, kLast = 4, kEnd = 8, kMissingShift = 8 };
+enum : int { kShared = 1, kFirst = 2, kLast = 4, kEnd = 8, kMixed = 16, kMissingShift = 8, kRingShift = 16 };
 struct __align__(16) Tile {
-    int flags;    // kShared: entries of all requests, else own keys; kFirst / kLast of a pair's part of a
-                  // row tile; kEnd: no tile.  Bit kMissingShift + i: entries 16 i .. 16 i + 15 have no page
-    int rt;       // row tile
-    int b;        // request (own keys)
-    int e_first;  // entry index of key 0 (own keys: may pass the last entry)
-    int ent;      // keys [0, ent) are entries that some row sees
-    int cnt;      // keys [ent, cnt) are window rows, of position
-    int wpos;     //   wpos + key
-    int ring;     // their row in the request's ring: (ring + key - ent) % win_rows
-    int rows[8];  // pool row (linear: row of the copy) of entry 16 i; < 0: none, reads as zeros
+    int flags;         // kShared: entries of all requests, else own keys of request b; kFirst / kLast of a pair's
+                       // part of a row tile; kEnd: no tile; kMixed: window rows among the keys.  Of keys 16 i ..
+                       // 16 i + 15, bit kMissingShift + i: entries without a page, kRingShift + i: window rows
+    int rt;            // row tile
+    int b;
+    int e_first;       // entry index of key 0
+    int ent;           // keys [0, ent) are entries that some row sees
+    int r_first;       // ring row of key 0 (kMixed: keys from -r_first on, where that is positive)
+    int rows[8];       // row of key 16 i in the pool, the rings or (linear) the copy; < 0: none, reads as zeros
+    uint32_t zero[4];  // keys that a copy brings (FP8 own keys: any) and no row takes: cleared in V
+    int pad[2];
 };
 
 struct Smem {
     uint8_t *q, *slots, *p;  // slots: K's ring, then V's; so are their barriers
-    uint64_t *full, *empty, *sfull, *sempty, *pfull, *pvdone, *qland, *qready, *qempty, *vfix, *dfull, *dempty;
+    uint64_t *full, *empty, *sfull, *sempty, *pfull, *pvdone, *qland, *qready, *qempty, *vfix, *dfull, *dempty, *mdec, *rbar, *xbar;
     Tile *desc;      // [kDescs]
-    uint16_t *xmax;  // [2][4][64] the upper halves of the row maxima of a tile's four threads per row
-    float *xsum;     // [4][64], the same memory
+    // Per 32 rows, [2][128] floats: sums of a row's four threads [4][32] before and after its tiles;
+    // during them its running maximum after tile g at mref[(g & 1) * 32 + row], and the upper halves of
+    // a tile's maxima, xmax[(group * 2 + half) * 32 + row] (uint16, after the 64 floats of mref)
+    float *xch;
     uint32_t *tmem_slot;
     int *abort_flag;
 };
@@ -119,19 +125,21 @@ CSA_DEVINL Smem carve(uint8_t *raw) {
     s.q = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     s.slots = s.q + Layout<DP>::kQBytes;
     s.p = s.slots + 2 * kSlots * kSlotBytes;
-    s.xsum = reinterpret_cast<float *>(s.p + 2 * kPBytes);
-    s.xmax = reinterpret_cast<uint16_t *>(s.xsum);
-    s.desc = reinterpret_cast<Tile *>(s.xsum + 256);
+    s.xch = reinterpret_cast<float *>(s.p + 2 * kPBytes);
+    s.desc = reinterpret_cast<Tile *>(s.xch + 256);
     uint64_t *bars = reinterpret_cast<uint64_t *>(s.desc + kDescs);
     s.full = bars;
     s.empty = s.full + 2 * kSlots;
     s.dfull = s.empty + 2 * kSlots;
     s.dempty = s.dfull + kDescs;
     s.sfull = s.dempty + kDescs;
-    s.sempty = s.sfull + 2;
-    s.pfull = s.sempty + 2;
+    s.sempty = s.sfull + kSBufs;
+    s.pfull = s.sempty + kSBufs;
     s.pvdone = s.pfull + 2;
-    s.qland = s.pvdone + 2;
+    s.mdec = s.pvdone + 2;
+    s.rbar = s.mdec + 2;  // [2 x 32 rows]
+    s.xbar = s.rbar + 2;  // [2 groups][2 x 32 rows]
+    s.qland = s.xbar + 4;
     s.qready = s.qland + 1;
     s.qempty = s.qready + 1;
     s.vfix = s.qempty + 1;  // [2]
@@ -143,7 +151,7 @@ CSA_DEVINL Smem carve(uint8_t *raw) {
 template <int DP>
 constexpr size_t smem_bytes() {
     return 1024 + Layout<DP>::kQBytes + 2 * kSlots * kSlotBytes + 2 * kPBytes + 1024 + kDescs * sizeof(Tile) +
-           (4 * kSlots + 2 * kDescs + 13) * 8 + 8;
+           (4 * kSlots + 2 * kDescs + 2 * kSBufs + 17) * 8 + 8;
 }
 static_assert(smem_bytes<512>() <= 227 * 1024, "shared memory of one CTA");
 
@@ -156,26 +164,24 @@ CSA_DEVINL int visible(const Params &p, int t, int cap) {
 }
 
 // The own keys of queries [q0, q1] of one request: entries n_shared..n_shared + n_own - 1,
-// then the window rows of positions u0..u0 + (total - n_own) - 1.
+// then, from a multiple of 16 on, the rows of its ring in order.
 struct Own {
-    int n_own, u0;
-    long long total;
-    CSA_DEVINL int tiles() const { return (int)((total + kPrefixKeys - 1) / kPrefixKeys); }
+    int n_own;
+    uint32_t total;  // with the entries padded to 16 and every row of the ring (no live query: 0)
+    CSA_DEVINL uint32_t ring0() const { return ((uint32_t)n_own + 15u) & ~15u; }  // key of ring row 0
+    CSA_DEVINL int tiles() const { return (int)((total + (uint32_t)kPrefixKeys - 1u) / (uint32_t)kPrefixKeys); }
 };
 
 CSA_DEVINL Own own_keys(const Params &p, int q0, int q1) {
-    int vis = 0, u0 = 0x7fffffff, u1 = -1;
+    int vis = 0, t1 = -1;
     for (int q = q0; q <= q1; ++q) {
         const int t = __ldg(p.a.q_pos + q);
-        if (t < 0) continue;
         vis = std::max(vis, visible(p, t, (int)p.a.N));
-        u0 = std::min(u0, std::max(0, t - p.a.W + 1));
-        u1 = std::max(u1, t);
+        t1 = std::max(t1, t);
     }
     Own o;
     o.n_own = std::max(0, vis - p.n_shared);
-    o.u0 = u0;
-    o.total = o.n_own + (u1 >= 0 ? (long long)u1 - u0 + 1 : 0);
+    o.total = t1 < 0 ? 0u : o.ring0() + (uint32_t)p.a.win_rows;
     return o;
 }
 
@@ -214,8 +220,7 @@ CSA_DEVINL int count_units(const Params &p, int rt, int subs) {
 
 // A pair's units: `left` of them from number x of row tile rt on.
 struct Units {
-    long long left;
-    int rt, x;
+    int left, rt, x;
 };
 
 // By one warp; `write`: also where every row tile begins.
@@ -225,8 +230,7 @@ CSA_DEVINL Units deal_units(const Params &p, int pair, bool write) {
     int subs = 1;
     while (subs < 32 && subs * p.a.H * p.a.nq < kPrefixRows) subs *= 2;
     const int step = 32 / subs;  // row tiles per pass
-    long long total = 0;
-    int n = 0, inc = 0;
+    int total = 0, n = 0, inc = 0;
     const auto pass = [&](int r0) {  // n: units of row tile r0 + lane / subs; inc: of those up to it in this pass
         n = count_units(p, r0 + lane / subs, subs);
         inc = n;
@@ -242,19 +246,18 @@ CSA_DEVINL Units deal_units(const Params &p, int pair, bool write) {
         total += __shfl_sync(0xffffffffu, inc, 31);
     }
     if (write && lane == 0) p.first[RT] = total;
-    const int P = p.plan.active(total);
     Units u = {0, 0, 0};
-    const long long u0 = pair < P ? total * pair / P : 0;
-    u.left = pair < P ? total * (pair + 1) / P - u0 : 0;
+    const int u0 = p.plan.begin(pair, total);
+    u.left = p.plan.begin(pair + 1, total) - u0;
     if (u.left == 0) return u;
-    long long base = 0;
+    int base = 0;
     for (int r0 = 0; r0 < RT; r0 += step) {
         if (RT > step) pass(r0);
         const uint32_t here = __ballot_sync(0xffffffffu, base + inc - n <= u0 && u0 < base + inc);
         if (here) {
             const int l = __ffs(here) - 1;
             u.rt = r0 + l / subs;
-            u.x = (int)(u0 - base) - __shfl_sync(0xffffffffu, inc - n, l);
+            u.x = u0 - base - __shfl_sync(0xffffffffu, inc - n, l);
             break;
         }
         base += __shfl_sync(0xffffffffu, inc, 31);
@@ -266,18 +269,12 @@ CSA_DEVINL bool warp_wait(uint32_t bar, uint32_t parity, const DevCtx &ctx, vola
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctx, abort));
 }
 
-CSA_DEVINL void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-
-// ... and whether `v` holds for all of the barrier's threads
-CSA_DEVINL bool group_all(int id, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-        "bar.red.and.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"((int)v)
-        : "memory");
-    return r != 0;
+// Where a few warps meet (an mbarrier of one arrival per warp, `uses` its phases so far): a named
+// barrier is cheaper, but would hang for good if a warp had given up a wait and left.
+CSA_DEVINL bool warps_meet(uint32_t bar, uint32_t &uses, const DevCtx &ctx, volatile int *abort) {
+    __syncwarp();
+    mbar_arrive(bar, (threadIdx.x & 31) == 0);
+    return warp_wait(bar, uses++ & 1u, ctx, abort);
 }
 
 // The tile's query rows as they landed: this thread's quarter of row r (units
@@ -336,102 +333,91 @@ CSA_DEVINL void query_rewrite(const AttendArgs &a, uint8_t *q, int r, int q4, in
 // the first n of 32 bits
 CSA_DEVINL uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
 
-// Which of keys off..off + 31 of a tile the row of a query at t takes (of
-// request b_row, seeing vis entries).
-CSA_DEVINL uint32_t key_mask(const Tile &d, int off, int t, int W, int vis, int b_row) {
-    if (!(d.flags & kShared) && b_row != d.b) return 0u;
-    uint32_t mask = low_bits(std::min(vis - d.e_first, d.ent) - off);
-    if (d.flags >> kMissingShift) {
-        const int miss = d.flags >> (kMissingShift + off / 16);
-        mask &= ~((miss & 1 ? 0x0000ffffu : 0u) | (miss & 2 ? 0xffff0000u : 0u));
-    }
-    if (d.cnt > d.ent && t >= 0) {  // window rows t-W+1..t
-        const int lo = std::max(std::max(0, t - W + 1) - d.wpos, d.ent), hi = std::min(t - d.wpos + 1, d.cnt);
-        mask |= low_bits(hi - off) & ~low_bits(lo - off);
+// bits x..y (either may lie outside)
+CSA_DEVINL uint32_t bits_between(int x, int y) { return low_bits(y + 1) & ~low_bits(x); }
+
+// The row of a query at t, of request b, that sees vis entries and the ring rows
+// w0..w1 (w0 > w1: ..w1 and w0..; none: w1 = -1 and w0 past the ring).
+struct Row {
+    int t, vis, b, w0, w1;
+};
+
+// Which of keys off..off + 31 of a tile it takes.
+CSA_DEVINL uint32_t key_mask(const Tile &d, int off, const Row &r, int win_rows) {
+    const int flags = d.flags;
+    if (!(flags & kShared) && r.b != d.b) return 0u;
+    uint32_t mask = low_bits(std::min(r.vis - d.e_first, d.ent) - off);
+    const int miss = flags >> (kMissingShift + off / 16);
+    mask &= ~((miss & 1 ? 0x0000ffffu : 0u) | (miss & 2 ? 0xffff0000u : 0u));
+    if (flags & kMixed) {
+        const int k0 = d.r_first + off;  // ring row of key `off`
+        mask |= r.w0 <= r.w1 ? bits_between(r.w0 - k0, r.w1 - k0)
+                             : bits_between(-k0, r.w1 - k0) | bits_between(r.w0 - k0, win_rows - 1 - k0);
     }
     return mask;
 }
 
-// One slot of an own tile, by one warp: K (V = false): the CTA's 64 keys x dims
-// [128 w, 128 w + 128), V: keys [w kVKeys, ..) x the CTA's half of the dims, in
-// the layouts that the TMA copies of shared tiles make.  Keys that do not exist
-// are zeros (no weight is on them, and nothing is known of their memory).
-template <int DP, bool FP8, bool V>
-CSA_DEVINL void gather_slot(const Params &p, const Tile &d, int rank, int w, uint32_t dst) {
+// One slot of an own tile over FP8 rows, by one warp: K (V = false): the CTA's 64
+// keys x dims [128 w, 128 w + 128), V: keys [w kVKeys, ..) x the CTA's half of
+// the dims, in the layouts that the TMA copies make.  Keys that no row takes are
+// zeros (nothing is known of their memory).
+template <int DP, bool V>
+CSA_DEVINL void expand_slot(const Params &p, const Tile &d, int rank, int w, uint32_t dst, int vbox) {
     using Lt = Layout<DP>;
     const AttendArgs &a = p.a;
-    constexpr int kKeys = V ? Lt::kVKeys : 64, kUnits = V ? Lt::kVChunks * 8 : 16;  // 16-byte units (8 dims) of a key
-    constexpr int kPer = FP8 ? 2 : 1;                       // units per thread and step (16 codes)
-    constexpr int kStep = 32 * kPer / kUnits;               // keys per step of the warp
-    const int lane = threadIdx.x & 31, u = lane % (kUnits / kPer) * kPer;
+    constexpr int kKeys = V ? Lt::kVKeys : 64, kUnits = V ? Lt::kVChunks * 4 : 8;  // 16 codes of a key each
+    constexpr int kStep = 32 / kUnits, kBatch = 4;                                 // keys per step of the warp; steps in flight
+    const int lane = threadIdx.x & 31, u = lane % kUnits * 2;
     const int key0 = V ? w * kKeys : rank * 64, dim = (V ? rank * (DP / 2) : w * 128) + u * 8;
-    const int vsh = 31 - __clz(p.vbox);
-    const long long ring0 = (long long)d.b * a.win_rows;
-    const int rows = (int)a.win_rows;
-    // row of key k, ~row in the rings, or none
-    constexpr long long kNone = 0x7fffffffffffffffLL;
-    const auto row_of = [&](int k) -> long long {
-        if (k < d.ent) {
-            const int r = d.rows[k >> 4];
-            return r < 0 ? kNone : (long long)(r + (k & 15));
-        }
-        if (k >= d.cnt) return kNone;
-        int r = d.ring + (k - d.ent);
-        if (r >= rows) r = r - rows < rows ? r - rows : r % rows;
-        return ~(ring0 + r);
-    };
-    // shared-memory address of unit x of the slot's key k: V as [k / vbox][64-dim chunk][k % vbox]
-    // [128 B], K as [chunk][k][128 B], 128-byte swizzle
+    const int vsh = 31 - __clz(vbox);
+    // shared-memory address of 16-byte unit x (8 dims) of the slot's key k: V as [k / vbox]
+    // [64-dim chunk][k % vbox][128 B], K as [chunk][k][128 B], 128-byte swizzle
     const auto at = [&](int k, int x) {
-        const uint32_t line = V ? ((uint32_t)((k >> vsh) * Lt::kVChunks + (x >> 3)) << vsh) + (k & (p.vbox - 1))
+        const uint32_t line = V ? ((uint32_t)((k >> vsh) * Lt::kVChunks + (x >> 3)) << vsh) + (k & (vbox - 1))
                                 : (uint32_t)((x >> 3) * 64 + k);
         return dst + line * 128 + (((x & 7) ^ (k & 7)) << 4);
     };
-    if constexpr (FP8) {
-        constexpr int kBatch = 4;
 #pragma unroll 1
-        for (int k0 = lane / (kUnits / 2); k0 < kKeys; k0 += kBatch * kStep) {
-            uint4 v[kBatch];
-            uint32_t e[kBatch];
+    for (int k0 = lane / kUnits; k0 < kKeys; k0 += kBatch * kStep) {
+        uint4 v[kBatch];
+        uint32_t e[kBatch];
 #pragma unroll
-            for (int c = 0; c < kBatch; ++c) {
-                const long long r = row_of(key0 + k0 + c * kStep);
-                v[c] = make_uint4(0u, 0u, 0u, 0u);
-                e[c] = 0u;
-                if (r != kNone) {
-                    const size_t ri = (size_t)(r < 0 ? ~r : r);
-                    v[c] = ldg16((r < 0 ? a.win8 : a.kv8) + ri * a.D + dim);
-                    e[c] = __ldg((r < 0 ? a.win8e : a.kv8e) + ri * (a.D / 128) + dim / 128);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < kBatch; ++c) {
-                const int k = k0 + c * kStep;
-                const uint4 lo = e4m3x8_bf16x8(make_uint2(v[c].x, v[c].y), e[c]);
-                const uint4 hi = e4m3x8_bf16x8(make_uint2(v[c].z, v[c].w), e[c]);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(k, u)), "r"(lo.x), "r"(lo.y), "r"(lo.z),
-                             "r"(lo.w)
-                             : "memory");
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(k, u + 1)), "r"(hi.x), "r"(hi.y), "r"(hi.z),
-                             "r"(hi.w)
-                             : "memory");
+        for (int c = 0; c < kBatch; ++c) {
+            const int k = key0 + k0 + c * kStep, row = d.rows[k >> 4];
+            v[c] = make_uint4(0u, 0u, 0u, 0u);
+            e[c] = 0u;
+            if (row >= 0 && !((d.zero[k >> 5] >> (k & 31)) & 1u)) {
+                const bool ring = (d.flags >> (kRingShift + (k >> 4))) & 1;
+                const size_t r = (size_t)row + (k & 15);
+                v[c] = ldg16((ring ? a.win8 : a.kv8) + r * a.D + dim);
+                e[c] = __ldg((ring ? a.win8e : a.kv8e) + r * (a.D / 128) + dim / 128);
             }
         }
-    } else {
-        const bool in_row = dim < a.D;
-#pragma unroll 4
-        for (int k = lane / kUnits; k < kKeys; k += kStep) {
-            const long long r = row_of(key0 + k);
-            const uint16_t *src = r < 0 ? a.win + (size_t)~r * a.D + dim : a.kv + (size_t)r * a.D + dim;
-            cp_async16_or_zero(at(k, u), r != kNone && in_row ? src : nullptr, a.win);
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+            const int k = k0 + c * kStep;
+            const uint4 lo = e4m3x8_bf16x8(make_uint2(v[c].x, v[c].y), e[c]);
+            const uint4 hi = e4m3x8_bf16x8(make_uint2(v[c].z, v[c].w), e[c]);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(k, u)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w)
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(k, u + 1)), "r"(hi.x), "r"(hi.y), "r"(hi.z),
+                         "r"(hi.w)
+                         : "memory");
         }
     }
 }
 
+// The tensor maps of one call, [64-dim chunk][row][64] each.
+struct Maps {
+    CUtensorMap q;         // 64 rows x 2 chunks
+    CUtensorMap k, v;      // pool or copy: box rows x 2 chunks (box 64) or 1, vbox rows x an SM's half of V
+    CUtensorMap k16, v16;  // pool, 16 rows x 1 chunk, 16 rows x an SM's half
+    CUtensorMap rk16, rv16;  // the rings, the same
+};
+
 template <int DP, bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    attend_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                         const __grid_constant__ CUtensorMap vmap, const Params p) {
+    attend_prefix_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     using Lt = Layout<DP>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const Smem s = carve<DP>(smem_raw);
@@ -445,12 +431,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(s.full + i, 2);   // used on the leader: each CTA's producer (+ bytes of both)
             mbar_init(s.empty + i, 1);  // commit
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kSBufs; ++i) {
             mbar_init(s.sfull + i, 1);
-            mbar_init(s.sempty + i, 2 * kSoftWarps);  // leader: the softmax warps of both CTAs
-            mbar_init(s.pfull + i, 2 * kSoftWarps);   // leader
-            mbar_init(s.pvdone + i, 1);
+            mbar_init(s.sempty + i, kSoftWarps);  // leader: a group's warps in both CTAs
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s.pfull + i, kSoftWarps);  // leader: the same
+            mbar_init(s.pvdone + i, 1);
+            mbar_init(s.mdec + i, kSoftWarps / 2);
+            mbar_init(s.rbar + i, kSoftWarps / 2);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(s.xbar + i, 2);
         mbar_init(s.qland, 1);
         mbar_init(s.qready, q_rw ? 2 * kSoftWarps : 2);  // leader
         mbar_init(s.qempty, 1 + kSoftWarps);
@@ -461,9 +452,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         *s.abort_flag = 0;
         fence_mbar_init();
-        tc::prefetch_tmap(&qmap);
-        tc::prefetch_tmap(&kmap);
-        tc::prefetch_tmap(&vmap);
+        tc::prefetch_tmap(&maps.q);
+        tc::prefetch_tmap(&maps.k);
+        tc::prefetch_tmap(&maps.v);
     }
     if (warp == kQueryWarp) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
     tc::fence_before_sync();
@@ -486,26 +477,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp < kProducers) {
         // ------------------------------------------------------------ producers
-        // The copies of an own slot are in flight while the warp's next slot is issued (unless
-        // that one is not free yet).  TMA copies are issued by one thread inside an elect_one
-        // branch (one issued by every lane under a guard, or by a diverged lane, took ~200
-        // cycles: more than the MMAs that it feeds).
+        // TMA copies are issued by one thread inside an elect_one branch (one issued by every lane
+        // under a guard, or by a diverged lane, took ~200 cycles: more than the MMAs that it feeds).
         if (p.linear) asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' copy
         const bool v = warp >= 2;  // K's or V's ring
         const int ring = v ? kSlots : 0;
         const uint32_t full0 = tc::map_to_rank(smem_u32(s.full + ring), 0), slots = smem_u32(s.slots) + ring * kSlotBytes;
         const uint32_t vfix = smem_u32(s.vfix + (warp & 1));
         uint32_t it = 0, nfix = 0;  // ring position
-        int pending = -1;
         bool ok = true;
-        const auto flush = [&] {
-            if (pending < 0) return;
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            mbar_arrive_cluster(full0 + pending * 8, lane == 0);
-            pending = -1;
-        };
         for (uint32_t g = 0; ok; ++g) {
             const Tile *dp = warp_desc_of(g);
             if (!(ok = dp != nullptr)) break;
@@ -516,64 +496,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if ((it ^ (uint32_t)warp) & 1u) continue;
                 const uint32_t sl = it % kSlots, par = ((it / kSlots) & 1u) ^ 1u, empty = smem_u32(s.empty + ring + sl);
                 const uint32_t dst = slots + sl * kSlotBytes, full = full0 + sl * 8;
-                if (!__all_sync(0xffffffffu, mbar_test_wait(empty, par))) {
-                    flush();
-                    if (!(ok = warp_wait(empty, par, p.ctx, s.abort_flag))) break;
-                }
-                if (!(d.flags & kShared)) {
-                    if (v) gather_slot<DP, FP8, true>(p, d, rank, w, dst);
-                    else gather_slot<DP, FP8, false>(p, d, rank, w, dst);
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    const int before = pending;
-                    pending = (int)sl;
-                    if (FP8) {
-                        flush();
-                    } else if (before >= 0) {
-                        asm volatile("cp.async.wait_group 1;" ::: "memory");
-                        tc::fence_proxy_async_smem();
-                        __syncwarp();
-                        mbar_arrive_cluster(full0 + before * 8, lane == 0);
-                    }
+                if (!(ok = warp_wait(empty, par, p.ctx, s.abort_flag))) break;
+                const bool mixed = d.flags & kMixed;
+                const int vbox = mixed ? 16 : p.vbox;
+                if (FP8 && !(d.flags & kShared)) {
+                    if (v) expand_slot<DP, true>(p, d, rank, w, dst, vbox);
+                    else expand_slot<DP, false>(p, d, rank, w, dst, vbox);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    mbar_arrive_cluster(full, lane == 0);
                     continue;
                 }
-                flush();
                 if (!v) {
                     if (tc::elect_one()) {
                         mbar_arrive_expect_tx_cluster(full, kSlotBytes);
-                        if (p.box == 64) {
-                            tc::tma_load_3d_2sm(dst, &kmap, full, 0, d.rows[rank * 4], 2 * w);
+                        if (p.box == 64 && !mixed) {
+                            tc::tma_load_3d_2sm(dst, &maps.k, full, 0, d.rows[rank * 4], 2 * w);
                         } else {
-                            for (int x = 0; x < 64; x += p.box) {
-                                const int row = d.rows[rank * 4 + x / 16];
-                                tc::tma_load_3d_2sm(dst + x * 128, &kmap, full, 0, row, 2 * w);
-                                tc::tma_load_3d_2sm(dst + 8192 + x * 128, &kmap, full, 0, row, 2 * w + 1);
+                            const int box = mixed ? 16 : p.box;
+                            for (int x = 0; x < 64; x += box) {
+                                const int i = rank * 4 + x / 16, row = d.rows[i];
+                                const CUtensorMap *map =
+                                    !mixed ? &maps.k : (d.flags >> (kRingShift + i)) & 1 ? &maps.rk16 : &maps.k16;
+                                tc::tma_load_3d_2sm(dst + x * 128, map, full, 0, row, 2 * w);
+                                tc::tma_load_3d_2sm(dst + 8192 + x * 128, map, full, 0, row, 2 * w + 1);
                             }
                         }
                     }
                     __syncwarp();
                     continue;
                 }
-                // V: entries of the tile that do not count have zero weights; their values (anything,
-                // in memory) are cleared where a copy brings them
-                const int end = d.ent - w * Lt::kVKeys;  // entries of the slot that count
-                const bool fix = end > 0 && end < Lt::kVKeys && (end & (p.vbox - 1)) != 0;
+                // V: keys that no row takes have zero weights; their values (anything, in memory) are
+                // cleared where a copy brings them
+                bool fix = false;
+#pragma unroll
+                for (int i = 0; i < Lt::kVKeys / 32; ++i) fix |= d.zero[w * (Lt::kVKeys / 32) + i] != 0u;
                 if (tc::elect_one()) {
                     const uint32_t bar = fix ? tc::map_to_rank(vfix, rank) : full;
                     mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
-                    for (int x = 0; x < Lt::kVKeys; x += p.vbox)
-                        tc::tma_load_3d_2sm(dst + x * (Lt::kVChunks * 128), &vmap, bar, 0, d.rows[(w * Lt::kVKeys + x) / 16],
-                                            rank * Lt::kVChunks);
+                    for (int x = 0; x < Lt::kVKeys; x += vbox) {
+                        const int i = (w * Lt::kVKeys + x) / 16;
+                        const CUtensorMap *map =
+                            !mixed ? &maps.v : (d.flags >> (kRingShift + i)) & 1 ? &maps.rv16 : &maps.v16;
+                        tc::tma_load_3d_2sm(dst + x * (Lt::kVChunks * 128), map, bar, 0, d.rows[i], rank * Lt::kVChunks);
+                    }
                 }
                 __syncwarp();
                 if (fix) {
                     if (!(ok = warp_wait(vfix, nfix & 1u, p.ctx, s.abort_flag))) break;
                     ++nfix;
-                    // entry e of the slot, chunk c: [e / vbox][c][e % vbox][128 B]
+                    // key e of the slot, chunk c: [e / vbox][c][e % vbox][128 B]
                     uint4 *slot = reinterpret_cast<uint4 *>(s.slots + (ring + sl) * kSlotBytes);
+                    const int vsh = 31 - __clz(vbox);
 #pragma unroll 1
                     for (int y = lane; y < Lt::kVKeys * Lt::kVChunks * 8; y += 32) {
-                        const int line = y >> 3, e = line / (Lt::kVChunks * p.vbox) * p.vbox + (line & (p.vbox - 1));
-                        if (e >= end) slot[y] = make_uint4(0u, 0u, 0u, 0u);
+                        const int line = y >> 3, e = w * Lt::kVKeys + (line >> vsh) / Lt::kVChunks * vbox + (line & (vbox - 1));
+                        if ((d.zero[e >> 5] >> (e & 31)) & 1u) slot[y] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     tc::fence_proxy_async_smem();
                     __syncwarp();
@@ -581,8 +559,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (ok) flush();
-        asm volatile("cp.async.wait_all;" ::: "memory");
         copies = !ok;
     } else if (warp == kQkWarp) {
         // ------------------------------------------------------------ Q K^T (one thread of the leader)
@@ -596,12 +572,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!d) break;
                 const int flags = d->flags;
                 if (flags & kEnd) break;
-                const uint32_t b = g & 1u;
+                const uint32_t b = g % kSBufs;
                 if (flags & kFirst) {
                     if (!mbar_wait(smem_u32(s.qready), nq & 1u, p.ctx, s.abort_flag)) break;
                     ++nq;
                 }
-                if (!mbar_wait(smem_u32(s.sempty + b), ((g >> 1) & 1u) ^ 1u, p.ctx, s.abort_flag)) break;
+                if (!mbar_wait(smem_u32(s.sempty + b), ((g / kSBufs) & 1u) ^ 1u, p.ctx, s.abort_flag)) break;
                 for (int w = 0; w < Lt::kPieces; ++w, ++it) {
                     const uint32_t sl = it % kSlots;
                     if (!(ok = mbar_wait(smem_u32(s.full + sl), (it / kSlots) & 1u, p.ctx, s.abort_flag))) break;
@@ -623,10 +599,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ P V (one thread of the leader)
         if (rank == 0 && tc::elect_one()) {
             // V as stored, [keys][dims] (MN-major): 64-dim chunks vbox * 128 bytes apart, 8-key groups 1024
-            const uint64_t vdesc =
-                tc::smem_desc_lbo(smem_u32(s.slots) + kSlots * kSlotBytes, p.vbox * 128, 1024, tc::kLayoutSw128);
+            const uint32_t vslots = smem_u32(s.slots) + kSlots * kSlotBytes;
             const uint64_t pdesc = tc::smem_desc(smem_u32(s.p), 1024, tc::kLayoutSw128);
-            const int vsh = 31 - __clz(p.vbox);
             uint32_t it = 0;
             bool ok = true;
             for (uint32_t g = 0; ok; ++g) {
@@ -634,7 +608,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!d) break;
                 const int flags = d->flags;
                 if (flags & kEnd) break;
-                const uint32_t b = g & 1u;
+                const uint32_t b = g & 1u, vbox = flags & kMixed ? 16 : p.vbox, vsh = 31 - __clz(vbox);
+                const uint64_t vdesc = tc::smem_desc_lbo(vslots, vbox * 128, 1024, tc::kLayoutSw128);
                 if (!mbar_wait(smem_u32(s.pfull + b), (g >> 1) & 1u, p.ctx, s.abort_flag)) break;
                 for (int w = 0; w < Lt::kPieces; ++w, ++it) {
                     const uint32_t sl = it % kSlots;
@@ -643,12 +618,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < Lt::kVKeys / 16; ++k) {  // 16 keys each
                         const uint32_t kt = w * (Lt::kVKeys / 16) + k, x = k * 16;
-                        const uint32_t voff = ((((x >> vsh) * Lt::kVChunks) << vsh) + (x & (p.vbox - 1))) * 128;
+                        const uint32_t voff = ((((x >> vsh) * Lt::kVChunks) << vsh) + (x & (vbox - 1))) * 128;
 #pragma unroll
                         for (int i = 0; i < Lt::kPvMmas; ++i)
                             tc::mma_f16_2sm(tmem + i * (Lt::kPvN / 2),
                                             pdesc + ((b * kPBytes + (kt >> 2) * 8192 + (kt & 3) * 32) >> 4),
-                                            vdesc + ((sl * kSlotBytes + voff + i * 2 * p.vbox * 128) >> 4), p.idesc_pv,
+                                            vdesc + ((sl * kSlotBytes + voff + i * 2 * vbox * 128) >> 4), p.idesc_pv,
                                             (!(flags & kFirst) || kt) ? 1u : 0u);
                     }
                     tc::mma_commit_2sm(smem_u32(s.empty + kSlots + sl));
@@ -674,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (tc::elect_one()) {
                 mbar_arrive_expect_tx_cluster(qland, Lt::kQBytes);
                 for (int c = 0; c < DP / 64; c += 2)
-                    tc::tma_load_3d_2sm(smem_u32(s.q) + c * 8192, &qmap, qland, 0, row, c);
+                    tc::tma_load_3d_2sm(smem_u32(s.q) + c * 8192, &maps.q, qland, 0, row, c);
             }
             __syncwarp();
             if (!(ok = warp_wait(smem_u32(s.qland), nq & 1u, p.ctx, s.abort_flag))) break;
@@ -704,79 +679,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int b0 = qs.bq0 / a.nq, b1 = qs.bq1 / a.nq;
             int vmax = 0, n = 0;
             for (int q = qs.bq0 + lane; q <= qs.bq1; q += 32) vmax = std::max(vmax, visible(p, __ldg(a.q_pos + q), p.n_shared));
-            const auto request = [&](int b) {
-                return own_keys(p, std::max(qs.bq0, b * a.nq), std::min(qs.bq1, b * a.nq + a.nq - 1));
-            };
-            for (int b = b0 + lane; b <= b1; b += 32) n += request(b).tiles();
+            const auto query0 = [&](int b) { return std::max(qs.bq0, b * a.nq); };
+            const auto query1 = [&](int b) { return std::min(qs.bq1, b * a.nq + a.nq - 1); };
+            for (int b = b0 + lane; b <= b1; b += 32) n += own_keys(p, query0(b), query1(b)).tiles();
             vmax = __reduce_max_sync(0xffffffffu, vmax);
             const int shared = (vmax + kPrefixKeys - 1) / kPrefixKeys;
-            n = __reduce_add_sync(0xffffffffu, n) + shared - un.x;
-            if (n > 0) {
-                n = (int)std::min<long long>(n, un.left);
-                un.left -= n;
-                int x = un.x, b = b0 - 1;
-                long long y = x - shared;  // the tile's number among its request's own ones
-                Own own = {0, 0, 0};
-                for (int j = 0; j < n && ok; ++j, ++x, ++y) {
-                    Tile *d = entry();
-                    if (!d) break;
-                    const bool sh = x < shared;
-                    int ent, cnt, e_first, wpos = 0, ring = 0;
-                    if (sh) {
-                        e_first = x * kPrefixKeys;
-                        cnt = ent = std::min(vmax - e_first, +kPrefixKeys);
-                    } else {
-                        while (y >= own.tiles()) {
-                            y -= own.tiles();
-                            own = request(++b);
-                        }
-                        const long long first = y * kPrefixKeys;
-                        e_first = (int)std::min<long long>(p.n_shared + first, 0x7fffffff);
-                        ent = (int)std::min<long long>(std::max<long long>(own.n_own - first, 0), +kPrefixKeys);
-                        cnt = (int)std::min<long long>(own.total - first, +kPrefixKeys);
-                        wpos = (int)(own.u0 + first - own.n_own);
-                        ring = ent < cnt ? (int)((uint32_t)(wpos + ent) % (uint32_t)a.win_rows) : 0;
+            n = std::min((int)__reduce_add_sync(0xffffffffu, n) + shared - un.x, un.left);
+            un.left -= std::max(n, 0);
+            int x = un.x, b = b0 - 1;
+            int y = x - shared;  // the tile's number among its request's own ones
+            Own own = {0, 0u};
+            for (int j = 0; j < n; ++j, ++x, ++y) {
+                Tile *d = entry();
+                if (!d) break;
+                const bool sh = x < shared;
+                int flags = (sh ? kShared : 0) | (j == 0 ? kFirst : 0) | (j == n - 1 ? kLast : 0);
+                int ent, e_first, r_first = 0;
+                const int *table = a.table;
+                if (sh) {
+                    e_first = x * kPrefixKeys;
+                    ent = std::min(vmax - e_first, +kPrefixKeys);
+                } else {
+                    while (y >= own.tiles()) {
+                        y -= own.tiles();
+                        ++b;
+                        own = own_keys(p, query0(b), query1(b));
                     }
-                    int row = -kPrefixKeys;
-                    bool missing = false;
-                    if (lane < 8 && lane * 16 < ent) {
-                        const uint32_t e = (uint32_t)(e_first + lane * 16), pg = e / (uint32_t)a.page;
-                        const int id = __ldg(a.table + (sh ? 0 : (size_t)b * a.max_pages) + pg);
+                    const uint32_t first = (uint32_t)y * kPrefixKeys;
+                    e_first = p.n_shared + (int)first;
+                    ent = std::min(std::max(own.n_own - (int)first, 0), +kPrefixKeys);
+                    r_first = (int)first - (int)own.ring0();
+                    if (r_first > -kPrefixKeys) flags |= kMixed;
+                    table += (size_t)b * a.max_pages;
+                }
+                // 16 keys by lane: their first row
+                int row = -kPrefixKeys;
+                bool missing = false, from_ring = false;
+                if (lane < 8) {
+                    const int k = lane * 16, rr = r_first + k;
+                    if (k < ent) {
+                        const uint32_t e = (uint32_t)(e_first + k), pg = e / (uint32_t)a.page;
+                        const int id = __ldg(table + pg);
                         missing = id < 0 || id >= a.n_pages;
                         if (sh && p.linear) row = (int)e;
                         else if (!missing) row = id * a.page + (int)(e - pg * (uint32_t)a.page);
+                    } else if ((flags & kMixed) && rr >= 0 && rr < a.win_rows) {
+                        row = b * (int)a.win_rows + rr;
+                        from_ring = true;
                     }
-                    if (lane < 8) d->rows[lane] = row;
-                    const int miss = (int)__ballot_sync(0xffffffffu, missing);
-                    if (lane == 0) {
-                        d->flags = (sh ? kShared : 0) | (j == 0 ? kFirst : 0) | (j == n - 1 ? kLast : 0) | (miss << kMissingShift);
-                        d->rt = un.rt;
-                        d->b = b;
-                        d->e_first = e_first;
-                        d->ent = ent;
-                        d->cnt = cnt;
-                        d->wpos = wpos;
-                        d->ring = ring;
-                    }
-                    publish();
-                    if (sh || rank == 0) continue;
-                    // own rows into L2, by the pair's other CTA
+                    d->rows[lane] = row;
+                }
+                flags |= (int)(__ballot_sync(0xffffffffu, missing) << kMissingShift);
+                flags |= (int)(__ballot_sync(0xffffffffu, from_ring) << kRingShift);
+                // 32 keys at a time: which of them some row takes, and which others a copy brings
+                const int vb = flags & kMixed ? 16 : p.vbox;
 #pragma unroll 1
-                    for (int k = lane; k < kPrefixKeys; k += 32) {
-                        const int er = __shfl_sync(0xffffffffu, row, k >> 4);
-                        const void *src = nullptr;
-                        if (k < ent) {
-                            if (er >= 0) src = FP8 ? (const void *)(a.kv8 + (size_t)(er + (k & 15)) * a.D)
-                                                   : (const void *)(a.kv + (size_t)(er + (k & 15)) * a.D);
-                        } else if (k < cnt) {
-                            const size_t r = (size_t)b * a.win_rows + (uint32_t)(wpos + k) % (uint32_t)a.win_rows;
-                            src = FP8 ? (const void *)(a.win8 + r * a.D) : (const void *)(a.win + r * a.D);
+                for (int i = 0; i < 4; ++i) {
+                    const int k = i * 32 + lane;
+                    const int krow = __shfl_sync(0xffffffffu, row, k >> 4);
+                    const bool brought = __shfl_sync(0xffffffffu, row, (k & ~(vb - 1)) >> 4) >= 0;
+                    bool live = k < ent && krow >= 0;
+                    const int rr = r_first + k;
+                    if (!sh && k >= ent && rr >= 0 && rr < a.win_rows) {
+                        const int q1 = query1(b);
+                        for (int q = query0(b); q <= q1; ++q) {
+                            const int t = __ldg(a.q_pos + q);
+                            if (t < 0) continue;
+                            const int back = ((int)((uint32_t)t % (uint32_t)a.win_rows) - rr + (int)a.win_rows) % (int)a.win_rows;
+                            live |= back < a.W && back <= t;
                         }
-                        if (src)
-                            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(FP8 ? a.D : 2 * a.D)
-                                         : "memory");
+                    }
+                    const uint32_t z = __ballot_sync(0xffffffffu, !live && (brought || (FP8 && !sh)));
+                    if (lane == 0) d->zero[i] = z;
+                    // own rows into L2, by the pair's other CTA
+                    if (live && !sh && rank == 1) {
+                        const size_t r = (size_t)krow + (k & 15);
+                        const void *src;
+                        if (FP8) src = (rr >= 0 && k >= ent ? a.win8 : a.kv8) + r * a.D;
+                        else src = (rr >= 0 && k >= ent ? a.win : a.kv) + r * a.D;
+                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(FP8 ? a.D : 2 * a.D)
+                                     : "memory");
                     }
                 }
+                if (lane == 0) {
+                    d->flags = flags;
+                    d->rt = un.rt;
+                    d->b = b;
+                    d->e_first = e_first;
+                    d->ent = ent;
+                    d->r_first = r_first;
+                }
+                publish();
             }
             ++un.rt;
             un.x = 0;
@@ -790,146 +783,167 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ softmax, partial rows
-        // The four warps of 32 rows meet at named barriers: a wait that was given up is told to
-        // all of them at the next one (group_all), so that they leave together.
+        // Group wg takes the tiles of its parity; both meet where a row tile begins and ends.
         const int quarter = warp & 3, wg = (warp - kSoftWarp0) >> 2;
-        const int tl = quarter * 32 + lane;       // tensor-memory lane
-        const int r = tl & 63, hf = tl >> 6;      // row of this CTA's 64; first / second half of the columns
-        const int q4 = hf * 2 + wg;               // which of the row's four threads
-        const int off = hf * 64 + wg * 32;        // its first key of a tile
-        const int bar_id = 1 + (quarter & 1);     // the 128 threads of 32 rows
+        const int tl = quarter * 32 + lane;     // tensor-memory lane
+        const int r = tl & 63, hf = tl >> 6;    // row of this CTA's 64; first / second half of the columns
+        const int q4 = hf * 2 + wg;             // which of the row's four threads
+        float *xch = s.xch + (quarter & 1) * 128;       // of these 32 rows
+        uint16_t *xmax = reinterpret_cast<uint16_t *>(xch + 64) + wg * 64;
+        const uint32_t rbar = smem_u32(s.rbar + (quarter & 1)), xbar = smem_u32(s.xbar + wg * 2 + (quarter & 1));
+        uint32_t rbar_n = 0, xbar_n = 0;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t sempty0 = tc::map_to_rank(smem_u32(s.sempty), 0), pfull0 = tc::map_to_rank(smem_u32(s.pfull), 0);
         const uint32_t qready0 = tc::map_to_rank(smem_u32(s.qready), 0);
-        const int n_rows = (int)(a.n_bq * a.H);
+        const int n_rows = (int)(a.n_bq * a.H), win_rows = (int)a.win_rows;
         uint32_t nq = 0;
-        int t = -1, vis = 0, b_row = 0;
+        Row rw = {-1, 0, 0, 0, -1};
         float rq = 0.f, m_run = -INFINITY, l = 0.f;
-        const Tile *d = warp_desc_of(0);
-        bool ok = group_all(bar_id, d != nullptr);
-        if (!ok) d = nullptr;
-        for (uint32_t g = 0; d; ++g) {
-            const int flags = d->flags;
-            if (flags & kEnd) break;
-            const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
+        const auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return warp_wait(smem_u32(bar), parity, p.ctx, s.abort_flag);
+        };
+        for (uint32_t g = 0;; ++g) {
+            const Tile *dp = warp_desc_of(g);
+            if (!dp || (dp->flags & kEnd)) break;
+            const Tile &d = *dp;
+            const int flags = d.flags;
+            const size_t part = (size_t)pair + d.rt;
             if (flags & kFirst) {  // a new row tile
-                const int row = d->rt * kPrefixRows + rank * 64 + r;
+                const int row = d.rt * kPrefixRows + rank * 64 + r;
                 const int bq = row < n_rows ? row / a.H : 0;
-                t = row < n_rows ? __ldg(a.q_pos + bq) : -1;
-                b_row = bq / a.nq;
-                vis = visible(p, t, (int)a.N);
-                ok = warp_wait(smem_u32(s.qland), nq & 1u, p.ctx, s.abort_flag);
+                rw.t = row < n_rows ? __ldg(a.q_pos + bq) : -1;
+                rw.b = bq / a.nq;
+                rw.vis = visible(p, rw.t, (int)a.N);
+                rw.w0 = rw.t < 0 ? win_rows : (int)((uint32_t)std::max(0, rw.t - a.W + 1) % (uint32_t)win_rows);
+                rw.w1 = rw.t < 0 ? -1 : (int)((uint32_t)rw.t % (uint32_t)win_rows);
+                if (!wait(s.qland, nq & 1u)) break;
                 ++nq;
-                s.xsum[q4 * 64 + r] = query_squares<DP>(s.q, r, q4);
+                xch[q4 * 32 + lane] = query_squares<DP>(s.q, r, q4);
                 if (q_rw) {
-                    query_rewrite<DP>(a, s.q, r, q4, t);
+                    query_rewrite<DP>(a, s.q, r, q4, rw.t);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     mbar_arrive_cluster(qready0, lane == 0);
                 }
                 __syncwarp();
                 mbar_arrive(smem_u32(s.qempty), lane == 0);
-                group_sync(bar_id);
-                const float ss = (s.xsum[r] + s.xsum[64 + r]) + (s.xsum[128 + r] + s.xsum[192 + r]);
-                group_sync(bar_id);
+                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+                const float ss = (xch[lane] + xch[32 + lane]) + (xch[64 + lane] + xch[96 + lane]);
                 // 1 / RMS times the softmax scale, in log2 units
                 rq = (1.0f / sqrtf(ss / (float)a.D + a.eps)) * a.scale * 1.4426950408889634f;
                 m_run = -INFINITY;
                 l = 0.f;
+                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
             }
-            const uint32_t mask = key_mask(*d, off, t, a.W, vis, b_row);  // keys that take part
-            const bool whole = __all_sync(0xffffffffu, mask == 0xffffffffu);
-            const size_t part = (size_t)pair + d->rt;
-            const Tile *next = warp_desc_of(g + 1);
-            ok = warp_wait(smem_u32(s.sfull + b), ph, p.ctx, s.abort_flag) && next && ok;
-            tc::fence_after_sync();
-            float sc[32];
-            tc::tmem_ld32(tmem + lane_base + kSCols + b * 64 + wg * 32, sc);
-            tc::tmem_wait_ld();
-            tc::fence_before_sync();
-            __syncwarp();
-            mbar_arrive_cluster(sempty0 + b * 8, lane == 0);
-            // the largest scaled score: the largest raw one, or the smallest under a negative scale
-            float mt = -INFINITY;
-            if (whole && rq >= 0.f) {
-                float m2 = sc[1];
-                mt = sc[0];
-#pragma unroll
-                for (int i = 2; i < 32; i += 2) {
-                    mt = fmaxf(mt, sc[i]);
-                    m2 = fmaxf(m2, sc[i + 1]);
-                }
-                mt = fmaxf(mt, m2) * rq;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) mt = fmaxf(mt, (mask >> i) & 1u ? sc[i] * rq : -INFINITY);
-            }
-            // the row's maximum over its four threads, each rounded to 16 bits towards zero
-            // (any reference near the maximum serves, as long as the four agree)
-            s.xmax[(b * 4 + q4) * 64 + r] = (uint16_t)(__float_as_uint(mt) >> 16);
-            if (!group_all(bar_id, ok)) break;
-            mt = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mt = fmaxf(mt, __uint_as_float((uint32_t)s.xmax[(b * 4 + i) * 64 + r] << 16));
-            const bool mine = m_run != -INFINITY && mt > m_run + kRescaleThreshold;
-            if (__any_sync(0xffffffffu, mine)) {
-                const uint32_t gp = g - 1;  // O after the P.V of the tile before
-                ok = warp_wait(smem_u32(s.pvdone + (gp & 1u)), (gp >> 1) & 1u, p.ctx, s.abort_flag) && ok;
+            if ((g & 1u) == (uint32_t)wg) {
+                const uint32_t b = g & 1u, ph = (g >> 1) & 1u, sb = g % kSBufs;
+                const uint32_t mk0 = key_mask(d, hf * 64, rw, win_rows), mk1 = key_mask(d, hf * 64 + 32, rw, win_rows);
+                const bool whole = __all_sync(0xffffffffu, (mk0 & mk1) == 0xffffffffu);
+                if (!wait(s.sfull + sb, (g / kSBufs) & 1u)) break;
                 tc::fence_after_sync();
-                const float f = mine ? exp2f(m_run - mt) : 1.0f;
+                float sc[64];
+                tc::tmem_ld32(tmem + lane_base + kSCols + sb * 64, sc);
+                tc::tmem_ld32(tmem + lane_base + kSCols + sb * 64 + 32, sc + 32);
+                tc::tmem_wait_ld();
+                tc::fence_before_sync();
+                __syncwarp();
+                mbar_arrive_cluster(sempty0 + sb * 8, lane == 0);
+                // the largest scaled score: the largest raw one, or the smallest under a negative scale
+                float mt = -INFINITY;
+                if (whole && rq >= 0.f) {
+                    float m2 = sc[1];
+                    mt = sc[0];
+#pragma unroll
+                    for (int i = 2; i < 64; i += 2) {
+                        mt = fmaxf(mt, sc[i]);
+                        m2 = fmaxf(m2, sc[i + 1]);
+                    }
+                    mt = fmaxf(mt, m2) * rq;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        mt = fmaxf(mt, ((i < 32 ? mk0 : mk1) >> (i & 31)) & 1u ? sc[i] * rq : -INFINITY);
+                }
+                // The row's maximum over its two threads, each rounded to 16 bits towards zero (any
+                // reference near the maximum serves, as long as all agree).  The reference of the tile
+                // before is final once the other group says so; by then this group has read its own
+                // last maxima, too.
+                if (g > 0 && !wait(s.mdec + ((g - 1) & 1u), ((g - 1) >> 1) & 1u)) break;
+                xmax[hf * 32 + lane] = (uint16_t)(__float_as_uint(mt) >> 16);
+                if (!warps_meet(xbar, xbar_n, p.ctx, s.abort_flag)) break;
+                mt = fmaxf(__uint_as_float((uint32_t)xmax[lane] << 16), __uint_as_float((uint32_t)xmax[32 + lane] << 16));
+                const float m_old = flags & kFirst ? -INFINITY : xch[(b ^ 1u) * 32 + lane];
+                const bool mine = m_old != -INFINITY && mt > m_old + kRescaleThreshold;
+                const float m_new = mine || m_old == -INFINITY ? mt : m_old;
+                if (hf == 0) xch[b * 32 + lane] = m_new;
+                __syncwarp();
+                mbar_arrive(smem_u32(s.mdec + b), lane == 0);
+                // P buffer b was read by the P.V of tile g - 2
+                if (!wait(s.pvdone + b, ph ^ 1u)) break;
+                if (__any_sync(0xffffffffu, mine)) {
+                    const uint32_t gp = g - 1;  // O after the P.V of the tile before
+                    if (!wait(s.pvdone + (gp & 1u), (gp >> 1) & 1u)) break;
+                    tc::fence_after_sync();
+                    const float f = mine ? exp2f(m_old - m_new) : 1.0f;
 #pragma unroll 1
-                for (int c = wg * (DP / 4); c < (wg + 1) * (DP / 4); c += 16) {
-                    float v[16];
-                    tc::tmem_ld16(tmem + lane_base + c, v);
-                    tc::tmem_wait_ld();
+                    for (int c = 0; c < DP / 2; c += 16) {
+                        float v[16];
+                        tc::tmem_ld16(tmem + lane_base + c, v);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] *= f;
-                    tc::tmem_st16(tmem + lane_base + c, v);
+                        for (int i = 0; i < 16; ++i) v[i] *= f;
+                        tc::tmem_st16(tmem + lane_base + c, v);
+                    }
+                    tc::tmem_wait_st();
                 }
-                tc::tmem_wait_st();
-                if (mine) {
-                    l *= f;
-                    m_run = mt;
+                if (m_run != m_new) {  // this thread's sum is relative to m_run
+                    if (m_run != -INFINITY) l *= exp2f(m_run - m_new);
+                    m_run = m_new;
                 }
+                const float mref = m_new == -INFINITY ? 0.f : m_new;
+                uint8_t *prow = s.p + b * kPBytes + hf * 8192 + r * 128;
+                float ps[2] = {0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {  // 8 keys: 16 bytes
+                    float e[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) e[i] = exp2_ftz(fmaf(sc[x * 8 + i], rq, -mref));
+                    if (!whole) {
+                        const uint32_t mk = (x < 4 ? mk0 : mk1) >> (x * 8 & 31);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) e[i] = (mk >> i) & 1u ? e[i] : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        ps[0] += e[i];
+                        ps[1] += e[i + 1];
+                    }
+                    *reinterpret_cast<uint4 *>(prow + ((x ^ (r & 7)) << 4)) = pack8(e);
+                }
+                l += ps[0] + ps[1];
+                tc::fence_proxy_async_smem();
+                tc::fence_before_sync();
+                __syncwarp();
+                mbar_arrive_cluster(pfull0 + b * 8, lane == 0);
             }
-            if (m_run == -INFINITY) m_run = mt;
-            const float mref = m_run == -INFINITY ? 0.f : m_run;
-            float ps[2] = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sc[i] = exp2_ftz(fmaf(sc[i], rq, -mref));
-            if (!whole) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) sc[i] = (mask >> i) & 1u ? sc[i] : 0.f;
-            }
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                ps[0] += sc[i];
-                ps[1] += sc[i + 1];
-                pk[i / 2] = pack_bf16x2(sc[i], sc[i + 1]);
-            }
-            l += ps[0] + ps[1];
-            // P buffer b was read by the P.V of tile g - 2
-            ok = warp_wait(smem_u32(s.pvdone + b), ph ^ 1u, p.ctx, s.abort_flag) && ok;
-            uint8_t *prow = s.p + b * kPBytes + hf * 8192 + r * 128;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4 *>(prow + (((wg * 4 + x) ^ (r & 7)) << 4)) =
-                    make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
-            tc::fence_proxy_async_smem();
-            tc::fence_before_sync();
             __syncwarp();
-            mbar_arrive_cluster(pfull0 + b * 8, lane == 0);
             mbar_arrive(smem_u32(s.dempty + g % kDescs), lane == 0);
             if (flags & kLast) {
-                ok = warp_wait(smem_u32(s.pvdone + b), ph, p.ctx, s.abort_flag) && ok;
+                const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
+                if ((g & 1u) != (uint32_t)wg) {  // the reference is final; the phase before the one awaited is over
+                    if (!wait(s.mdec + b, ph) || !wait(s.pvdone + b, ph ^ 1u)) break;
+                }
+                if (!wait(s.pvdone + b, ph)) break;
                 tc::fence_after_sync();
-                s.xsum[q4 * 64 + r] = l;  // (every thread has read the last tile's maxima)
-                group_sync(bar_id);
+                const float m = xch[b * 32 + lane];
+                if (m_run != m && m_run != -INFINITY) l *= exp2f(m_run - m);
+                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+                xch[q4 * 32 + lane] = l;
+                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
                 if (q4 == 0)
                     p.ml[part * kPrefixRows + rank * 64 + r] =
-                        make_float2(m_run, (s.xsum[r] + s.xsum[64 + r]) + (s.xsum[128 + r] + s.xsum[192 + r]));
-                group_sync(bar_id);
+                        make_float2(m, (xch[lane] + xch[32 + lane]) + (xch[64 + lane] + xch[96 + lane]));
+                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
                 float4 *dst = reinterpret_cast<float4 *>(p.part) + (part * 2 + rank) * (DP / 8) * 128 + tl;
 #pragma unroll 1
                 for (int c = wg * (DP / 4); c < (wg + 1) * (DP / 4); c += 32) {
@@ -942,7 +956,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 tc::fence_before_sync();  // O is read before the next row tile's first P.V (through pfull)
             }
-            d = next;
         }
     }
     if (copies) {
@@ -1012,10 +1025,16 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
         return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
                                  CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    const long long key_rows = x.linear ? x.n_shared : x.a.n_pages * x.a.page;
-    CUtensorMap qmap, kmap, vmap;
-    if (!encode(&qmap, x.a.q, x.a.n_bq * x.a.H, 64, 2) || !encode(&kmap, x.keys, key_rows, p.box, p.box == 64 ? 2 : 1) ||
-        !encode(&vmap, x.keys, key_rows, p.vbox, Layout<DP>::kVChunks))
+    const long long key_rows = x.linear ? x.n_shared : x.a.n_pages * x.a.page, batch = x.a.n_bq / x.a.nq;
+    constexpr int kChunks = Layout<DP>::kVChunks;
+    Maps maps = {};
+    if (!encode(&maps.q, x.a.q, x.a.n_bq * x.a.H, 64, 2) ||
+        !encode(&maps.k, x.keys, key_rows, p.box, p.box == 64 ? 2 : 1) ||
+        !encode(&maps.v, x.keys, key_rows, p.vbox, kChunks))
+        return CSA_ERR_CUDA;
+    if (!FP8 && (!encode(&maps.k16, x.keys, key_rows, 16, 1) || !encode(&maps.v16, x.keys, key_rows, 16, kChunks) ||
+                 !encode(&maps.rk16, x.a.win, batch * x.a.win_rows, 16, 1) ||
+                 !encode(&maps.rv16, x.a.win, batch * x.a.win_rows, 16, kChunks)))
         return CSA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * x.plan.pairs));
@@ -1027,7 +1046,7 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = x.linear ? 1 : 0;  // a dependent of the rows' copy
-    return cudaLaunchKernelEx(&cfg, kern, qmap, kmap, vmap, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, maps, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 }  // namespace
