@@ -77,12 +77,32 @@ struct Layout {
     static constexpr uint32_t kQBytes = 64 * DP * 2;      // [DP/64][64 rows][128 B]
 };
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1: n / d = (n * mul) >> (32 + shift), mul =
+// ceil(2^(31 + ceil(log2 d)) / d); 1 by itself (a runtime division is ~100 cycles on the planner's
+// and the softmax warps' serial paths).
+struct FastDiv {
+    uint32_t d, mul, shift;
+    static FastDiv by(uint32_t d) {
+        FastDiv f = {d, 0, 0};
+        if (d > 1) {
+            uint32_t l = 0;
+            while ((1ull << l) < d) ++l;
+            f.mul = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
+            f.shift = l - 1;
+        }
+        return f;
+    }
+    CSA_DEVINL int div(int n) const { return d == 1 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift); }
+    CSA_DEVINL int mod(int n) const { return n - div(n) * (int)d; }
+};
+
 struct Params {
     AttendArgs a;
     PrefixPlan plan;
     int n_shared;
     int linear;
     int *first;       // [row_tiles + 1] first unit of a row tile; the units of all
+    FastDiv H, nq, m, page, ring;
     int box;          // entries that one copy brings at most (none crosses a page): 16, 32 or 64
     int vbox;         // those of a V copy: at most one slot's
     float *part;
@@ -158,9 +178,10 @@ static_assert(smem_bytes<512>() <= 227 * 1024, "shared memory of one CTA");
 // ---------------------------------------------------------------- units
 // The tiles of row tile rt, in order: the shared entries that any of its rows
 // sees, then request by request the own keys of its queries in the row tile.
-CSA_DEVINL int visible(const Params &p, int t, int cap) {
-    const uint32_t v = t < 0 ? 0u : ((uint32_t)t + 1u) / (uint32_t)p.a.m;
-    return v < (uint32_t)cap ? (int)v : cap;
+CSA_DEVINL int visible(const Params &p, int t, int cap) {  // min((t + 1) / m, cap)
+    if (t < 0) return 0;
+    const int q = p.m.div(t), v = q + (t - q * (int)p.m.d == (int)p.m.d - 1 ? 1 : 0);
+    return v < cap ? v : cap;
 }
 
 // The own keys of queries [q0, q1] of one request: entries n_shared..n_shared + n_own - 1,
@@ -192,9 +213,9 @@ struct Queries {
 
 CSA_DEVINL Queries queries_of(const Params &p, int rt) {
     Queries r;
-    const uint32_t row0 = (uint32_t)rt * kPrefixRows, H = (uint32_t)p.a.H;
-    r.bq0 = (int)(row0 / H);
-    r.bq1 = (int)std::min<uint32_t>((uint32_t)p.a.n_bq - 1, (row0 + kPrefixRows - 1) / H);
+    const int row0 = rt * kPrefixRows;
+    r.bq0 = p.H.div(row0);
+    r.bq1 = std::min((int)p.a.n_bq - 1, p.H.div(row0 + kPrefixRows - 1));
     return r;
 }
 
@@ -204,8 +225,8 @@ CSA_DEVINL int count_units(const Params &p, int rt, int subs) {
     int vmax = 0, n = 0;
     if (rt < p.plan.row_tiles) {
         const Queries r = queries_of(p, rt);
-        const int b1 = r.bq1 / p.a.nq;
-        for (int b = r.bq0 / p.a.nq + (threadIdx.x & (subs - 1)); b <= b1; b += subs) {
+        const int b1 = p.nq.div(r.bq1);
+        for (int b = p.nq.div(r.bq0) + (threadIdx.x & (subs - 1)); b <= b1; b += subs) {
             const int q0 = std::max(r.bq0, b * p.a.nq), q1 = std::min(r.bq1, b * p.a.nq + p.a.nq - 1);
             n += own_keys(p, q0, q1).tiles();
             for (int q = q0; q <= q1; ++q) vmax = std::max(vmax, visible(p, __ldg(p.a.q_pos + q), p.n_shared));
@@ -265,8 +286,39 @@ CSA_DEVINL Units deal_units(const Params &p, int pair, bool write) {
     return u;
 }
 
+// mbar_wait (common.cuh) with the hardware's own wait made long and the rest out of line: some thirty waits
+// inlined, polled by a dozen idle warps, cost the working warps their instruction fetch.
+CSA_DEVINL bool try_wait_long(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)  // ns
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, const DevCtx &ctx, volatile int *abort) {
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (try_wait_long(bar, parity)) return true;
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > ctx.budget_ns) {
+            record_status(ctx.status, CSA_ERR_TIMEOUT);
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+CSA_DEVINL bool bar_wait(uint32_t bar, uint32_t parity, const DevCtx &ctx, volatile int *abort) {
+    return try_wait_long(bar, parity) || wait_on(bar, parity, ctx, abort);
+}
+
 CSA_DEVINL bool warp_wait(uint32_t bar, uint32_t parity, const DevCtx &ctx, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctx, abort));
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, ctx, abort));
 }
 
 // Where a few warps meet (an mbarrier of one arrival per warp, `uses` its phases so far): a named
@@ -297,9 +349,9 @@ CSA_DEVINL float query_squares(uint8_t *q, int r, int q4) {
     return ss[0] + ss[1];
 }
 
-// Rewrites the same units: the gain, then the rotation of the trailing kRopeDim
-// channels (unit j of the slice pairs with j + 4, also this thread's); rounded
-// to bf16, as the tensor cores' operand is.
+// Rewrites the same units: the gain and the scale's sign, then the rotation of the
+// trailing kRopeDim channels (unit j of the slice pairs with j + 4, also this
+// thread's); rounded to bf16, as the tensor cores' operand is.
 template <int DP>
 CSA_DEVINL void query_rewrite(const AttendArgs &a, uint8_t *q, int r, int q4, int t) {
     const int r0 = a.D / 8 - kRopeDim / 8;  // first rotated unit
@@ -309,12 +361,11 @@ CSA_DEVINL void query_rewrite(const AttendArgs &a, uint8_t *q, int r, int q4, in
         float x[8], y[8];
         unpack8(*p0, x);
         unpack8(*p1, y);
-        if (a.q_gain) {
+        const float sign = a.scale < 0.f ? -1.f : 1.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] *= __ldg(a.q_gain + unit * 8 + e);
-                y[e] *= __ldg(a.q_gain + unit * 8 + 32 + e);
-            }
+        for (int e = 0; e < 8; ++e) {
+            x[e] *= a.q_gain ? sign * __ldg(a.q_gain + unit * 8 + e) : sign;
+            y[e] *= a.q_gain ? sign * __ldg(a.q_gain + unit * 8 + 32 + e) : sign;
         }
         if (a.rope_cos && unit >= r0) {
 #pragma unroll
@@ -336,24 +387,35 @@ CSA_DEVINL uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0
 // bits x..y (either may lie outside)
 CSA_DEVINL uint32_t bits_between(int x, int y) { return low_bits(y + 1) & ~low_bits(x); }
 
-// The row of a query at t, of request b, that sees vis entries and the ring rows
-// w0..w1 (w0 > w1: ..w1 and w0..; none: w1 = -1 and w0 past the ring).
+// The ring rows that hold the window of a query: w0..w1, or (w0 > w1) ..w1 and w0.. .
+struct Window {
+    int w0, w1;
+};
+
+CSA_DEVINL Window window_of(const Params &p, int t) {  // t >= 0
+    return {p.ring.mod(std::max(0, t - p.a.W + 1)), p.ring.mod(t)};
+}
+
+// which of ring rows k0..k0 + 31 they are
+CSA_DEVINL uint32_t ring_bits(const Params &p, const Window &w, int k0) {
+    return w.w0 <= w.w1 ? bits_between(w.w0 - k0, w.w1 - k0)
+                        : bits_between(-k0, w.w1 - k0) | bits_between(w.w0 - k0, (int)p.ring.d - 1 - k0);
+}
+
+// The row of a query at t, of request b, that sees vis entries.
 struct Row {
-    int t, vis, b, w0, w1;
+    int t, vis, b;
+    Window w;
 };
 
 // Which of keys off..off + 31 of a tile it takes.
-CSA_DEVINL uint32_t key_mask(const Tile &d, int off, const Row &r, int win_rows) {
+CSA_DEVINL uint32_t key_mask(const Params &p, const Tile &d, int off, const Row &r) {
     const int flags = d.flags;
     if (!(flags & kShared) && r.b != d.b) return 0u;
     uint32_t mask = low_bits(std::min(r.vis - d.e_first, d.ent) - off);
     const int miss = flags >> (kMissingShift + off / 16);
     mask &= ~((miss & 1 ? 0x0000ffffu : 0u) | (miss & 2 ? 0xffff0000u : 0u));
-    if (flags & kMixed) {
-        const int k0 = d.r_first + off;  // ring row of key `off`
-        mask |= r.w0 <= r.w1 ? bits_between(r.w0 - k0, r.w1 - k0)
-                             : bits_between(-k0, r.w1 - k0) | bits_between(r.w0 - k0, win_rows - 1 - k0);
-    }
+    if ((flags & kMixed) && r.t >= 0) mask |= ring_bits(p, r.w, d.r_first + off);
     return mask;
 }
 
@@ -424,7 +486,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const AttendArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)tc::cluster_rank(), pair = blockIdx.x >> 1;
-    const bool q_rw = a.q_gain != nullptr || a.rope_cos != nullptr;
+    // the query tile is rewritten for a gain, RoPE or a negative scale (its sign goes to the rows)
+    const bool q_rw = a.q_gain != nullptr || a.rope_cos != nullptr || a.scale < 0.f;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * kSlots; ++i) {
@@ -466,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     // tile number g's description, once it is there (null: given up)
     const auto desc_of = [&](uint32_t g) -> const Tile * {
-        return mbar_wait(smem_u32(s.dfull + g % kDescs), (g / kDescs) & 1u, p.ctx, s.abort_flag) ? s.desc + g % kDescs
+        return bar_wait(smem_u32(s.dfull + g % kDescs), (g / kDescs) & 1u, p.ctx, s.abort_flag) ? s.desc + g % kDescs
                                                                                                  : nullptr;
     };
     const auto warp_desc_of = [&](uint32_t g) -> const Tile * {
@@ -574,13 +637,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (flags & kEnd) break;
                 const uint32_t b = g % kSBufs;
                 if (flags & kFirst) {
-                    if (!mbar_wait(smem_u32(s.qready), nq & 1u, p.ctx, s.abort_flag)) break;
+                    if (!bar_wait(smem_u32(s.qready), nq & 1u, p.ctx, s.abort_flag)) break;
                     ++nq;
                 }
-                if (!mbar_wait(smem_u32(s.sempty + b), ((g / kSBufs) & 1u) ^ 1u, p.ctx, s.abort_flag)) break;
+                if (!bar_wait(smem_u32(s.sempty + b), ((g / kSBufs) & 1u) ^ 1u, p.ctx, s.abort_flag)) break;
                 for (int w = 0; w < Lt::kPieces; ++w, ++it) {
                     const uint32_t sl = it % kSlots;
-                    if (!(ok = mbar_wait(smem_u32(s.full + sl), (it / kSlots) & 1u, p.ctx, s.abort_flag))) break;
+                    if (!(ok = bar_wait(smem_u32(s.full + sl), (it / kSlots) & 1u, p.ctx, s.abort_flag))) break;
                     tc::fence_after_sync();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {  // 16 dims each: chunk 2 w + k / 4
@@ -610,10 +673,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (flags & kEnd) break;
                 const uint32_t b = g & 1u, vbox = flags & kMixed ? 16 : p.vbox, vsh = 31 - __clz(vbox);
                 const uint64_t vdesc = tc::smem_desc_lbo(vslots, vbox * 128, 1024, tc::kLayoutSw128);
-                if (!mbar_wait(smem_u32(s.pfull + b), (g >> 1) & 1u, p.ctx, s.abort_flag)) break;
+                if (!bar_wait(smem_u32(s.pfull + b), (g >> 1) & 1u, p.ctx, s.abort_flag)) break;
                 for (int w = 0; w < Lt::kPieces; ++w, ++it) {
                     const uint32_t sl = it % kSlots;
-                    if (!(ok = mbar_wait(smem_u32(s.full + kSlots + sl), (it / kSlots) & 1u, p.ctx, s.abort_flag))) break;
+                    if (!(ok = bar_wait(smem_u32(s.full + kSlots + sl), (it / kSlots) & 1u, p.ctx, s.abort_flag))) break;
                     tc::fence_after_sync();
 #pragma unroll
                     for (int k = 0; k < Lt::kVKeys / 16; ++k) {  // 16 keys each
@@ -674,9 +737,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_arrive(smem_u32(s.dfull + g % kDescs), lane == 0);
             ++g;
         };
+        const int win_rows = (int)a.win_rows;
         while (un.left > 0 && ok) {
             const Queries qs = queries_of(p, un.rt);
-            const int b0 = qs.bq0 / a.nq, b1 = qs.bq1 / a.nq;
+            const int b0 = p.nq.div(qs.bq0), b1 = p.nq.div(qs.bq1);
             int vmax = 0, n = 0;
             for (int q = qs.bq0 + lane; q <= qs.bq1; q += 32) vmax = std::max(vmax, visible(p, __ldg(a.q_pos + q), p.n_shared));
             const auto query0 = [&](int b) { return std::max(qs.bq0, b * a.nq); };
@@ -690,8 +754,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int y = x - shared;  // the tile's number among its request's own ones
             Own own = {0, 0u};
             for (int j = 0; j < n; ++j, ++x, ++y) {
-                Tile *d = entry();
-                if (!d) break;
                 const bool sh = x < shared;
                 int flags = (sh ? kShared : 0) | (j == 0 ? kFirst : 0) | (j == n - 1 ? kLast : 0);
                 int ent, e_first, r_first = 0;
@@ -705,61 +767,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ++b;
                         own = own_keys(p, query0(b), query1(b));
                     }
-                    const uint32_t first = (uint32_t)y * kPrefixKeys;
-                    e_first = p.n_shared + (int)first;
-                    ent = std::min(std::max(own.n_own - (int)first, 0), +kPrefixKeys);
-                    r_first = (int)first - (int)own.ring0();
+                    const int first = y * kPrefixKeys;
+                    e_first = p.n_shared + first;
+                    ent = std::min(std::max(own.n_own - first, 0), +kPrefixKeys);
+                    r_first = first - (int)own.ring0();
                     if (r_first > -kPrefixKeys) flags |= kMixed;
                     table += (size_t)b * a.max_pages;
                 }
-                // 16 keys by lane: their first row
+                // 16 keys by lane: their first row (its page's load flies while an entry is awaited)
+                const int k16 = lane * 16, e16 = e_first + k16;
+                int id = 0, off = 0;
+                if (lane < 8 && k16 < ent) {
+                    const int pg = p.page.div(e16);
+                    off = e16 - pg * a.page;
+                    id = __ldg(table + pg);
+                }
+                Tile *d = entry();
+                if (!d) break;
                 int row = -kPrefixKeys;
                 bool missing = false, from_ring = false;
                 if (lane < 8) {
-                    const int k = lane * 16, rr = r_first + k;
-                    if (k < ent) {
-                        const uint32_t e = (uint32_t)(e_first + k), pg = e / (uint32_t)a.page;
-                        const int id = __ldg(table + pg);
+                    const int rr = r_first + k16;
+                    if (k16 < ent) {
                         missing = id < 0 || id >= a.n_pages;
-                        if (sh && p.linear) row = (int)e;
-                        else if (!missing) row = id * a.page + (int)(e - pg * (uint32_t)a.page);
-                    } else if ((flags & kMixed) && rr >= 0 && rr < a.win_rows) {
-                        row = b * (int)a.win_rows + rr;
+                        if (sh && p.linear) row = e16;
+                        else if (!missing) row = id * a.page + off;
+                    } else if ((flags & kMixed) && rr >= 0 && rr < win_rows) {
+                        row = b * win_rows + rr;
                         from_ring = true;
                     }
                     d->rows[lane] = row;
                 }
-                flags |= (int)(__ballot_sync(0xffffffffu, missing) << kMissingShift);
-                flags |= (int)(__ballot_sync(0xffffffffu, from_ring) << kRingShift);
-                // 32 keys at a time: which of them some row takes, and which others a copy brings
-                const int vb = flags & kMixed ? 16 : p.vbox;
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int k = i * 32 + lane;
-                    const int krow = __shfl_sync(0xffffffffu, row, k >> 4);
-                    const bool brought = __shfl_sync(0xffffffffu, row, (k & ~(vb - 1)) >> 4) >= 0;
-                    bool live = k < ent && krow >= 0;
-                    const int rr = r_first + k;
-                    if (!sh && k >= ent && rr >= 0 && rr < a.win_rows) {
-                        const int q1 = query1(b);
+                const uint32_t miss = __ballot_sync(0xffffffffu, missing), rings = __ballot_sync(0xffffffffu, from_ring);
+                flags |= (int)(miss << kMissingShift) | (int)(rings << kRingShift);
+                if (lane < 4) {
+                    // 32 keys by lane: which ones a copy brings that no row takes.  Of entries the
+                    // last box's rest; of window rows those in no query's window and past the ring.
+                    const int vb = flags & kMixed ? 16 : p.vbox, k32 = lane * 32;
+                    uint32_t z;
+                    if (FP8 && !sh) z = ~low_bits(ent - k32);
+                    else z = bits_between(ent - k32, ((ent + vb - 1) & -vb) - 1 - k32);
+                    const uint32_t two = rings >> (2 * lane);
+                    const uint32_t wins = (two & 1u ? 0x0000ffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
+                    if (wins) {
+                        uint32_t live = 0u;
+                        const int q1 = query1(b), k0 = r_first + k32;
                         for (int q = query0(b); q <= q1; ++q) {
                             const int t = __ldg(a.q_pos + q);
-                            if (t < 0) continue;
-                            const int back = ((int)((uint32_t)t % (uint32_t)a.win_rows) - rr + (int)a.win_rows) % (int)a.win_rows;
-                            live |= back < a.W && back <= t;
+                            if (t >= 0) live |= ring_bits(p, window_of(p, t), k0);
                         }
+                        z = (z & ~wins) | (wins & ~live);
                     }
-                    const uint32_t z = __ballot_sync(0xffffffffu, !live && (brought || (FP8 && !sh)));
-                    if (lane == 0) d->zero[i] = z;
-                    // own rows into L2, by the pair's other CTA
-                    if (live && !sh && rank == 1) {
-                        const size_t r = (size_t)krow + (k & 15);
-                        const void *src;
-                        if (FP8) src = (rr >= 0 && k >= ent ? a.win8 : a.kv8) + r * a.D;
-                        else src = (rr >= 0 && k >= ent ? a.win : a.kv) + r * a.D;
-                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(FP8 ? a.D : 2 * a.D)
-                                     : "memory");
-                    }
+                    d->zero[lane] = z;
                 }
                 if (lane == 0) {
                     d->flags = flags;
@@ -770,6 +829,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     d->r_first = r_first;
                 }
                 publish();
+                if (sh || rank == 0) continue;
+                // own rows into L2, by the pair's other CTA
+#pragma unroll 1
+                for (int k = lane; k < kPrefixKeys; k += 32) {
+                    const int krow = __shfl_sync(0xffffffffu, row, k >> 4), rr = r_first + k;
+                    if (krow < 0 || (k < ent ? false : rr >= win_rows)) continue;
+                    const size_t r = (size_t)krow + (k & 15);
+                    const bool ring = (rings >> (k >> 4)) & 1u;
+                    if (!ring && k >= ent) continue;
+                    const void *src = FP8 ? (const void *)((ring ? a.win8 : a.kv8) + r * a.D)
+                                          : (const void *)((ring ? a.win : a.kv) + r * a.D);
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(FP8 ? a.D : 2 * a.D) : "memory");
+                }
             }
             ++un.rt;
             un.x = 0;
@@ -795,9 +867,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t sempty0 = tc::map_to_rank(smem_u32(s.sempty), 0), pfull0 = tc::map_to_rank(smem_u32(s.pfull), 0);
         const uint32_t qready0 = tc::map_to_rank(smem_u32(s.qready), 0);
-        const int n_rows = (int)(a.n_bq * a.H), win_rows = (int)a.win_rows;
+        const int n_rows = (int)(a.n_bq * a.H);
         uint32_t nq = 0;
-        Row rw = {-1, 0, 0, 0, -1};
+        Row rw = {-1, 0, 0, {0, 0}};
+        int vis_min = 0;  // the fewest entries that a row of this warp sees
         float rq = 0.f, m_run = -INFINITY, l = 0.f;
         const auto wait = [&](uint64_t *bar, uint32_t parity) {
             return warp_wait(smem_u32(bar), parity, p.ctx, s.abort_flag);
@@ -810,12 +883,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const size_t part = (size_t)pair + d.rt;
             if (flags & kFirst) {  // a new row tile
                 const int row = d.rt * kPrefixRows + rank * 64 + r;
-                const int bq = row < n_rows ? row / a.H : 0;
+                const int bq = row < n_rows ? p.H.div(row) : 0;
                 rw.t = row < n_rows ? __ldg(a.q_pos + bq) : -1;
-                rw.b = bq / a.nq;
+                rw.b = p.nq.div(bq);
                 rw.vis = visible(p, rw.t, (int)a.N);
-                rw.w0 = rw.t < 0 ? win_rows : (int)((uint32_t)std::max(0, rw.t - a.W + 1) % (uint32_t)win_rows);
-                rw.w1 = rw.t < 0 ? -1 : (int)((uint32_t)rw.t % (uint32_t)win_rows);
+                rw.w = window_of(p, std::max(rw.t, 0));
+                vis_min = __reduce_min_sync(0xffffffffu, rw.vis);
                 if (!wait(s.qland, nq & 1u)) break;
                 ++nq;
                 xch[q4 * 32 + lane] = query_squares<DP>(s.q, r, q4);
@@ -829,16 +902,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(s.qempty), lane == 0);
                 if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
                 const float ss = (xch[lane] + xch[32 + lane]) + (xch[64 + lane] + xch[96 + lane]);
-                // 1 / RMS times the softmax scale, in log2 units
-                rq = (1.0f / sqrtf(ss / (float)a.D + a.eps)) * a.scale * 1.4426950408889634f;
+                // 1 / RMS times the softmax scale (without its sign), in log2 units; above 0, so that a
+                // masked score stays -inf
+                rq = fmaxf((1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
                 m_run = -INFINITY;
                 l = 0.f;
                 if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
             }
             if ((g & 1u) == (uint32_t)wg) {
                 const uint32_t b = g & 1u, ph = (g >> 1) & 1u, sb = g % kSBufs;
-                const uint32_t mk0 = key_mask(d, hf * 64, rw, win_rows), mk1 = key_mask(d, hf * 64 + 32, rw, win_rows);
-                const bool whole = __all_sync(0xffffffffu, (mk0 & mk1) == 0xffffffffu);
+                uint32_t mk0 = 0xffffffffu, mk1 = 0xffffffffu;  // keys that take part
+                bool whole = (flags & (kShared | 0xff << kMissingShift)) == kShared && d.ent == kPrefixKeys &&
+                             d.e_first + kPrefixKeys <= vis_min;
+                if (!whole) {
+                    mk0 = key_mask(p, d, hf * 64, rw);
+                    mk1 = key_mask(p, d, hf * 64 + 32, rw);
+                    whole = __all_sync(0xffffffffu, (mk0 & mk1) == 0xffffffffu);
+                }
                 if (!wait(s.sfull + sb, (g / kSBufs) & 1u)) break;
                 tc::fence_after_sync();
                 float sc[64];
@@ -848,22 +928,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 mbar_arrive_cluster(sempty0 + sb * 8, lane == 0);
-                // the largest scaled score: the largest raw one, or the smallest under a negative scale
-                float mt = -INFINITY;
-                if (whole && rq >= 0.f) {
-                    float m2 = sc[1];
-                    mt = sc[0];
+                if (!whole) {
 #pragma unroll
-                    for (int i = 2; i < 64; i += 2) {
-                        mt = fmaxf(mt, sc[i]);
-                        m2 = fmaxf(m2, sc[i + 1]);
-                    }
-                    mt = fmaxf(mt, m2) * rq;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        mt = fmaxf(mt, ((i < 32 ? mk0 : mk1) >> (i & 31)) & 1u ? sc[i] * rq : -INFINITY);
+                    for (int i = 0; i < 64; ++i) sc[i] = ((i < 32 ? mk0 : mk1) >> (i & 31)) & 1u ? sc[i] : -INFINITY;
                 }
+                float m2[2] = {sc[0], sc[1]};
+#pragma unroll
+                for (int i = 2; i < 64; i += 2) {
+                    m2[0] = fmaxf(m2[0], sc[i]);
+                    m2[1] = fmaxf(m2[1], sc[i + 1]);
+                }
+                float mt = fmaxf(m2[0], m2[1]) * rq;
                 // The row's maximum over its two threads, each rounded to 16 bits towards zero (any
                 // reference near the maximum serves, as long as all agree).  The reference of the tile
                 // before is final once the other group says so; by then this group has read its own
@@ -908,11 +983,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float e[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) e[i] = exp2_ftz(fmaf(sc[x * 8 + i], rq, -mref));
-                    if (!whole) {
-                        const uint32_t mk = (x < 4 ? mk0 : mk1) >> (x * 8 & 31);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) e[i] = (mk >> i) & 1u ? e[i] : 0.f;
-                    }
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
                         ps[0] += e[i];
@@ -1008,6 +1078,11 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     p.part = x.part;
     p.ml = x.ml;
     p.first = x.first;
+    p.H = FastDiv::by((uint32_t)x.a.H);
+    p.nq = FastDiv::by((uint32_t)x.a.nq);
+    p.m = FastDiv::by((uint32_t)x.a.m);
+    p.page = FastDiv::by((uint32_t)x.a.page);
+    p.ring = FastDiv::by((uint32_t)x.a.win_rows);
     p.ctx = ctx;
     p.idesc_qk = idesc(kPrefixKeys, false);
     p.idesc_pv = idesc(Layout<DP>::kPvN, true);
