@@ -60,7 +60,6 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kProducers = 4, kQkWarp = 4, kPvWarp = 5, kQueryWarp = 6, kPlanWarp = 7, kSoftWarp0 = 8, kSoftWarps = 8;
 constexpr int kSlots = 4;  // of each ring
-constexpr int kDescs = 6;  // tiles described ahead
 constexpr uint32_t kSlotBytes = 16384;  // K: 64 keys x 128 dims, V: 16384 / DP keys x DP / 2 dims
 constexpr uint32_t kPBytes = 16384;     // 64 rows x 128 keys, bf16
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -74,6 +73,7 @@ struct Layout {
     static constexpr int kPvMmas = DP / kPvN;             // MMAs per 16 keys
     static constexpr int kVKeys = 16384 / DP;             // keys of a V slot
     static constexpr int kVChunks = DP / 128;             // its 64-dim chunks (this SM's half of V's columns)
+    static constexpr int kDescs = DP < 512 ? 16 : 8;      // tiles described ahead (8: what shared memory is left)
     static constexpr uint32_t kQBytes = 64 * DP * 2;      // [DP/64][64 rows][128 B]
 };
 
@@ -113,27 +113,26 @@ struct Params {
 
 // One tile of 128 keys, as the planner describes it.
 enum : int { kShared = 1, kFirst = 2, kLast = 4, kEnd = 8, kMixed = 16, kMissingShift = 8, kRingShift = 16 };
-struct __align__(16) Tile {
+struct Tile {
     int flags;         // kShared: entries of all requests, else own keys of request b; kFirst / kLast of a pair's
                        // part of a row tile; kEnd: no tile; kMixed: window rows among the keys.  Of keys 16 i ..
                        // 16 i + 15, bit kMissingShift + i: entries without a page, kRingShift + i: window rows
-    int rt;            // row tile
+    int ent_rt;        // keys [0, ent) are entries that some row sees; the row tile: ent | rt << 8
     int b;
     int e_first;       // entry index of key 0
-    int ent;           // keys [0, ent) are entries that some row sees
     int r_first;       // ring row of key 0 (kMixed: keys from -r_first on, where that is positive)
     int rows[8];       // row of key 16 i in the pool, the rings or (linear) the copy; < 0: none, reads as zeros
     uint32_t zero[4];  // keys that a copy brings (FP8 own keys: any) and no row takes: cleared in V
-    int pad[2];
+    CSA_DEVINL int ent() const { return ent_rt & 255; }
+    CSA_DEVINL int rt() const { return ent_rt >> 8; }
 };
 
 struct Smem {
     uint8_t *q, *slots, *p;  // slots: K's ring, then V's; so are their barriers
-    uint64_t *full, *empty, *sfull, *sempty, *pfull, *pvdone, *qland, *qready, *qempty, *vfix, *dfull, *dempty, *mdec, *rbar, *xbar;
-    Tile *desc;      // [kDescs]
+    uint64_t *full, *empty, *sfull, *sempty, *pfull, *pvdone, *qland, *qready, *qempty, *vfix, *dfull, *dempty, *rbar, *xbar;
+    Tile *desc;  // [kDescs]
     // Per 32 rows, [2][128] floats: sums of a row's four threads [4][32] before and after its tiles;
-    // during them its running maximum after tile g at mref[(g & 1) * 32 + row], and the upper halves of
-    // a tile's maxima, xmax[(group * 2 + half) * 32 + row] (uint16, after the 64 floats of mref)
+    // during them the upper halves of its maxima in tile g, uint16 [4: g % 4][2 halves of the keys][32]
     float *xch;
     uint32_t *tmem_slot;
     int *abort_flag;
@@ -147,18 +146,17 @@ CSA_DEVINL Smem carve(uint8_t *raw) {
     s.p = s.slots + 2 * kSlots * kSlotBytes;
     s.xch = reinterpret_cast<float *>(s.p + 2 * kPBytes);
     s.desc = reinterpret_cast<Tile *>(s.xch + 256);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(s.desc + kDescs);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(s.desc + Layout<DP>::kDescs);
     s.full = bars;
     s.empty = s.full + 2 * kSlots;
     s.dfull = s.empty + 2 * kSlots;
-    s.dempty = s.dfull + kDescs;
-    s.sfull = s.dempty + kDescs;
+    s.dempty = s.dfull + Layout<DP>::kDescs;
+    s.sfull = s.dempty + Layout<DP>::kDescs;
     s.sempty = s.sfull + kSBufs;
     s.pfull = s.sempty + kSBufs;
     s.pvdone = s.pfull + 2;
-    s.mdec = s.pvdone + 2;
-    s.rbar = s.mdec + 2;  // [2 x 32 rows]
-    s.xbar = s.rbar + 2;  // [2 groups][2 x 32 rows]
+    s.rbar = s.pvdone + 2;  // [2 x 32 rows]
+    s.xbar = s.rbar + 2;    // [tile parity = group][2 x 32 rows]
     s.qland = s.xbar + 4;
     s.qready = s.qland + 1;
     s.qempty = s.qready + 1;
@@ -170,8 +168,8 @@ CSA_DEVINL Smem carve(uint8_t *raw) {
 
 template <int DP>
 constexpr size_t smem_bytes() {
-    return 1024 + Layout<DP>::kQBytes + 2 * kSlots * kSlotBytes + 2 * kPBytes + 1024 + kDescs * sizeof(Tile) +
-           (4 * kSlots + 2 * kDescs + 2 * kSBufs + 17) * 8 + 8;
+    return 1024 + Layout<DP>::kQBytes + 2 * kSlots * kSlotBytes + 2 * kPBytes + 1024 + Layout<DP>::kDescs * sizeof(Tile) +
+           (4 * kSlots + 2 * Layout<DP>::kDescs + 2 * kSBufs + 15) * 8 + 8;
 }
 static_assert(smem_bytes<512>() <= 227 * 1024, "shared memory of one CTA");
 
@@ -412,7 +410,7 @@ struct Row {
 CSA_DEVINL uint32_t key_mask(const Params &p, const Tile &d, int off, const Row &r) {
     const int flags = d.flags;
     if (!(flags & kShared) && r.b != d.b) return 0u;
-    uint32_t mask = low_bits(std::min(r.vis - d.e_first, d.ent) - off);
+    uint32_t mask = low_bits(std::min(r.vis - d.e_first, d.ent()) - off);
     const int miss = flags >> (kMissingShift + off / 16);
     mask &= ~((miss & 1 ? 0x0000ffffu : 0u) | (miss & 2 ? 0xffff0000u : 0u));
     if ((flags & kMixed) && r.t >= 0) mask |= ring_bits(p, r.w, d.r_first + off);
@@ -481,6 +479,7 @@ template <int DP, bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_prefix_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     using Lt = Layout<DP>;
+    constexpr uint32_t kDescs = Lt::kDescs;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const Smem s = carve<DP>(smem_raw);
     const AttendArgs &a = p.a;
@@ -501,17 +500,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(s.pfull + i, kSoftWarps);  // leader: the same
             mbar_init(s.pvdone + i, 1);
-            mbar_init(s.mdec + i, kSoftWarps / 2);
             mbar_init(s.rbar + i, kSoftWarps / 2);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(s.xbar + i, 2);
+        for (int i = 0; i < 4; ++i) mbar_init(s.xbar + i, 2);  // the two warps of 32 rows in a group
         mbar_init(s.qland, 1);
         mbar_init(s.qready, q_rw ? 2 * kSoftWarps : 2);  // leader
         mbar_init(s.qempty, 1 + kSoftWarps);
         for (int i = 0; i < 2; ++i) mbar_init(s.vfix + i, 1);
         for (int i = 0; i < kDescs; ++i) {
             mbar_init(s.dfull + i, 1);
-            mbar_init(s.dempty + i, kSoftWarps + 1);  // and the query tiles' warp
+            mbar_init(s.dempty + i, kSoftWarps + (rank == 0 ? 1 : 2));  // and the query tiles', the prefetching warp
         }
         *s.abort_flag = 0;
         fence_mbar_init();
@@ -519,6 +517,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::prefetch_tmap(&maps.k);
         tc::prefetch_tmap(&maps.v);
     }
+    Units un = {0, 0, 0};
+    if (warp == kPlanWarp) un = deal_units(p, pair, blockIdx.x == 0);
     if (warp == kQueryWarp) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
     tc::fence_before_sync();
     __syncthreads();
@@ -609,13 +609,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!(ok = warp_wait(vfix, nfix & 1u, p.ctx, s.abort_flag))) break;
                     ++nfix;
                     // key e of the slot, chunk c: [e / vbox][c][e % vbox][128 B]
-                    uint4 *slot = reinterpret_cast<uint4 *>(s.slots + (ring + sl) * kSlotBytes);
                     const int vsh = 31 - __clz(vbox);
 #pragma unroll 1
-                    for (int y = lane; y < Lt::kVKeys * Lt::kVChunks * 8; y += 32) {
-                        const int line = y >> 3, e = w * Lt::kVKeys + (line >> vsh) / Lt::kVChunks * vbox + (line & (vbox - 1));
-                        if ((d.zero[e >> 5] >> (e & 31)) & 1u) slot[y] = make_uint4(0u, 0u, 0u, 0u);
-                    }
+                    for (int i = 0; i < Lt::kVKeys / 32; ++i)
+                        for (uint32_t z = d.zero[w * (Lt::kVKeys / 32) + i]; z; z &= z - 1) {
+                            const int e = i * 32 + __ffs(z) - 1;
+                            const uint32_t line = ((((uint32_t)(e >> vsh) * Lt::kVChunks + (lane >> 3)) << vsh) + (e & (vbox - 1)));
+                            if (lane < Lt::kVChunks * 8)
+                                *reinterpret_cast<uint4 *>(s.slots + (ring + sl) * kSlotBytes + line * 128 + (lane & 7) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        }
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     mbar_arrive_cluster(full, lane == 0);
@@ -695,6 +698,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc::mma_commit_2sm(smem_u32(s.pvdone + b));
             }
         }
+        else if (rank == 1) {
+            // -------------------------------------------------------- own rows into L2
+            const int lines = (FP8 ? a.D : 2 * a.D) / 128, lsh = 31 - __clz(lines);  // of 128 bytes per row
+            for (uint32_t g = 0;; ++g) {
+                const Tile *d = warp_desc_of(g);
+                if (!d) break;
+                const int flags = d->flags;
+                if (!(flags & (kEnd | kShared)))
+#pragma unroll 1
+                    for (int x = lane; x < kPrefixKeys << lsh; x += 32) {
+                        const int k = x >> lsh, line = x & (lines - 1), row = d->rows[k >> 4];
+                        const bool ring = (flags >> (kRingShift + (k >> 4))) & 1;
+                        if (row < 0 || ((d->zero[k >> 5] >> (k & 31)) & 1u)) continue;
+                        const uint8_t *base = FP8 ? (ring ? a.win8 : a.kv8)
+                                                  : reinterpret_cast<const uint8_t *>(ring ? a.win : a.kv);
+                        const uint8_t *src = base + ((size_t)row + (k & 15)) * (FP8 ? a.D : 2 * a.D) + line * 128;
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+                    }
+                __syncwarp();
+                mbar_arrive(smem_u32(s.dempty + g % kDescs), lane == 0);
+                if (flags & kEnd) break;
+            }
+        }
     } else if (warp == kQueryWarp) {
         // ------------------------------------------------------------ query tiles
         const uint32_t qland = tc::map_to_rank(smem_u32(s.qland), rank), qready0 = tc::map_to_rank(smem_u32(s.qready), 0);
@@ -703,7 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (uint32_t g = 0; ok; ++g) {
             const Tile *d = warp_desc_of(g);
             if (!(ok = d != nullptr)) break;
-            const int flags = d->flags, row = d->rt * kPrefixRows + rank * 64;
+            const int flags = d->flags, row = d->rt() * kPrefixRows + rank * 64;
             __syncwarp();
             mbar_arrive(smem_u32(s.dempty + g % kDescs), lane == 0);
             if (flags & kEnd) break;
@@ -722,14 +748,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         copies = !ok;
     } else if (warp == kPlanWarp) {
         // ------------------------------------------------------------ planner
-        Units un = deal_units(p, pair, blockIdx.x == 0);
         uint32_t g = 0;
         bool ok = true;
         // An entry is free for tile g once tile g - kDescs is done with everywhere: once the
         // softmax warps are done with tile g - kDescs + 2, whose P went where the P of that tile was.
         const auto entry = [&]() -> Tile * {
-            const int h = (int)g - kDescs + 2;
-            if (h >= 0) ok = warp_wait(smem_u32(s.dempty + h % kDescs), (uint32_t)(h / kDescs) & 1u, p.ctx, s.abort_flag);
+            if (g + 2 >= kDescs) ok = warp_wait(smem_u32(s.dempty + (g + 2) % kDescs), ((g + 2) / kDescs + 1) & 1u, p.ctx, s.abort_flag);
             return ok ? s.desc + g % kDescs : nullptr;
         };
         const auto publish = [&] {
@@ -822,26 +846,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) {
                     d->flags = flags;
-                    d->rt = un.rt;
+                    d->ent_rt = ent | un.rt << 8;
                     d->b = b;
                     d->e_first = e_first;
-                    d->ent = ent;
                     d->r_first = r_first;
                 }
                 publish();
-                if (sh || rank == 0) continue;
-                // own rows into L2, by the pair's other CTA
-#pragma unroll 1
-                for (int k = lane; k < kPrefixKeys; k += 32) {
-                    const int krow = __shfl_sync(0xffffffffu, row, k >> 4), rr = r_first + k;
-                    if (krow < 0 || (k < ent ? false : rr >= win_rows)) continue;
-                    const size_t r = (size_t)krow + (k & 15);
-                    const bool ring = (rings >> (k >> 4)) & 1u;
-                    if (!ring && k >= ent) continue;
-                    const void *src = FP8 ? (const void *)((ring ? a.win8 : a.kv8) + r * a.D)
-                                          : (const void *)((ring ? a.win : a.kv) + r * a.D);
-                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(FP8 ? a.D : 2 * a.D) : "memory");
-                }
             }
             ++un.rt;
             un.x = 0;
@@ -861,9 +871,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int r = tl & 63, hf = tl >> 6;    // row of this CTA's 64; first / second half of the columns
         const int q4 = hf * 2 + wg;             // which of the row's four threads
         float *xch = s.xch + (quarter & 1) * 128;       // of these 32 rows
-        uint16_t *xmax = reinterpret_cast<uint16_t *>(xch + 64) + wg * 64;
-        const uint32_t rbar = smem_u32(s.rbar + (quarter & 1)), xbar = smem_u32(s.xbar + wg * 2 + (quarter & 1));
-        uint32_t rbar_n = 0, xbar_n = 0;
+        uint16_t *xmax = reinterpret_cast<uint16_t *>(xch);
+        const uint32_t rbar = smem_u32(s.rbar + (quarter & 1)), xbar = smem_u32(s.xbar + (quarter & 1));  // + 16 * group
+        uint32_t rbar_n = 0;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t sempty0 = tc::map_to_rank(smem_u32(s.sempty), 0), pfull0 = tc::map_to_rank(smem_u32(s.pfull), 0);
         const uint32_t qready0 = tc::map_to_rank(smem_u32(s.qready), 0);
@@ -871,7 +881,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t nq = 0;
         Row rw = {-1, 0, 0, {0, 0}};
         int vis_min = 0;  // the fewest entries that a row of this warp sees
-        float rq = 0.f, m_run = -INFINITY, l = 0.f;
+        // The rows' reference m follows the maxima of all tiles, of either group; l is relative to m_l.
+        float rq = 0.f, m = -INFINITY, m_l = -INFINITY, l = 0.f;
+        const auto tile_max = [&](uint32_t g) {  // of the row, once xbar says so
+            return fmaxf(__uint_as_float((uint32_t)xmax[(g & 3u) * 64 + lane] << 16),
+                         __uint_as_float((uint32_t)xmax[(g & 3u) * 64 + 32 + lane] << 16));
+        };
+        const auto raise = [](float m0, float mt) { return m0 == -INFINITY || mt > m0 + kRescaleThreshold ? mt : m0; };
         const auto wait = [&](uint64_t *bar, uint32_t parity) {
             return warp_wait(smem_u32(bar), parity, p.ctx, s.abort_flag);
         };
@@ -880,9 +896,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!dp || (dp->flags & kEnd)) break;
             const Tile &d = *dp;
             const int flags = d.flags;
-            const size_t part = (size_t)pair + d.rt;
+            const size_t part = (size_t)pair + d.rt();
             if (flags & kFirst) {  // a new row tile
-                const int row = d.rt * kPrefixRows + rank * 64 + r;
+                const int row = d.rt() * kPrefixRows + rank * 64 + r;
                 const int bq = row < n_rows ? p.H.div(row) : 0;
                 rw.t = row < n_rows ? __ldg(a.q_pos + bq) : -1;
                 rw.b = p.nq.div(bq);
@@ -905,14 +921,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // 1 / RMS times the softmax scale (without its sign), in log2 units; above 0, so that a
                 // masked score stays -inf
                 rq = fmaxf((1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
-                m_run = -INFINITY;
+                m = m_l = -INFINITY;
                 l = 0.f;
                 if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
             }
             if ((g & 1u) == (uint32_t)wg) {
                 const uint32_t b = g & 1u, ph = (g >> 1) & 1u, sb = g % kSBufs;
                 uint32_t mk0 = 0xffffffffu, mk1 = 0xffffffffu;  // keys that take part
-                bool whole = (flags & (kShared | 0xff << kMissingShift)) == kShared && d.ent == kPrefixKeys &&
+                bool whole = (flags & (kShared | 0xff << kMissingShift)) == kShared && d.ent() == kPrefixKeys &&
                              d.e_first + kPrefixKeys <= vis_min;
                 if (!whole) {
                     mk0 = key_mask(p, d, hf * 64, rw);
@@ -940,26 +956,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 float mt = fmaxf(m2[0], m2[1]) * rq;
                 // The row's maximum over its two threads, each rounded to 16 bits towards zero (any
-                // reference near the maximum serves, as long as all agree).  The reference of the tile
-                // before is final once the other group says so; by then this group has read its own
-                // last maxima, too.
-                if (g > 0 && !wait(s.mdec + ((g - 1) & 1u), ((g - 1) >> 1) & 1u)) break;
-                xmax[hf * 32 + lane] = (uint16_t)(__float_as_uint(mt) >> 16);
-                if (!warps_meet(xbar, xbar_n, p.ctx, s.abort_flag)) break;
-                mt = fmaxf(__uint_as_float((uint32_t)xmax[lane] << 16), __uint_as_float((uint32_t)xmax[32 + lane] << 16));
-                const float m_old = flags & kFirst ? -INFINITY : xch[(b ^ 1u) * 32 + lane];
-                const bool mine = m_old != -INFINITY && mt > m_old + kRescaleThreshold;
-                const float m_new = mine || m_old == -INFINITY ? mt : m_old;
-                if (hf == 0) xch[b * 32 + lane] = m_new;
+                // reference near the maximum serves, as long as all four agree).  A slot of the
+                // maxima is used again four tiles on: by then the other group, which has given
+                // those of the tile before, has read it.
+                if (g > 0 && !warp_wait(xbar + (b ^ 1u) * 16, ((g - 1) >> 1) & 1u, p.ctx, s.abort_flag)) break;
+                xmax[(g & 3u) * 64 + hf * 32 + lane] = (uint16_t)(__float_as_uint(mt) >> 16);
                 __syncwarp();
-                mbar_arrive(smem_u32(s.mdec + b), lane == 0);
+                mbar_arrive(xbar + b * 16, lane == 0);
+                if (g > 0 && !(flags & kFirst)) m = raise(m, tile_max(g - 1));
+                if (!warp_wait(xbar + b * 16, ph, p.ctx, s.abort_flag)) break;
+                mt = tile_max(g);
+                const float m_old = m;
+                const bool mine = m != -INFINITY && mt > m + kRescaleThreshold;
+                m = raise(m, mt);
                 // P buffer b was read by the P.V of tile g - 2
                 if (!wait(s.pvdone + b, ph ^ 1u)) break;
                 if (__any_sync(0xffffffffu, mine)) {
                     const uint32_t gp = g - 1;  // O after the P.V of the tile before
                     if (!wait(s.pvdone + (gp & 1u), (gp >> 1) & 1u)) break;
                     tc::fence_after_sync();
-                    const float f = mine ? exp2f(m_old - m_new) : 1.0f;
+                    const float f = mine ? exp2f(m_old - m) : 1.0f;
 #pragma unroll 1
                     for (int c = 0; c < DP / 2; c += 16) {
                         float v[16];
@@ -971,11 +987,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     tc::tmem_wait_st();
                 }
-                if (m_run != m_new) {  // this thread's sum is relative to m_run
-                    if (m_run != -INFINITY) l *= exp2f(m_run - m_new);
-                    m_run = m_new;
+                if (m_l != m) {
+                    if (m_l != -INFINITY) l *= exp2f(m_l - m);
+                    m_l = m;
                 }
-                const float mref = m_new == -INFINITY ? 0.f : m_new;
+                const float mref = m == -INFINITY ? 0.f : m;
                 uint8_t *prow = s.p + b * kPBytes + hf * 8192 + r * 128;
                 float ps[2] = {0.f, 0.f};
 #pragma unroll
@@ -1000,13 +1016,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_arrive(smem_u32(s.dempty + g % kDescs), lane == 0);
             if (flags & kLast) {
                 const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
-                if ((g & 1u) != (uint32_t)wg) {  // the reference is final; the phase before the one awaited is over
-                    if (!wait(s.mdec + b, ph) || !wait(s.pvdone + b, ph ^ 1u)) break;
+                if ((g & 1u) != (uint32_t)wg) {  // the last tile's maxima, too; the phase before the one awaited is over
+                    if (!warp_wait(xbar + b * 16, ph, p.ctx, s.abort_flag) || !wait(s.pvdone + b, ph ^ 1u)) break;
+                    m = raise(m, tile_max(g));
                 }
                 if (!wait(s.pvdone + b, ph)) break;
                 tc::fence_after_sync();
-                const float m = xch[b * 32 + lane];
-                if (m_run != m && m_run != -INFINITY) l *= exp2f(m_run - m);
+                if (m_l != m && m_l != -INFINITY) l *= exp2f(m_l - m);
                 if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
                 xch[q4 * 32 + lane] = l;
                 if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
