@@ -418,8 +418,8 @@ static int validate_paged(const csa::PagedArgs &a) {
 }
 
 static int run_paged(const csa::PagedArgs &a, void *workspace, size_t workspace_bytes, void *stream) {
-    const size_t need = csa::attend_paged_workspace_bytes(a.batch, a.nq, a.H, a.D, a.page, a.max_pages, a.n_shared, a.W,
-                                                          a.fp8.kv != nullptr);
+    const size_t need = csa::attend_paged_workspace_bytes(a.batch, a.nq, a.H, a.D, a.page, a.max_pages, a.n_shared,
+                                                          a.ring_rows, a.W, a.fp8.kv != nullptr);
     if (need > 0 && (!al16(workspace) || workspace_bytes < need)) return CSA_ERR_WORKSPACE;
     csa::DevCtx ctx;
     if (!ctx_for_launch(&ctx)) return CSA_ERR_CUDA;
@@ -427,11 +427,11 @@ static int run_paged(const csa::PagedArgs &a, void *workspace, size_t workspace_
 }
 
 size_t csa_attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared,
-                                        int W, int fp8) {
-    if (batch < 1 || nq < 1 || H < 1 || H > 128 || page < 1 || max_pages < 1 || n_shared < 0 || W < 1 ||
-        !(D == 64 || D == 128 || D == 256 || D == 512))
+                                        int ring_rows, int W, int fp8) {
+    if (batch < 1 || nq < 1 || H < 1 || H > 128 || page < 1 || max_pages < 1 || n_shared < 0 || ring_rows < 1 || W < 1 ||
+        !(D == 64 || D == 128 || D == 256 || D == 512) || n_shared > (long long)max_pages * page)
         return 0;
-    return csa::attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, W, fp8 != 0);
+    return csa::attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, ring_rows, W, fp8 != 0);
 }
 
 int hca_attend_paged(const uint16_t *q, const float *q_gain, const float *sinks, const float *rope_cos,

@@ -99,17 +99,17 @@ struct PrefixArgs {
     AttendArgs a;          // of the whole call
     PrefixPlan plan;
     long long n_shared;
-    const uint16_t *keys;  // the entries' rows: the pool, or (linear) rows 0..n_shared-1 in order
-    bool linear;
+    // The entries' rows: the pool; or (own_cap >= 0) a bf16 copy of an FP8 cache: rows of the shared
+    // entries in order, then own_cap rows of each request's own entries, then the rings
+    const uint16_t *keys;
+    int own_cap;
     float *part;           // [partials][128][DP], see above
     float2 *ml;            // [partials][128]
     int *first;            // [row_tiles + 1] first unit of every row tile, and the units of all (out)
 };
 
 PrefixPlan prefix_plan(long long rows);
-// entries 0..n_shared-1 of an FP8 pool, in order, as bf16 rows
-int launch_prefix_rows(const uint8_t *codes, const uint8_t *exps, const int *table, int page, long long n_pages, int D,
-                       long long n_shared, uint16_t *out, cudaStream_t st);
+int launch_expand_rows(const PrefixArgs &p, uint16_t *out, cudaStream_t st);  // that copy
 int launch_attend_prefix(const PrefixArgs &p, const DevCtx &ctx, cudaStream_t st);
 
 }  // namespace csa

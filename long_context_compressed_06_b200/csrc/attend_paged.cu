@@ -130,13 +130,21 @@ size_t take(size_t &at, size_t bytes) {
     return o;
 }
 
-PagedPlan paged_plan(long long n_bq, int H, int D, int page, int max_pages, long long n_shared, int W, bool fp8) {
+// The most that a bf16 copy of an FP8 cache's rows may take; beyond it the gather kernel reads the codes in place.
+constexpr long long kMaxCopyBytes = 1LL << 30;
+
+PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared, int ring_rows, int W,
+                     bool fp8) {
     PagedPlan pl = {};
-    const long long rows = n_bq * H, cap = (long long)max_pages * page;
+    const long long n_bq = (long long)batch * nq, rows = n_bq * H, cap = (long long)max_pages * page;
+    const long long copy = fp8 ? (n_shared + batch * (cap - n_shared + ring_rows)) * D * (long long)sizeof(uint16_t) : 0;
+    // units are counted in 32 bits: shared tiles and, of each request in a row tile, own ones
+    const long long tiles = n_shared / kPrefixKeys + 1 + (1 + kPrefixRows / H) * ((cap - n_shared + ring_rows) / kPrefixKeys + 2);
     size_t at = 0;
-    if (n_shared > 0 && rows <= 0x7fffffffLL - kPrefixRows) {
+    if (n_shared > 0 && rows <= 0x7fffffffLL - kPrefixRows && copy <= kMaxCopyBytes &&
+        tiles <= 0x7fffffffLL / (rows / kPrefixRows + 1)) {
         pl.prefix = prefix_plan(rows);
-        if (fp8) pl.keys = take(at, (size_t)n_shared * D * sizeof(uint16_t));
+        if (fp8) pl.keys = take(at, (size_t)copy);
         pl.part = take(at, (size_t)pl.prefix.partials() * kPrefixRows * prefix_dims(D) * sizeof(float));
         pl.ml = take(at, (size_t)pl.prefix.partials() * kPrefixRows * sizeof(float2));
         pl.first = take(at, (size_t)(pl.prefix.row_tiles + 1) * sizeof(int));
@@ -153,9 +161,9 @@ PagedPlan paged_plan(long long n_bq, int H, int D, int page, int max_pages, long
 
 }  // namespace
 
-size_t attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared, int W,
-                                    bool fp8) {
-    return paged_plan((long long)batch * nq, H, D, page, max_pages, n_shared, W, fp8).bytes;
+size_t attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared,
+                                    int ring_rows, int W, bool fp8) {
+    return paged_plan(batch, nq, H, D, page, max_pages, n_shared, ring_rows, W, fp8).bytes;
 }
 
 int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const DevCtx &ctx, cudaStream_t st) {
@@ -169,7 +177,7 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     a.table = p.table; a.max_pages = p.max_pages; a.page = p.page; a.n_pages = p.n_pages;
     a.win_rows = p.ring_rows; a.W = p.W; a.q_pos = p.q_pos; a.nq = p.nq; a.n_bq = (long long)p.batch * p.nq;
     a.H = p.H; a.D = p.D; a.scale = p.scale; a.eps = p.eps; a.out = p.out;
-    const PagedPlan pl = paged_plan(a.n_bq, a.H, a.D, a.page, a.max_pages, p.n_shared, a.W, fp8);
+    const PagedPlan pl = paged_plan(p.batch, a.nq, a.H, a.D, a.page, a.max_pages, p.n_shared, p.ring_rows, a.W, fp8);
     if (pl.bytes > 0 && (!ws || ws_bytes < pl.bytes)) return CSA_ERR_WORKSPACE;
     char *w = static_cast<char *>(ws);
     a.splits = pl.splits;
@@ -178,18 +186,15 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     g.a = a;
     int rc;
     if (pl.prefix.pairs > 0) {
-        // the units are counted in 32 bits
-        const long long requests = 1 + kPrefixRows / a.H, own = (a.N - p.n_shared + a.win_rows) / kPrefixKeys + 2;
-        if ((p.n_shared / kPrefixKeys + 1 + requests * own) > 0x7fffffffLL / pl.prefix.row_tiles) return CSA_ERR_UNSUPPORTED;
         PrefixArgs x = {};
         x.a = a;
         x.plan = g.plan = pl.prefix;
         x.n_shared = p.n_shared;
         x.keys = p.pool;
-        x.linear = fp8;
+        x.own_cap = fp8 ? (int)(a.N - p.n_shared) : -1;
         if (fp8) {
             uint16_t *keys = reinterpret_cast<uint16_t *>(w + pl.keys);
-            rc = launch_prefix_rows(a.kv8, a.kv8e, a.table, a.page, a.n_pages, a.D, p.n_shared, keys, st);
+            rc = launch_expand_rows(x, keys, st);
             if (rc != CSA_OK) return rc;
             x.keys = keys;
         }

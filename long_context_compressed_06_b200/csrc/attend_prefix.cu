@@ -39,9 +39,10 @@
 // K and V have a ring of 16 KiB slots each; every tile passes through both, and
 // two producer warps take a ring's positions in turn.  Rows arrive by TMA,
 // entries in boxes that never cross a page, window rows 16 at a time in the
-// order of the ring; FP8 own rows are expanded by the producers.  (A slot's
-// phase bit tells its use from the one before only: whoever waits on a ring
-// passes every use.)
+// order of the ring; FP8 rows are expanded to a bf16 copy by a launch before
+// (expanding them in the producers took ~12K cycles a tile).  (A slot's phase
+// bit tells its use from the one before only: whoever waits on a ring passes
+// every use.)
 //
 // The tiles of all row tiles ("units") are counted on the device from the
 // positions and dealt to the pairs in balanced contiguous ranges.
@@ -103,6 +104,9 @@ struct Params {
     int linear;
     int *first;       // [row_tiles + 1] first unit of a row tile; the units of all
     FastDiv H, nq, m, page, ring;
+    const uint16_t *keys;  // the pool's rows; linear: the copy's, see PrefixArgs
+    int batch;
+    int own_cap;           // linear: rows of the copy for one request's own entries
     int box;          // entries that one copy brings at most (none crosses a page): 16, 32 or 64
     int vbox;         // those of a V copy: at most one slot's
     float *part;
@@ -118,11 +122,12 @@ struct Tile {
                        // part of a row tile; kEnd: no tile; kMixed: window rows among the keys.  Of keys 16 i ..
                        // 16 i + 15, bit kMissingShift + i: entries without a page, kRingShift + i: window rows
     int ent_rt;        // keys [0, ent) are entries that some row sees; the row tile: ent | rt << 8
+    int n;             // kFirst: tiles of the part
     int b;
     int e_first;       // entry index of key 0
     int r_first;       // ring row of key 0 (kMixed: keys from -r_first on, where that is positive)
     int rows[8];       // row of key 16 i in the pool, the rings or (linear) the copy; < 0: none, reads as zeros
-    uint32_t zero[4];  // keys that a copy brings (FP8 own keys: any) and no row takes: cleared in V
+    uint32_t zero[4];  // keys that a copy brings and no row takes: cleared in V
     CSA_DEVINL int ent() const { return ent_rt & 255; }
     CSA_DEVINL int rt() const { return ent_rt >> 8; }
 };
@@ -242,26 +247,48 @@ struct Units {
     int left, rt, x;
 };
 
-// By one warp; `write`: also where every row tile begins.
-CSA_DEVINL Units deal_units(const Params &p, int pair, bool write) {
-    const int lane = threadIdx.x & 31, RT = p.plan.row_tiles;
-    // lanes per row tile: about its requests
+// Units of the row tiles, by the whole block, to `counts` (at most kCounts of them).
+constexpr int kCounts = (int)(2 * kPBytes / sizeof(int));
+
+CSA_DEVINL int count_lanes(const Params &p) {  // lanes per row tile: about its requests
     int subs = 1;
     while (subs < 32 && subs * p.a.H * p.a.nq < kPrefixRows) subs *= 2;
-    const int step = 32 / subs;  // row tiles per pass
+    return subs;
+}
+
+CSA_DEVINL void count_all(const Params &p, int *counts) {
+    const int subs = count_lanes(p), RT = std::min(p.plan.row_tiles, +kCounts), step = kThreads / subs;
+    for (int r0 = 0; r0 < RT; r0 += step) {
+        const int rt = r0 + (int)threadIdx.x / subs, n = count_units(p, rt, subs);
+        if (rt < RT && (threadIdx.x & (subs - 1)) == 0) counts[rt] = n;
+    }
+}
+
+// By one warp; `write`: also where every row tile begins.
+CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool write) {
+    const int lane = threadIdx.x & 31, RT = p.plan.row_tiles, subs = count_lanes(p);
     int total = 0, n = 0, inc = 0;
-    const auto pass = [&](int r0) {  // n: units of row tile r0 + lane / subs; inc: of those up to it in this pass
-        n = count_units(p, r0 + lane / subs, subs);
+    const auto pass = [&](int r0) {  // n: units of row tile r0 + lane; inc: of those up to it in this pass
+        n = 0;
+        if (r0 + 32 <= kCounts) {
+            if (r0 + lane < RT) n = counts[r0 + lane];
+        } else {
+            for (int l0 = 0; l0 < 32; l0 += 32 / subs) {
+                const int c = count_units(p, r0 + l0 + lane / subs, subs);
+                const int of = __shfl_sync(0xffffffffu, c, (lane - l0) * subs & 31);
+                if (lane >= l0 && lane < l0 + 32 / subs) n = of;
+            }
+        }
         inc = n;
-        for (int d = subs; d < 32; d <<= 1) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, inc, d);
             if (lane >= d) inc += up;
         }
     };
-    for (int r0 = 0; r0 < RT; r0 += step) {
+    for (int r0 = 0; r0 < RT; r0 += 32) {
         pass(r0);
-        const int rt = r0 + lane / subs;
-        if (write && rt < RT && (lane & (subs - 1)) == 0) p.first[rt] = total + inc - n;
+        if (write && r0 + lane < RT) p.first[r0 + lane] = total + inc - n;
         total += __shfl_sync(0xffffffffu, inc, 31);
     }
     if (write && lane == 0) p.first[RT] = total;
@@ -270,12 +297,12 @@ CSA_DEVINL Units deal_units(const Params &p, int pair, bool write) {
     u.left = p.plan.begin(pair + 1, total) - u0;
     if (u.left == 0) return u;
     int base = 0;
-    for (int r0 = 0; r0 < RT; r0 += step) {
-        if (RT > step) pass(r0);
+    for (int r0 = 0; r0 < RT; r0 += 32) {
+        if (RT > 32) pass(r0);
         const uint32_t here = __ballot_sync(0xffffffffu, base + inc - n <= u0 && u0 < base + inc);
         if (here) {
             const int l = __ffs(here) - 1;
-            u.rt = r0 + l / subs;
+            u.rt = r0 + l;
             u.x = u0 - base - __shfl_sync(0xffffffffu, inc - n, l);
             break;
         }
@@ -417,56 +444,6 @@ CSA_DEVINL uint32_t key_mask(const Params &p, const Tile &d, int off, const Row 
     return mask;
 }
 
-// One slot of an own tile over FP8 rows, by one warp: K (V = false): the CTA's 64
-// keys x dims [128 w, 128 w + 128), V: keys [w kVKeys, ..) x the CTA's half of
-// the dims, in the layouts that the TMA copies make.  Keys that no row takes are
-// zeros (nothing is known of their memory).
-template <int DP, bool V>
-CSA_DEVINL void expand_slot(const Params &p, const Tile &d, int rank, int w, uint32_t dst, int vbox) {
-    using Lt = Layout<DP>;
-    const AttendArgs &a = p.a;
-    constexpr int kKeys = V ? Lt::kVKeys : 64, kUnits = V ? Lt::kVChunks * 4 : 8;  // 16 codes of a key each
-    constexpr int kStep = 32 / kUnits, kBatch = 4;                                 // keys per step of the warp; steps in flight
-    const int lane = threadIdx.x & 31, u = lane % kUnits * 2;
-    const int key0 = V ? w * kKeys : rank * 64, dim = (V ? rank * (DP / 2) : w * 128) + u * 8;
-    const int vsh = 31 - __clz(vbox);
-    // shared-memory address of 16-byte unit x (8 dims) of the slot's key k: V as [k / vbox]
-    // [64-dim chunk][k % vbox][128 B], K as [chunk][k][128 B], 128-byte swizzle
-    const auto at = [&](int k, int x) {
-        const uint32_t line = V ? ((uint32_t)((k >> vsh) * Lt::kVChunks + (x >> 3)) << vsh) + (k & (vbox - 1))
-                                : (uint32_t)((x >> 3) * 64 + k);
-        return dst + line * 128 + (((x & 7) ^ (k & 7)) << 4);
-    };
-#pragma unroll 1
-    for (int k0 = lane / kUnits; k0 < kKeys; k0 += kBatch * kStep) {
-        uint4 v[kBatch];
-        uint32_t e[kBatch];
-#pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
-            const int k = key0 + k0 + c * kStep, row = d.rows[k >> 4];
-            v[c] = make_uint4(0u, 0u, 0u, 0u);
-            e[c] = 0u;
-            if (row >= 0 && !((d.zero[k >> 5] >> (k & 31)) & 1u)) {
-                const bool ring = (d.flags >> (kRingShift + (k >> 4))) & 1;
-                const size_t r = (size_t)row + (k & 15);
-                v[c] = ldg16((ring ? a.win8 : a.kv8) + r * a.D + dim);
-                e[c] = __ldg((ring ? a.win8e : a.kv8e) + r * (a.D / 128) + dim / 128);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
-            const int k = k0 + c * kStep;
-            const uint4 lo = e4m3x8_bf16x8(make_uint2(v[c].x, v[c].y), e[c]);
-            const uint4 hi = e4m3x8_bf16x8(make_uint2(v[c].z, v[c].w), e[c]);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(k, u)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w)
-                         : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(k, u + 1)), "r"(hi.x), "r"(hi.y), "r"(hi.z),
-                         "r"(hi.w)
-                         : "memory");
-        }
-    }
-}
-
 // The tensor maps of one call, [64-dim chunk][row][64] each.
 struct Maps {
     CUtensorMap q;         // 64 rows x 2 chunks
@@ -475,7 +452,7 @@ struct Maps {
     CUtensorMap rk16, rv16;  // the rings, the same
 };
 
-template <int DP, bool FP8>
+template <int DP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_prefix_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     using Lt = Layout<DP>;
@@ -509,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) mbar_init(s.vfix + i, 1);
         for (int i = 0; i < kDescs; ++i) {
             mbar_init(s.dfull + i, 1);
-            mbar_init(s.dempty + i, kSoftWarps + (rank == 0 ? 1 : 2));  // and the query tiles', the prefetching warp
+            mbar_init(s.dempty + i, kSoftWarps / 2 + (rank == 0 ? 1 : 2));  // a group, the query tiles', the prefetching warp
         }
         *s.abort_flag = 0;
         fence_mbar_init();
@@ -517,8 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::prefetch_tmap(&maps.k);
         tc::prefetch_tmap(&maps.v);
     }
-    Units un = {0, 0, 0};
-    if (warp == kPlanWarp) un = deal_units(p, pair, blockIdx.x == 0);
+    count_all(p, reinterpret_cast<int *>(s.p));  // (P is written long after the planner has read them)
     if (warp == kQueryWarp) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
     tc::fence_before_sync();
     __syncthreads();
@@ -562,14 +538,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!(ok = warp_wait(empty, par, p.ctx, s.abort_flag))) break;
                 const bool mixed = d.flags & kMixed;
                 const int vbox = mixed ? 16 : p.vbox;
-                if (FP8 && !(d.flags & kShared)) {
-                    if (v) expand_slot<DP, true>(p, d, rank, w, dst, vbox);
-                    else expand_slot<DP, false>(p, d, rank, w, dst, vbox);
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    mbar_arrive_cluster(full, lane == 0);
-                    continue;
-                }
                 if (!v) {
                     if (tc::elect_one()) {
                         mbar_arrive_expect_tx_cluster(full, kSlotBytes);
@@ -700,7 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         else if (rank == 1) {
             // -------------------------------------------------------- own rows into L2
-            const int lines = (FP8 ? a.D : 2 * a.D) / 128, lsh = 31 - __clz(lines);  // of 128 bytes per row
+            const int lines = a.D / 64, lsh = 31 - __clz(lines);  // of 128 bytes per row
             for (uint32_t g = 0;; ++g) {
                 const Tile *d = warp_desc_of(g);
                 if (!d) break;
@@ -711,9 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int k = x >> lsh, line = x & (lines - 1), row = d->rows[k >> 4];
                         const bool ring = (flags >> (kRingShift + (k >> 4))) & 1;
                         if (row < 0 || ((d->zero[k >> 5] >> (k & 31)) & 1u)) continue;
-                        const uint8_t *base = FP8 ? (ring ? a.win8 : a.kv8)
-                                                  : reinterpret_cast<const uint8_t *>(ring ? a.win : a.kv);
-                        const uint8_t *src = base + ((size_t)row + (k & 15)) * (FP8 ? a.D : 2 * a.D) + line * 128;
+                        const uint16_t *src = (ring && !p.linear ? a.win : p.keys) + ((size_t)row + (k & 15)) * a.D + line * 64;
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
                     }
                 __syncwarp();
@@ -748,6 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         copies = !ok;
     } else if (warp == kPlanWarp) {
         // ------------------------------------------------------------ planner
+        Units un = deal_units(p, reinterpret_cast<const int *>(s.p), pair, blockIdx.x == 0);
         uint32_t g = 0;
         bool ok = true;
         // An entry is free for tile g once tile g - kDescs is done with everywhere: once the
@@ -815,9 +782,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (k16 < ent) {
                         missing = id < 0 || id >= a.n_pages;
                         if (sh && p.linear) row = e16;
+                        else if (p.linear) row = p.n_shared + b * p.own_cap + (e16 - p.n_shared);
                         else if (!missing) row = id * a.page + off;
                     } else if ((flags & kMixed) && rr >= 0 && rr < win_rows) {
-                        row = b * win_rows + rr;
+                        row = b * win_rows + rr + (p.linear ? p.n_shared + p.batch * p.own_cap : 0);
                         from_ring = true;
                     }
                     d->rows[lane] = row;
@@ -829,8 +797,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // last box's rest; of window rows those in no query's window and past the ring.
                     const int vb = flags & kMixed ? 16 : p.vbox, k32 = lane * 32;
                     uint32_t z;
-                    if (FP8 && !sh) z = ~low_bits(ent - k32);
-                    else z = bits_between(ent - k32, ((ent + vb - 1) & -vb) - 1 - k32);
+                    z = bits_between(ent - k32, ((ent + vb - 1) & -vb) - 1 - k32);
                     const uint32_t two = rings >> (2 * lane);
                     const uint32_t wins = (two & 1u ? 0x0000ffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
                     if (wins) {
@@ -847,6 +814,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     d->flags = flags;
                     d->ent_rt = ent | un.rt << 8;
+                    d->n = n;
                     d->b = b;
                     d->e_first = e_first;
                     d->r_first = r_first;
@@ -891,41 +859,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const auto wait = [&](uint64_t *bar, uint32_t parity) {
             return warp_wait(smem_u32(bar), parity, p.ctx, s.abort_flag);
         };
-        for (uint32_t g = 0;; ++g) {
-            const Tile *dp = warp_desc_of(g);
-            if (!dp || (dp->flags & kEnd)) break;
-            const Tile &d = *dp;
-            const int flags = d.flags;
-            const size_t part = (size_t)pair + d.rt();
-            if (flags & kFirst) {  // a new row tile
-                const int row = d.rt() * kPrefixRows + rank * 64 + r;
-                const int bq = row < n_rows ? p.H.div(row) : 0;
-                rw.t = row < n_rows ? __ldg(a.q_pos + bq) : -1;
-                rw.b = p.nq.div(bq);
-                rw.vis = visible(p, rw.t, (int)a.N);
-                rw.w = window_of(p, std::max(rw.t, 0));
-                vis_min = __reduce_min_sync(0xffffffffu, rw.vis);
-                if (!wait(s.qland, nq & 1u)) break;
-                ++nq;
-                xch[q4 * 32 + lane] = query_squares<DP>(s.q, r, q4);
-                if (q_rw) {
-                    query_rewrite<DP>(a, s.q, r, q4, rw.t);
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    mbar_arrive_cluster(qready0, lane == 0);
-                }
+        for (uint32_t g0 = 0;;) {
+            const Tile *d0 = warp_desc_of(g0);  // the first tile of a part
+            if (!d0 || (d0->flags & kEnd)) break;
+            const uint32_t last = g0 + (uint32_t)d0->n - 1u;
+            const size_t part = (size_t)pair + d0->rt();
+            const int row = d0->rt() * kPrefixRows + rank * 64 + r;
+            const int bq = row < n_rows ? p.H.div(row) : 0;
+            rw.t = row < n_rows ? __ldg(a.q_pos + bq) : -1;
+            rw.b = p.nq.div(bq);
+            rw.vis = visible(p, rw.t, (int)a.N);
+            rw.w = window_of(p, std::max(rw.t, 0));
+            vis_min = __reduce_min_sync(0xffffffffu, rw.vis);
+            if (!wait(s.qland, nq & 1u)) break;
+            ++nq;
+            xch[q4 * 32 + lane] = query_squares<DP>(s.q, r, q4);
+            if (q_rw) {
+                query_rewrite<DP>(a, s.q, r, q4, rw.t);
+                tc::fence_proxy_async_smem();
                 __syncwarp();
-                mbar_arrive(smem_u32(s.qempty), lane == 0);
-                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
-                const float ss = (xch[lane] + xch[32 + lane]) + (xch[64 + lane] + xch[96 + lane]);
-                // 1 / RMS times the softmax scale (without its sign), in log2 units; above 0, so that a
-                // masked score stays -inf
-                rq = fmaxf((1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
-                m = m_l = -INFINITY;
-                l = 0.f;
-                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+                mbar_arrive_cluster(qready0, lane == 0);
             }
-            if ((g & 1u) == (uint32_t)wg) {
+            __syncwarp();
+            mbar_arrive(smem_u32(s.qempty), lane == 0);
+            if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+            const float ss = (xch[lane] + xch[32 + lane]) + (xch[64 + lane] + xch[96 + lane]);
+            // 1 / RMS times the softmax scale (without its sign), in log2 units; above 0, so that a
+            // masked score stays -inf
+            rq = fmaxf((1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
+            m = m_l = -INFINITY;
+            l = 0.f;
+            if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+            // this group's tiles
+            bool ok = true;
+            for (uint32_t g = g0 + ((g0 ^ (uint32_t)wg) & 1u); g <= last; g += 2) {
+                ok = false;  // until the tile is done
+                const Tile *dp = warp_desc_of(g);
+                if (!dp) break;
+                const Tile &d = *dp;
+                const int flags = d.flags;
                 const uint32_t b = g & 1u, ph = (g >> 1) & 1u, sb = g % kSBufs;
                 uint32_t mk0 = 0xffffffffu, mk1 = 0xffffffffu;  // keys that take part
                 bool whole = (flags & (kShared | 0xff << kMissingShift)) == kShared && d.ent() == kPrefixKeys &&
@@ -1011,37 +983,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 mbar_arrive_cluster(pfull0 + b * 8, lane == 0);
+                __syncwarp();
+                mbar_arrive(smem_u32(s.dempty + g % kDescs), lane == 0);
+                ok = true;
             }
-            __syncwarp();
-            mbar_arrive(smem_u32(s.dempty + g % kDescs), lane == 0);
-            if (flags & kLast) {
-                const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
-                if ((g & 1u) != (uint32_t)wg) {  // the last tile's maxima, too; the phase before the one awaited is over
-                    if (!warp_wait(xbar + b * 16, ph, p.ctx, s.abort_flag) || !wait(s.pvdone + b, ph ^ 1u)) break;
-                    m = raise(m, tile_max(g));
-                }
-                if (!wait(s.pvdone + b, ph)) break;
-                tc::fence_after_sync();
-                if (m_l != m && m_l != -INFINITY) l *= exp2f(m_l - m);
-                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
-                xch[q4 * 32 + lane] = l;
-                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
-                if (q4 == 0)
-                    p.ml[part * kPrefixRows + rank * 64 + r] =
-                        make_float2(m, (xch[lane] + xch[32 + lane]) + (xch[64 + lane] + xch[96 + lane]));
-                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
-                float4 *dst = reinterpret_cast<float4 *>(p.part) + (part * 2 + rank) * (DP / 8) * 128 + tl;
-#pragma unroll 1
-                for (int c = wg * (DP / 4); c < (wg + 1) * (DP / 4); c += 32) {
-                    float v[32];
-                    tc::tmem_ld32(tmem + lane_base + c, v);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[(size_t)(c / 4 + i) * 128] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                }
-                tc::fence_before_sync();  // O is read before the next row tile's first P.V (through pfull)
+            if (!ok) break;
+            {
+                const uint32_t g = last;
+                                const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
+                                if ((g & 1u) != (uint32_t)wg) {  // the last tile's maxima, too; the phase before the one awaited is over
+                                    if (!warp_wait(xbar + b * 16, ph, p.ctx, s.abort_flag) || !wait(s.pvdone + b, ph ^ 1u)) break;
+                                    m = raise(m, tile_max(g));
+                                }
+                                if (!wait(s.pvdone + b, ph)) break;
+                                tc::fence_after_sync();
+                                if (m_l != m && m_l != -INFINITY) l *= exp2f(m_l - m);
+                                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+                                xch[q4 * 32 + lane] = l;
+                                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+                                if (q4 == 0)
+                                    p.ml[part * kPrefixRows + rank * 64 + r] =
+                                        make_float2(m, (xch[lane] + xch[32 + lane]) + (xch[64 + lane] + xch[96 + lane]));
+                                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+                                float4 *dst = reinterpret_cast<float4 *>(p.part) + (part * 2 + rank) * (DP / 8) * 128 + tl;
+                #pragma unroll 1
+                                for (int c = wg * (DP / 4); c < (wg + 1) * (DP / 4); c += 32) {
+                                    float v[32];
+                                    tc::tmem_ld32(tmem + lane_base + c, v);
+                                    tc::tmem_wait_ld();
+                #pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        dst[(size_t)(c / 4 + i) * 128] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                                }
+                                tc::fence_before_sync();  // O is read before the next row tile's first P.V (through pfull)
             }
+            g0 = last + 1u;
         }
     }
     if (copies) {
@@ -1058,39 +1034,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// Rows 0..n_shared-1 of an FP8 pool in order, as bf16 (exact); entries without a page are zero.
-__global__ void __launch_bounds__(256)
-    prefix_rows_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ exps, const int *__restrict__ table,
-                       int page, long long n_pages, int D, long long units, uint4 *__restrict__ out) {
+// The rows of an FP8 cache that a call reads, as bf16 (exact) in the order of
+// PrefixArgs; entries without a page are zero, those that no query sees stay as
+// they are (nothing reads them).
+struct ExpandParams {
+    AttendArgs a;
+    int units;  // of 16 codes
+    int n_shared, own_cap, batch;
+    FastDiv upr, own, page;
+    uint4 *out;
+};
+
+__global__ void __launch_bounds__(256) expand_rows_kernel(const ExpandParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long u = (long long)blockIdx.x * 256 + threadIdx.x;  // 16 codes each
-    if (u >= units) return;
-    const int upr = D / 16;
-    const uint32_t j = (uint32_t)(u / upr);
-    const int c = (int)(u - (long long)j * upr);
-    const int id = __ldg(table + j / (uint32_t)page);
+    const AttendArgs &a = p.a;
+    const int u = (int)(blockIdx.x * 256 + threadIdx.x);
+    if (u >= p.units) return;
+    const int row = p.upr.div(u), c = u - row * (int)p.upr.d;
+    const int own0 = p.n_shared, ring0 = own0 + p.batch * p.own_cap;
+    const uint8_t *codes = a.kv8, *exps = a.kv8e;
+    long long src = -1;
+    if (row >= ring0) {
+        src = row - ring0;
+        codes = a.win8;
+        exps = a.win8e;
+    } else {
+        int e = row, b = 0;
+        if (row >= own0) {
+            b = p.own.div(row - own0);
+            e = own0 + (row - own0) - b * p.own_cap;
+            int t = -1;
+            for (int i = 0; i < a.nq; ++i) t = max(t, __ldg(a.q_pos + (size_t)b * a.nq + i));
+            if (e >= n_visible(t, a.m, a.N)) return;
+        }
+        const int pg = p.page.div(e), id = __ldg(a.table + (size_t)b * a.max_pages + pg);
+        if (id >= 0 && id < a.n_pages) src = (long long)id * a.page + (e - pg * a.page);
+    }
     uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-    if (id >= 0 && id < n_pages) {
-        const size_t row = (size_t)id * page + j % (uint32_t)page;
-        const uint4 v = ldg_stream(codes + row * D + c * 16);
-        const uint32_t e = __ldg(exps + row * (D / 128) + c / 8);
+    if (src >= 0) {
+        const uint4 v = ldg_stream(codes + src * a.D + c * 16);
+        const uint32_t e = __ldg(exps + src * (a.D / 128) + c / 8);
         lo = e4m3x8_bf16x8(make_uint2(v.x, v.y), e);
         hi = e4m3x8_bf16x8(make_uint2(v.z, v.w), e);
     }
-    out[2 * u] = lo;
-    out[2 * u + 1] = hi;
+    p.out[2 * (size_t)u] = lo;
+    p.out[2 * (size_t)u + 1] = hi;
 }
 
 // kind::f16 instruction descriptor: bf16 operands, fp32 accumulate, M = 128
 constexpr uint32_t idesc(int n, bool b_mn) { return tc::idesc_f16(n, true) | (b_mn ? (1u << 16) : 0u); }
 
-template <int DP, bool FP8>
+template <int DP>
 int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     Params p = {};
     p.a = x.a;
     p.plan = x.plan;
     p.n_shared = (int)x.n_shared;
-    p.linear = x.linear ? 1 : 0;
+    p.linear = x.own_cap >= 0 ? 1 : 0;
+    p.keys = x.keys;
+    p.batch = (int)(x.a.n_bq / x.a.nq);
+    p.own_cap = x.own_cap;
     p.part = x.part;
     p.ml = x.ml;
     p.first = x.first;
@@ -1102,9 +1105,9 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     p.ctx = ctx;
     p.idesc_qk = idesc(kPrefixKeys, false);
     p.idesc_pv = idesc(Layout<DP>::kPvN, true);
-    p.box = x.linear || x.a.page % 64 == 0 ? 64 : (x.a.page % 32 == 0 ? 32 : 16);
+    p.box = p.linear || x.a.page % 64 == 0 ? 64 : (x.a.page % 32 == 0 ? 32 : 16);
     p.vbox = std::min(p.box, Layout<DP>::kVKeys);
-    auto kern = attend_prefix_kernel<DP, FP8>;
+    auto kern = attend_prefix_kernel<DP>;
     constexpr size_t smem = smem_bytes<DP>();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return CSA_ERR_CUDA;
@@ -1116,16 +1119,18 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
         return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
                                  CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    const long long key_rows = x.linear ? x.n_shared : x.a.n_pages * x.a.page, batch = x.a.n_bq / x.a.nq;
+    const long long batch = p.batch, rings = batch * x.a.win_rows;
+    const long long key_rows = p.linear ? x.n_shared + batch * x.own_cap + rings : x.a.n_pages * x.a.page;
     constexpr int kChunks = Layout<DP>::kVChunks;
     Maps maps = {};
     if (!encode(&maps.q, x.a.q, x.a.n_bq * x.a.H, 64, 2) ||
         !encode(&maps.k, x.keys, key_rows, p.box, p.box == 64 ? 2 : 1) ||
         !encode(&maps.v, x.keys, key_rows, p.vbox, kChunks))
         return CSA_ERR_CUDA;
-    if (!FP8 && (!encode(&maps.k16, x.keys, key_rows, 16, 1) || !encode(&maps.v16, x.keys, key_rows, 16, kChunks) ||
-                 !encode(&maps.rk16, x.a.win, batch * x.a.win_rows, 16, 1) ||
-                 !encode(&maps.rv16, x.a.win, batch * x.a.win_rows, 16, kChunks)))
+    if (!encode(&maps.k16, x.keys, key_rows, 16, 1) || !encode(&maps.v16, x.keys, key_rows, 16, kChunks)) return CSA_ERR_CUDA;
+    maps.rk16 = maps.k16;  // (linear: the rings' rows are in the copy, too)
+    maps.rv16 = maps.v16;
+    if (!p.linear && (!encode(&maps.rk16, x.a.win, rings, 16, 1) || !encode(&maps.rv16, x.a.win, rings, 16, kChunks)))
         return CSA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * x.plan.pairs));
@@ -1136,7 +1141,7 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = x.linear ? 1 : 0;  // a dependent of the rows' copy
+    cfg.numAttrs = p.linear ? 1 : 0;  // a dependent of the rows' copy
     return cudaLaunchKernelEx(&cfg, kern, maps, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
@@ -1149,20 +1154,26 @@ PrefixPlan prefix_plan(long long rows) {
     return pl;
 }
 
-int launch_prefix_rows(const uint8_t *codes, const uint8_t *exps, const int *table, int page, long long n_pages, int D,
-                       long long n_shared, uint16_t *out, cudaStream_t st) {
-    const long long units = n_shared * (D / 16), blocks = (units + 255) / 256;
-    prefix_rows_kernel<<<(unsigned)blocks, 256, 0, st>>>(codes, exps, table, page, n_pages, D, units,
-                                                         reinterpret_cast<uint4 *>(out));
+int launch_expand_rows(const PrefixArgs &x, uint16_t *out, cudaStream_t st) {
+    ExpandParams p = {};
+    p.a = x.a;
+    p.n_shared = (int)x.n_shared;
+    p.own_cap = x.own_cap;
+    p.batch = (int)(x.a.n_bq / x.a.nq);
+    p.upr = FastDiv::by((uint32_t)(x.a.D / 16));
+    p.own = FastDiv::by((uint32_t)std::max(x.own_cap, 1));
+    p.page = FastDiv::by((uint32_t)x.a.page);
+    p.units = (int)((x.n_shared + p.batch * (x.own_cap + x.a.win_rows)) * (x.a.D / 16));  // below 2^25: a limited copy
+    p.out = reinterpret_cast<uint4 *>(out);
+    expand_rows_kernel<<<(unsigned)(p.units + 255) / 256, 256, 0, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 int launch_attend_prefix(const PrefixArgs &p, const DevCtx &ctx, cudaStream_t st) {
-    const bool fp8 = p.a.kv8 != nullptr;
     switch (prefix_dims(p.a.D)) {
-        case 128: return fp8 ? launch_d<128, true>(p, ctx, st) : launch_d<128, false>(p, ctx, st);
-        case 256: return fp8 ? launch_d<256, true>(p, ctx, st) : launch_d<256, false>(p, ctx, st);
-        case 512: return fp8 ? launch_d<512, true>(p, ctx, st) : launch_d<512, false>(p, ctx, st);
+        case 128: return launch_d<128>(p, ctx, st);
+        case 256: return launch_d<256>(p, ctx, st);
+        case 512: return launch_d<512>(p, ctx, st);
         default: return CSA_ERR_UNSUPPORTED;
     }
 }

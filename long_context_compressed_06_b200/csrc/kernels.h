@@ -91,8 +91,8 @@ struct PagedArgs {
     uint16_t *out;
 };
 
-size_t attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared, int W,
-                                    bool fp8);
+size_t attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared,
+                                    int ring_rows, int W, bool fp8);
 int launch_attend_paged(const PagedArgs &a, void *ws, size_t ws_bytes, const DevCtx &ctx, cudaStream_t st);
 
 // Block tables and slot maps (csa_plan_pages); the pointers' shapes are the ABI's.
