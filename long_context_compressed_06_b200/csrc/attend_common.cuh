@@ -66,30 +66,30 @@ int launch_attend_combine(const AttendArgs &a, cudaStream_t st);
 // Paged attention of a batch with a shared prefix (attend_prefix.cu): the query
 // rows of the whole batch, [rows = n_bq * H][D], by tiles of 128, against tiles
 // of 128 keys.  A row tile's units are the tiles of shared entries (read through
-// the table's row 0) and of its requests' own keys; the units of all row tiles
-// are dealt to `active` CTA pairs in balanced contiguous ranges, and a pair
-// writes one partial per row tile that its range meets: partial p + r for pair p
-// and row tile r, [rank 2][DP / 8 pieces][128 threads][4] fp32 with (running max
-// in log2 units, sum) per row in ml.  O is not divided by the sum.
+// the table's row 0) and of its requests' own keys; those of all row tiles are
+// dealt to the CTA pairs in contiguous ranges, and a pair writes one partial per
+// row tile that its range meets: partial p + r for pair p and row tile r,
+// [rank 2][DP / 8 pieces][128 threads][4] fp32 with (running max in log2 units,
+// sum) per row in ml.  O is not divided by the sum.
+//
+// Ranges are balanced by cost: a unit is 1, and a row tile begins with kPartCost
+// more, what a pair spends on beginning and ending one (its rows, their norms,
+// O to memory: ~10 us at D = 512 against 1.45 us a unit, 6 us against 0.9 at
+// D = 128).  So row tile r's unit k lies at first[r] + kPartCost + k.
 struct PrefixPlan {
+    static constexpr int kPartCost = 6;
     int row_tiles, pairs;
     CSA_HOSTDEV int partials() const { return pairs + row_tiles; }
-    // pairs that `units` units are dealt to
-    CSA_HOSTDEV int active(int units) const {
-        const int most = (units + kMinUnits - 1) / kMinUnits;
-        return most < 1 ? 1 : (most < pairs ? most : pairs);
+    // pair p's range begins here: an even share, the first pairs one more
+    CSA_HOSTDEV int begin(int p, int total) const {
+        const int each = total / pairs, more = total - each * pairs;
+        return each * p + (p < more ? p : more);
     }
-    // pair p owns units [begin(p), begin(p + 1)): units / active of them, the first pairs one more
-    CSA_HOSTDEV int begin(int p, int units) const {
-        const int n = active(units), more = units % n;
-        return p >= n ? units : units / n * p + (p < more ? p : more);
-    }
-    // the pair that owns unit u
-    CSA_HOSTDEV int pair_of(int u, int units) const {
-        const int n = active(units), each = units / n, more = units % n;
+    // the pair whose range holds place u
+    CSA_HOSTDEV int pair_of(int u, int total) const {
+        const int each = total / pairs, more = total - each * pairs;
         return u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each;
     }
-    static constexpr int kMinUnits = 1;
 };
 
 constexpr int kPrefixRows = 128, kPrefixKeys = 128;
@@ -105,7 +105,7 @@ struct PrefixArgs {
     int own_cap;
     float *part;           // [partials][128][DP], see above
     float2 *ml;            // [partials][128]
-    int *first;            // [row_tiles + 1] first unit of every row tile, and the units of all (out)
+    int *first;            // [row_tiles + 1] where every row tile's cost begins, and the cost of all (out)
 };
 
 PrefixPlan prefix_plan(long long rows);

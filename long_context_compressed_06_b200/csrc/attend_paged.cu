@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Merge
         const int DP = prefix_dims(a.D), rt = (int)(row / kPrefixRows), rr = (int)(row % kPrefixRows);
         const int u0 = g.first[rt], u1 = g.first[rt + 1], units = g.first[g.plan.row_tiles];
         if (u1 > u0) {
-            const int p0 = g.plan.pair_of(u0, units);
+            const int p0 = g.plan.pair_of(u0 + PrefixPlan::kPartCost, units);
             np = g.plan.pair_of(u1 - 1, units) - p0 + 1;
             ml = g.ml + (size_t)(p0 + rt) * kPrefixRows + rr;
             // dim d0 of row rr: [rank][piece of 4 columns][lane half x 64 rows][4]
@@ -77,19 +77,42 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Merge
         }
     }
     float M = -INFINITY;
-    for (int i = 0; i < np; ++i) M = fmaxf(M, ml[i * mstride].x);
     float L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < np; ++i) {
-        const float2 s = ml[i * mstride];
-        if (s.x == -INFINITY) continue;  // no key
-        const float w = exp2f(s.x - M);
-        const float4 x = src[i * stride], y = src[i * stride + step];
+    const auto add = [&](const float2 &s, const float4 &x, const float4 &y) {
+        const float w = s.x == -INFINITY ? 0.f : exp2f(s.x - M);
         L = fmaf(w, s.y, L);
         acc[0] = fmaf(w, x.x, acc[0]); acc[1] = fmaf(w, x.y, acc[1]);
         acc[2] = fmaf(w, x.z, acc[2]); acc[3] = fmaf(w, x.w, acc[3]);
         acc[4] = fmaf(w, y.x, acc[4]); acc[5] = fmaf(w, y.y, acc[5]);
         acc[6] = fmaf(w, y.z, acc[6]); acc[7] = fmaf(w, y.w, acc[7]);
+    };
+    constexpr int kAtOnce = 4;
+    if (np <= kAtOnce) {  // all loads in flight: (m, l), then the rows that have a key
+        float2 s[kAtOnce];
+        float4 x[kAtOnce], y[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            s[i] = i < np ? ml[i * mstride] : make_float2(-INFINITY, 0.f);
+            M = fmaxf(M, s[i].x);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s[i].x != -INFINITY) {
+                x[i] = src[i * stride];
+                y[i] = src[i * stride + step];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) add(s[i], x[i], y[i]);
+    } else {
+        for (int i = 0; i < np; ++i) M = fmaxf(M, ml[i * mstride].x);
+#pragma unroll 4
+        for (int i = 0; i < np; ++i) {
+            const float2 s = ml[i * mstride];
+            if (s.x == -INFINITY) continue;  // no key: nothing was written
+            add(s, src[i * stride], src[i * stride + step]);
+        }
     }
     if (a.sinks && active) L += exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - M);
     const float inv = L > 0.f ? 1.0f / L : 0.f;

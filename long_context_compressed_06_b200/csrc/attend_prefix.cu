@@ -102,7 +102,7 @@ struct Params {
     PrefixPlan plan;
     int n_shared;
     int linear;
-    int *first;       // [row_tiles + 1] first unit of a row tile; the units of all
+    int *first;       // [row_tiles + 1] where a row tile's cost begins, see PrefixPlan; the cost of all
     FastDiv H, nq, m, page, ring;
     const uint16_t *keys;  // the pool's rows; linear: the copy's, see PrefixArgs
     int batch;
@@ -134,11 +134,11 @@ struct Tile {
 
 struct Smem {
     uint8_t *q, *slots, *p;  // slots: K's ring, then V's; so are their barriers
-    uint64_t *full, *empty, *sfull, *sempty, *pfull, *pvdone, *qland, *qready, *qempty, *vfix, *dfull, *dempty, *rbar, *xbar;
+    uint64_t *full, *empty, *sfull, *sempty, *pfull, *pvdone, *qland, *qready, *qempty, *vfix, *dfull, *dempty, *rbar;
     Tile *desc;  // [kDescs]
-    // Per 32 rows, [2][128] floats: sums of a row's four threads [4][32] before and after its tiles;
-    // during them the upper halves of its maxima in tile g, uint16 [4: g % 4][2 halves of the keys][32]
-    float *xch;
+    // [2 x 32 rows][tile parity][2 halves of the keys][32] (upper half of the row's maximum, number of
+    // the tile) in one word
+    uint32_t *xch;
     uint32_t *tmem_slot;
     int *abort_flag;
 };
@@ -149,7 +149,7 @@ CSA_DEVINL Smem carve(uint8_t *raw) {
     s.q = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     s.slots = s.q + Layout<DP>::kQBytes;
     s.p = s.slots + 2 * kSlots * kSlotBytes;
-    s.xch = reinterpret_cast<float *>(s.p + 2 * kPBytes);
+    s.xch = reinterpret_cast<uint32_t *>(s.p + 2 * kPBytes);
     s.desc = reinterpret_cast<Tile *>(s.xch + 256);
     uint64_t *bars = reinterpret_cast<uint64_t *>(s.desc + Layout<DP>::kDescs);
     s.full = bars;
@@ -161,8 +161,7 @@ CSA_DEVINL Smem carve(uint8_t *raw) {
     s.pfull = s.sempty + kSBufs;
     s.pvdone = s.pfull + 2;
     s.rbar = s.pvdone + 2;  // [2 x 32 rows]
-    s.xbar = s.rbar + 2;    // [tile parity = group][2 x 32 rows]
-    s.qland = s.xbar + 4;
+    s.qland = s.rbar + 2;
     s.qready = s.qland + 1;
     s.qempty = s.qready + 1;
     s.vfix = s.qempty + 1;  // [2]
@@ -174,7 +173,7 @@ CSA_DEVINL Smem carve(uint8_t *raw) {
 template <int DP>
 constexpr size_t smem_bytes() {
     return 1024 + Layout<DP>::kQBytes + 2 * kSlots * kSlotBytes + 2 * kPBytes + 1024 + Layout<DP>::kDescs * sizeof(Tile) +
-           (4 * kSlots + 2 * Layout<DP>::kDescs + 2 * kSBufs + 15) * 8 + 8;
+           (4 * kSlots + 2 * Layout<DP>::kDescs + 2 * kSBufs + 11) * 8 + 8;
 }
 static_assert(smem_bytes<512>() <= 227 * 1024, "shared memory of one CTA");
 
@@ -268,7 +267,7 @@ CSA_DEVINL void count_all(const Params &p, int *counts) {
 CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool write) {
     const int lane = threadIdx.x & 31, RT = p.plan.row_tiles, subs = count_lanes(p);
     int total = 0, n = 0, inc = 0;
-    const auto pass = [&](int r0) {  // n: units of row tile r0 + lane; inc: of those up to it in this pass
+    const auto pass = [&](int r0) {  // n: cost of row tile r0 + lane; inc: of those up to it in this pass
         n = 0;
         if (r0 + 32 <= kCounts) {
             if (r0 + lane < RT) n = counts[r0 + lane];
@@ -279,6 +278,7 @@ CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool w
                 if (lane >= l0 && lane < l0 + 32 / subs) n = of;
             }
         }
+        if (n > 0) n += PrefixPlan::kPartCost;
         inc = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -292,22 +292,35 @@ CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool w
         total += __shfl_sync(0xffffffffu, inc, 31);
     }
     if (write && lane == 0) p.first[RT] = total;
-    Units u = {0, 0, 0};
-    const int u0 = p.plan.begin(pair, total);
-    u.left = p.plan.begin(pair + 1, total) - u0;
-    if (u.left == 0) return u;
-    int base = 0;
-    for (int r0 = 0; r0 < RT; r0 += 32) {
-        if (RT > 32) pass(r0);
-        const uint32_t here = __ballot_sync(0xffffffffu, base + inc - n <= u0 && u0 < base + inc);
-        if (here) {
-            const int l = __ffs(here) - 1;
-            u.rt = r0 + l;
-            u.x = u0 - base - __shfl_sync(0xffffffffu, inc - n, l);
-            break;
+    // the row tile and the unit within it of a place among all costs
+    const auto find = [&](int u, int &rt, int &x, int &units) {  // units: those before it
+        int base = 0, before = 0;
+        rt = RT;
+        x = units = 0;
+        for (int r0 = 0; r0 < RT; r0 += 32) {
+            if (RT > 32) pass(r0);
+            const uint32_t here = __ballot_sync(0xffffffffu, base + inc - n <= u && u < base + inc);
+            const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+            const int end = __shfl_sync(0xffffffffu, inc, 31);
+            if (here) {
+                const int l = __ffs(here) - 1, off = u - base - __shfl_sync(0xffffffffu, inc - n, l);
+                rt = r0 + l;
+                x = std::max(off - PrefixPlan::kPartCost, 0);
+                units = before + __shfl_sync(0xffffffffu, inc - n, l) -
+                        PrefixPlan::kPartCost * __popc(some & ((1u << l) - 1u)) + x;
+                return;
+            }
+            before += end - PrefixPlan::kPartCost * __popc(some);
+            base += end;
         }
-        base += __shfl_sync(0xffffffffu, inc, 31);
-    }
+        units = before;
+    };
+    Units u = {0, 0, 0};
+    if (total == 0) return u;
+    int n0, n1, rt1, x1;
+    find(p.plan.begin(pair, total), u.rt, u.x, n0);
+    find(p.plan.begin(pair + 1, total), rt1, x1, n1);
+    u.left = n1 - n0;
     return u;
 }
 
@@ -479,7 +492,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(s.pvdone + i, 1);
             mbar_init(s.rbar + i, kSoftWarps / 2);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(s.xbar + i, 2);  // the two warps of 32 rows in a group
         mbar_init(s.qland, 1);
         mbar_init(s.qready, q_rw ? 2 * kSoftWarps : 2);  // leader
         mbar_init(s.qempty, 1 + kSoftWarps);
@@ -494,6 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::prefetch_tmap(&maps.k);
         tc::prefetch_tmap(&maps.v);
     }
+    if (threadIdx.x < 256) s.xch[threadIdx.x] = 0xffffffffu;  // no tile's
     count_all(p, reinterpret_cast<int *>(s.p));  // (P is written long after the planner has read them)
     if (warp == kQueryWarp) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
     tc::fence_before_sync();
@@ -838,9 +851,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int tl = quarter * 32 + lane;     // tensor-memory lane
         const int r = tl & 63, hf = tl >> 6;    // row of this CTA's 64; first / second half of the columns
         const int q4 = hf * 2 + wg;             // which of the row's four threads
-        float *xch = s.xch + (quarter & 1) * 128;       // of these 32 rows
-        uint16_t *xmax = reinterpret_cast<uint16_t *>(xch);
-        const uint32_t rbar = smem_u32(s.rbar + (quarter & 1)), xbar = smem_u32(s.xbar + (quarter & 1));  // + 16 * group
+        volatile uint32_t *xch = s.xch + (quarter & 1) * 128;                     // of these 32 rows
+        float *sums = reinterpret_cast<float *>(s.p + (quarter & 1) * 4096);      // [4][32], where none of their P is
+        const uint32_t rbar = smem_u32(s.rbar + (quarter & 1));
         uint32_t rbar_n = 0;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t sempty0 = tc::map_to_rank(smem_u32(s.sempty), 0), pfull0 = tc::map_to_rank(smem_u32(s.pfull), 0);
@@ -851,9 +864,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int vis_min = 0;  // the fewest entries that a row of this warp sees
         // The rows' reference m follows the maxima of all tiles, of either group; l is relative to m_l.
         float rq = 0.f, m = -INFINITY, m_l = -INFINITY, l = 0.f;
-        const auto tile_max = [&](uint32_t g) {  // of the row, once xbar says so
-            return fmaxf(__uint_as_float((uint32_t)xmax[(g & 3u) * 64 + lane] << 16),
-                         __uint_as_float((uint32_t)xmax[(g & 3u) * 64 + 32 + lane] << 16));
+        // The row's maximum in tile g, once both halves of it are there.  A poll of the words
+        // themselves: an mbarrier between the two warps took ~400 cycles.
+        const auto tile_max = [&](uint32_t g, float &mt) {
+            const uint32_t at = (g & 1u) * 64 + lane, tag = g & 0xffffu;
+            uint64_t t0 = 0;
+            for (int i = 0;; ++i) {
+                const uint32_t x = xch[at], y = xch[at + 32];
+                if (__all_sync(0xffffffffu, (x & 0xffffu) == tag && (y & 0xffffu) == tag)) {
+                    mt = fmaxf(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u));
+                    return true;
+                }
+                if ((i & 63) == 63) {
+                    const uint64_t now = global_timer_ns();
+                    if (t0 == 0) t0 = now;
+                    if (now - t0 > p.ctx.budget_ns) {
+                        record_status(p.ctx.status, CSA_ERR_TIMEOUT);
+                        *(volatile int *)s.abort_flag = 1;
+                    }
+                    if (__any_sync(0xffffffffu, *(volatile int *)s.abort_flag)) return false;
+                }
+            }
         };
         const auto raise = [](float m0, float mt) { return m0 == -INFINITY || mt > m0 + kRescaleThreshold ? mt : m0; };
         const auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -873,7 +904,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             vis_min = __reduce_min_sync(0xffffffffu, rw.vis);
             if (!wait(s.qland, nq & 1u)) break;
             ++nq;
-            xch[q4 * 32 + lane] = query_squares<DP>(s.q, r, q4);
+            sums[q4 * 32 + lane] = query_squares<DP>(s.q, r, q4);
             if (q_rw) {
                 query_rewrite<DP>(a, s.q, r, q4, rw.t);
                 tc::fence_proxy_async_smem();
@@ -883,7 +914,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             mbar_arrive(smem_u32(s.qempty), lane == 0);
             if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
-            const float ss = (xch[lane] + xch[32 + lane]) + (xch[64 + lane] + xch[96 + lane]);
+            const float ss = (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]);
             // 1 / RMS times the softmax scale (without its sign), in log2 units; above 0, so that a
             // masked score stays -inf
             rq = fmaxf((1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
@@ -928,21 +959,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 float mt = fmaxf(m2[0], m2[1]) * rq;
                 // The row's maximum over its two threads, each rounded to 16 bits towards zero (any
-                // reference near the maximum serves, as long as all four agree).  A slot of the
-                // maxima is used again four tiles on: by then the other group, which has given
-                // those of the tile before, has read it.
-                if (g > 0 && !warp_wait(xbar + (b ^ 1u) * 16, ((g - 1) >> 1) & 1u, p.ctx, s.abort_flag)) break;
-                xmax[(g & 3u) * 64 + hf * 32 + lane] = (uint16_t)(__float_as_uint(mt) >> 16);
-                __syncwarp();
-                mbar_arrive(xbar + b * 16, lane == 0);
-                if (g > 0 && !(flags & kFirst)) m = raise(m, tile_max(g - 1));
-                if (!warp_wait(xbar + b * 16, ph, p.ctx, s.abort_flag)) break;
-                mt = tile_max(g);
+                // reference near the maximum serves, as long as all four agree).  A word is written
+                // again two tiles on: by then this tile's P.V is over, for which the partner has read
+                // it, and the other group has written the tile's between, before which it has.
+                if (!wait(s.pvdone + b, ph ^ 1u)) break;  // (P buffer b is free, too)
+                float other;
+                if (g > g0) {
+                    if (!tile_max(g - 1, other)) break;
+                    m = raise(m, other);
+                } else if (g > 0 && !tile_max(g - 1, other)) {
+                    break;
+                }
+                xch[b * 64 + hf * 32 + lane] = (__float_as_uint(mt) & 0xffff0000u) | (g & 0xffffu);
+                if (!tile_max(g, mt)) break;
                 const float m_old = m;
                 const bool mine = m != -INFINITY && mt > m + kRescaleThreshold;
                 m = raise(m, mt);
-                // P buffer b was read by the P.V of tile g - 2
-                if (!wait(s.pvdone + b, ph ^ 1u)) break;
                 if (__any_sync(0xffffffffu, mine)) {
                     const uint32_t gp = g - 1;  // O after the P.V of the tile before
                     if (!wait(s.pvdone + (gp & 1u), (gp >> 1) & 1u)) break;
@@ -988,35 +1020,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = true;
             }
             if (!ok) break;
-            {
-                const uint32_t g = last;
-                                const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
-                                if ((g & 1u) != (uint32_t)wg) {  // the last tile's maxima, too; the phase before the one awaited is over
-                                    if (!warp_wait(xbar + b * 16, ph, p.ctx, s.abort_flag) || !wait(s.pvdone + b, ph ^ 1u)) break;
-                                    m = raise(m, tile_max(g));
-                                }
-                                if (!wait(s.pvdone + b, ph)) break;
-                                tc::fence_after_sync();
-                                if (m_l != m && m_l != -INFINITY) l *= exp2f(m_l - m);
-                                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
-                                xch[q4 * 32 + lane] = l;
-                                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
-                                if (q4 == 0)
-                                    p.ml[part * kPrefixRows + rank * 64 + r] =
-                                        make_float2(m, (xch[lane] + xch[32 + lane]) + (xch[64 + lane] + xch[96 + lane]));
-                                if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
-                                float4 *dst = reinterpret_cast<float4 *>(p.part) + (part * 2 + rank) * (DP / 8) * 128 + tl;
-                #pragma unroll 1
-                                for (int c = wg * (DP / 4); c < (wg + 1) * (DP / 4); c += 32) {
-                                    float v[32];
-                                    tc::tmem_ld32(tmem + lane_base + c, v);
-                                    tc::tmem_wait_ld();
-                #pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        dst[(size_t)(c / 4 + i) * 128] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                                }
-                                tc::fence_before_sync();  // O is read before the next row tile's first P.V (through pfull)
+            const uint32_t lb = last & 1u, lph = (last >> 1) & 1u;
+            if (lb != (uint32_t)wg) {  // the last tile's maxima, too; the phase before the one awaited is over
+                float other;
+                if (!tile_max(last, other) || !wait(s.pvdone + lb, lph ^ 1u)) break;
+                m = raise(m, other);
             }
+            if (!wait(s.pvdone + lb, lph)) break;
+            tc::fence_after_sync();
+            if (m_l != m && m_l != -INFINITY) l *= exp2f(m_l - m);
+            if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+            sums[q4 * 32 + lane] = l;
+            if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+            if (q4 == 0)
+                p.ml[part * kPrefixRows + rank * 64 + r] =
+                    make_float2(m, (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]));
+            if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
+            float4 *dst = reinterpret_cast<float4 *>(p.part) + (part * 2 + rank) * (DP / 8) * 128 + tl;
+#pragma unroll 1
+            for (int c = wg * (DP / 4); c < (wg + 1) * (DP / 4); c += 32) {
+                float v[32];
+                tc::tmem_ld32(tmem + lane_base + c, v);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    dst[(size_t)(c / 4 + i) * 128] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+            tc::fence_before_sync();  // O is read before the next row tile's first P.V (through pfull)
             g0 = last + 1u;
         }
     }
