@@ -76,43 +76,40 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Merge
             src += ((size_t)h * a.D + d0) / 4;
         }
     }
-    float M = -INFINITY;
-    float L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const auto add = [&](const float2 &s, const float4 &x, const float4 &y) {
-        const float w = s.x == -INFINITY ? 0.f : exp2f(s.x - M);
-        L = fmaf(w, s.y, L);
-        acc[0] = fmaf(w, x.x, acc[0]); acc[1] = fmaf(w, x.y, acc[1]);
-        acc[2] = fmaf(w, x.z, acc[2]); acc[3] = fmaf(w, x.w, acc[3]);
-        acc[4] = fmaf(w, y.x, acc[4]); acc[5] = fmaf(w, y.y, acc[5]);
-        acc[6] = fmaf(w, y.z, acc[6]); acc[7] = fmaf(w, y.w, acc[7]);
-    };
+    // A few partials at a time, their (m, l) and rows all in flight together (a row without a key
+    // was not written: whatever is there is not used), under a running maximum.
     constexpr int kAtOnce = 4;
-    if (np <= kAtOnce) {  // all loads in flight: (m, l), then the rows that have a key
+    float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < np; i0 += kAtOnce) {
         float2 s[kAtOnce];
         float4 x[kAtOnce], y[kAtOnce];
+        float top = M;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            s[i] = i < np ? ml[i * mstride] : make_float2(-INFINITY, 0.f);
-            M = fmaxf(M, s[i].x);
-        }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (s[i].x != -INFINITY) {
-                x[i] = src[i * stride];
-                y[i] = src[i * stride + step];
+            s[i] = make_float2(-INFINITY, 0.f);
+            if (i0 + i < np) {
+                s[i] = ml[(i0 + i) * mstride];
+                x[i] = src[(i0 + i) * stride];
+                y[i] = src[(i0 + i) * stride + step];
             }
         }
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) add(s[i], x[i], y[i]);
-    } else {
-        for (int i = 0; i < np; ++i) M = fmaxf(M, ml[i * mstride].x);
-#pragma unroll 4
-        for (int i = 0; i < np; ++i) {
-            const float2 s = ml[i * mstride];
-            if (s.x == -INFINITY) continue;  // no key: nothing was written
-            add(s, src[i * stride], src[i * stride + step]);
-        }
+        for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, s[i].x);
+        const float f = M == top ? 1.f : exp2f(M - top);  // (also while both are -inf)
+        M = top;
+        L *= f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (s[i].x != -INFINITY) {
+                const float w = exp2f(s[i].x - M);
+                L = fmaf(w, s[i].y, L);
+                acc[0] = fmaf(w, x[i].x, acc[0]); acc[1] = fmaf(w, x[i].y, acc[1]);
+                acc[2] = fmaf(w, x[i].z, acc[2]); acc[3] = fmaf(w, x[i].w, acc[3]);
+                acc[4] = fmaf(w, y[i].x, acc[4]); acc[5] = fmaf(w, y[i].y, acc[5]);
+                acc[6] = fmaf(w, y[i].z, acc[6]); acc[7] = fmaf(w, y[i].w, acc[7]);
+            }
     }
     if (a.sinks && active) L += exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - M);
     const float inv = L > 0.f ? 1.0f / L : 0.f;
@@ -164,7 +161,7 @@ PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, l
     // units are counted in 32 bits: shared tiles and, of each request in a row tile, own ones
     const long long tiles = n_shared / kPrefixKeys + 1 + (1 + kPrefixRows / H) * ((cap - n_shared + ring_rows) / kPrefixKeys + 2);
     size_t at = 0;
-    if (n_shared > 0 && rows <= 0x7fffffffLL - kPrefixRows && copy <= kMaxCopyBytes &&
+    if (rows <= 0x7fffffffLL - kPrefixRows && copy <= kMaxCopyBytes &&
         tiles <= 0x7fffffffLL / (rows / kPrefixRows + 1)) {
         pl.prefix = prefix_plan(rows);
         if (fp8) pl.keys = take(at, (size_t)copy);
