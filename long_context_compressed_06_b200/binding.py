@@ -8,6 +8,7 @@ missing the first call raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -93,28 +94,43 @@ def _check(rc: int, where: str) -> None:
 
 
 def _p(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# A decode step makes several of these calls in the time that its kernels take: the current device and stream come
+# from torch's own accessors without the wrappers around them (3.4 us for a stream object, 0.1 us for its handle).
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        return torch._C._cuda_getCurrentRawStream(_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _need(t: torch.Tensor, dtype, name: str, ndim: Optional[int] = None) -> torch.Tensor:
+    try:
+        if (t.is_cuda and t.dtype == dtype and (ndim is None or t.dim() == ndim) and t.is_contiguous()
+                and t.get_device() == _device()):
+            return t
+    except AttributeError:
+        pass
+    raise _refusal(t, dtype, name, ndim)
+
+
+def _refusal(t, dtype, name: str, ndim: Optional[int]) -> Exception:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
+        return TypeError("%s must be a CUDA tensor" % name)
     # every call launches on the current device: a tensor on another GPU would be
     # read through the wrong context
     if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s but the current device is cuda:%d (use torch.cuda.device(...))"
-                         % (name, t.device, torch.cuda.current_device()))
+        return ValueError("%s is on %s but the current device is cuda:%d (use torch.cuda.device(...))"
+                          % (name, t.device, torch.cuda.current_device()))
     if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        return TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if ndim is not None and t.dim() != ndim:
-        raise ValueError("%s must have %d dims, got %s" % (name, ndim, tuple(t.shape)))
-    return t
+        return ValueError("%s must be contiguous" % name)
+    return ValueError("%s must have %d dims, got %s" % (name, ndim, tuple(t.shape)))
 
 
 # --------------------------------------------------------------------------- ops
@@ -441,6 +457,11 @@ def csa_attend_noalloc(q, kv, idx, win, q_pos, W: int, scale: float, eps: float 
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _plan_workspace_bytes(batch: int) -> int:
+    return int(load().csa_plan_workspace_bytes(batch))
+
+
 def csa_plan_pages(old_len, new_len, free_pages, block_table, m: int, page: int, ring_rows: int, max_tokens: int,
                    max_entries: int, out=None, workspace=None):
     """Block tables and slot maps of one step from the requests' lengths: old_len, new_len [b] int32 tokens cached
@@ -456,18 +477,21 @@ def csa_plan_pages(old_len, new_len, free_pages, block_table, m: int, page: int,
     batch, max_pages = block_table.shape
     if old_len.shape[0] != batch or new_len.shape[0] != batch:
         raise ValueError("old_len, new_len and block_table must have one row per request")
-    shapes = ((batch + 1,), (batch + 1,), (max_entries,), (max_tokens,), (max_tokens,), (4,))
-    dtypes = (torch.int64, torch.int64, torch.int64, torch.int32, torch.int64, torch.int64)
+    sizes = (batch + 1, batch + 1, max_entries, max_tokens, max_tokens, 4)
     if out is None:
         if max_tokens < 0 or max_entries < 0:
             raise ValueError("max_tokens and max_entries must not be negative")
-        out = tuple(torch.empty(s, dtype=t, device=old_len.device) for s, t in zip(shapes, dtypes))
+        # the int64 ones share an allocation (an allocation each took a third of the call)
+        cu_t, cu_e, slots, win, counts = torch.empty(2 * batch + 6 + max_entries + max_tokens, dtype=torch.int64,
+                                                     device=old_len.device).split(
+            (batch + 1, batch + 1, max_entries, max_tokens, 4))
+        out = (cu_t, cu_e, slots, torch.empty(max_tokens, dtype=torch.int32, device=old_len.device), win, counts)
     else:
-        for x, s, t in zip(out, shapes, dtypes):
-            if _need(x, t, "out").shape != s:
-                raise ValueError("out must hold tensors of shapes %s" % (shapes,))
+        for i, (x, n) in enumerate(zip(out, sizes)):
+            if _need(x, torch.int32 if i == 3 else torch.int64, "out", 1).shape[0] != n:
+                raise ValueError("out must hold tensors of sizes %s" % (sizes,))
     cu_t, cu_e, slots, pos, win, counts = out
-    ws, wsb = _workspace(int(L.csa_plan_workspace_bytes(batch)), old_len.device, workspace)
+    ws, wsb = _workspace(_plan_workspace_bytes(batch), old_len.device, workspace)
     _check(L.csa_plan_pages(_p(old_len), _p(new_len), batch, m, page, ring_rows, _p(free_pages), free_pages.shape[0],
                             _p(block_table), max_pages, _p(cu_t), _p(cu_e), _p(slots), max_entries, _p(pos), _p(win),
                             max_tokens, _p(counts), _p(ws), wsb, _stream()), "csa_plan_pages")
@@ -512,6 +536,11 @@ def attend_paged_workspace_bytes(batch: int, nq: int, H: int, D: int, page: int,
     return int(load().csa_attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, ring_rows, W, int(fp8)))
 
 
+@functools.lru_cache(maxsize=256)
+def _attend_paged_bytes(device: int, *shape) -> int:  # (the split plan knows the device's SMs)
+    return attend_paged_workspace_bytes(*shape)
+
+
 def _paged(q, block_table, q_pos, pool, ring, q_gain, out):
     """The shape checks that both paged attention calls make -> (batch, nq, H, D, out)."""
     _need(q, torch.bfloat16, "q", 4)
@@ -542,8 +571,8 @@ def hca_attend_paged(q, pool, block_table, m: int, ring, q_pos, W: int, scale: f
     _need(ring, torch.bfloat16, "ring", 3)
     batch, nq, H, D, out = _paged(q, block_table, q_pos, pool, ring, q_gain, out)
     n_pages, page, max_pages = pool.shape[0], pool.shape[1], block_table.shape[1]
-    ws, wsb = _workspace(attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, ring.shape[1], W),
-                         q.device, workspace)
+    ws, wsb = _workspace(_attend_paged_bytes(_device(), batch, nq, H, D, page, max_pages, n_shared, ring.shape[1], W), q.device,
+                         workspace)
     _check(L.hca_attend_paged(_p(q), _p(q_gain), _sinks(sinks, H), *_rope(rope, D), _p(pool), n_pages, page,
                               _p(block_table), max_pages, n_shared, m, _p(ring), ring.shape[1], W, _p(q_pos), batch,
                               nq, H, D, float(scale), float(eps), _p(out), _p(ws), wsb, _stream()), "hca_attend_paged")
@@ -559,8 +588,8 @@ def hca_attend_paged_fp8kv(q, pool8, pool8_exp, block_table, m: int, ring8, ring
     _fp8_rows(ring8, ring8_exp, "ring8")
     batch, nq, H, D, out = _paged(q, block_table, q_pos, pool8, ring8, q_gain, out)
     n_pages, page, max_pages = pool8.shape[0], pool8.shape[1], block_table.shape[1]
-    ws, wsb = _workspace(attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, ring8.shape[1], W,
-                                                      True), q.device, workspace)
+    ws, wsb = _workspace(_attend_paged_bytes(_device(), batch, nq, H, D, page, max_pages, n_shared, ring8.shape[1], W, True),
+                         q.device, workspace)
     _check(L.hca_attend_paged_fp8kv(_p(q), _p(q_gain), _sinks(sinks, H), *_rope(rope, D), _p(pool8), _p(pool8_exp),
                                     n_pages, page, _p(block_table), max_pages, n_shared, m, _p(ring8), _p(ring8_exp),
                                     ring8.shape[1], W, _p(q_pos), batch, nq, H, D, float(scale), float(eps), _p(out),

@@ -76,21 +76,32 @@ int launch_attend_combine(const AttendArgs &a, cudaStream_t st);
 // more, what a pair spends on beginning and ending one (its rows, their norms,
 // O to memory: ~10 us at D = 512 against 1.45 us a unit, 6 us against 0.9 at
 // D = 128).  So row tile r's unit k lies at first[r] + kPartCost + k.
+// Few row tiles are not cut into as many ranges as there are pairs: with u units
+// in each of R row tiles and r ranges per row tile a unit's time is spent u / r
+// times, and the merge of r partials takes ~1/3 of it each, least at r =
+// sqrt(3 u), that is at sqrt(3 u R * R) ranges (1 row tile of 130 units at D =
+// 512: 57 us with 74 ranges, 40 us with 20).
 struct PrefixPlan {
     static constexpr int kPartCost = 6;
     int row_tiles, pairs;
     CSA_HOSTDEV int partials() const { return pairs + row_tiles; }
-    // pair p's range begins here: an even share, the first pairs one more
-    CSA_HOSTDEV int begin(int p, int total) const {
-        const int each = total / pairs, more = total - each * pairs;
-        return each * p + (p < more ? p : more);
-    }
-    // the pair whose range holds place u
-    CSA_HOSTDEV int pair_of(int u, int total) const {
-        const int each = total / pairs, more = total - each * pairs;
-        return u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each;
+    // the ranges that `units` units are cut into
+    CSA_HOSTDEV int ranges(int units) const {
+        const float r = sqrtf(3.f * (float)units * (float)row_tiles);
+        return r < 1.f ? 1 : (r < (float)pairs ? (int)r : pairs);
     }
 };
+
+// Range p of n begins here: an even share of `total`, the first ones one more.
+CSA_HOSTDEV inline int range_begin(int p, int n, int total) {
+    const int each = total / n, more = total - each * n;
+    return p >= n ? total : each * p + (p < more ? p : more);
+}
+// the range that holds place u
+CSA_HOSTDEV inline int range_of(int u, int n, int total) {
+    const int each = total / n, more = total - each * n;
+    return u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each;
+}
 
 constexpr int kPrefixRows = 128, kPrefixKeys = 128;
 CSA_HOSTDEV inline int prefix_dims(int D) { return D < 128 ? 128 : D; }  // a row's dims in the kernel (zero-padded)
@@ -105,7 +116,7 @@ struct PrefixArgs {
     int own_cap;
     float *part;           // [partials][128][DP], see above
     float2 *ml;            // [partials][128]
-    int *first;            // [row_tiles + 1] where every row tile's cost begins, and the cost of all (out)
+    int *first;            // [row_tiles + 2] where every row tile's cost begins, the cost of all, the ranges (out)
 };
 
 PrefixPlan prefix_plan(long long rows);

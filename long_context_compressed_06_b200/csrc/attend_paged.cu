@@ -12,6 +12,7 @@
 #include "attend_common.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace csa {
 
@@ -51,8 +52,8 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Merge
         const int DP = prefix_dims(a.D), rt = (int)(row / kPrefixRows), rr = (int)(row % kPrefixRows);
         const int u0 = g.first[rt], u1 = g.first[rt + 1], units = g.first[g.plan.row_tiles];
         if (u1 > u0) {
-            const int p0 = g.plan.pair_of(u0 + PrefixPlan::kPartCost, units);
-            np = g.plan.pair_of(u1 - 1, units) - p0 + 1;
+            const int ranges = g.first[g.plan.row_tiles + 1], p0 = range_of(u0 + PrefixPlan::kPartCost, ranges, units);
+            np = range_of(u1 - 1, ranges, units) - p0 + 1;
             ml = g.ml + (size_t)(p0 + rt) * kPrefixRows + rr;
             // dim d0 of row rr: [rank][piece of 4 columns][lane half x 64 rows][4]
             const int hf = d0 / (DP / 2), col = d0 % (DP / 2);
@@ -153,6 +154,27 @@ size_t take(size_t &at, size_t bytes) {
 // The most that a bf16 copy of an FP8 cache's rows may take; beyond it the gather kernel reads the codes in place.
 constexpr long long kMaxCopyBytes = 1LL << 30;
 
+// Estimated time in us of the two kernels, from a sweep (D 64..512, 8..128 heads, 1..64 queries, 0..16384
+// shared and 64..4096 own entries): the gather kernel takes 2.6 us per tile of 64 keys and 64 heads of its
+// busiest CTA (FP8: 5.6), attend_prefix.cu 0.9 to 1.45 us per unit and what its ranges' partials cost the merge.
+// E.g. at D = 512, 128 heads: 8 requests over 1024 shared entries 22 us and 24 us, 32 over 1024 42 and 36,
+// 32 over 16384 331 and 122; at D = 128, 16 heads: 16 over 1024 16 and 28, 64 over 16384 281 and 38.
+bool prefix_pays(long long n_bq, int H, int D, long long n_shared, long long own, int nq, const PagedPlan &gather, int W,
+                 bool fp8, const PrefixPlan &pl) {
+    const long long HH = (H + 63) / 64, keys = n_shared + own + W;
+    const long long per = ((keys + 63) / 64 + gather.splits - 1) / gather.splits;
+    const long long waves = (n_bq * HH * gather.splits + num_sms() - 1) / num_sms();
+    const double t_gather = 8.0 + (gather.splits > 1 ? 2.0 : 0.0) + (fp8 ? 5.6 : 2.6) * (double)(waves * (per + 1));
+    // requests whose rows a row tile holds
+    const double requests = std::max(1.0, (double)kPrefixRows / ((double)H * nq));
+    const double u = (double)((n_shared + kPrefixKeys - 1) / kPrefixKeys) + requests * (double)((own + W + 2 * kPrefixKeys - 17) / kPrefixKeys);
+    const double units = u * pl.row_tiles, ranges = pl.ranges((int)std::min(units, 2e9));
+    const double unit = D == 512 ? 1.45 : (D == 256 ? 1.1 : 0.9);
+    const double t_prefix = 14.0 + (fp8 ? 2.0 : 0.0) + unit * ((units + PrefixPlan::kPartCost * pl.row_tiles) / ranges) +
+                            unit / 3 * (ranges / pl.row_tiles);
+    return t_prefix < t_gather;
+}
+
 PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared, int ring_rows, int W,
                      bool fp8) {
     PagedPlan pl = {};
@@ -161,19 +183,18 @@ PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, l
     // units are counted in 32 bits: shared tiles and, of each request in a row tile, own ones
     const long long tiles = n_shared / kPrefixKeys + 1 + (1 + kPrefixRows / H) * ((cap - n_shared + ring_rows) / kPrefixKeys + 2);
     size_t at = 0;
-    if (rows <= 0x7fffffffLL - kPrefixRows && copy <= kMaxCopyBytes &&
-        tiles <= 0x7fffffffLL / (rows / kPrefixRows + 1)) {
-        pl.prefix = prefix_plan(rows);
+    attend_tc_plan(n_bq, H, cap + W, &pl.splits, &pl.keys_per_split);
+    const PrefixPlan prefix = prefix_plan(std::min(rows, 0x7fffffffLL));
+    if (rows <= 0x7fffffffLL - kPrefixRows && copy <= kMaxCopyBytes && tiles <= 0x7fffffffLL / (rows / kPrefixRows + 1) &&
+        prefix_pays(n_bq, H, D, n_shared, cap - n_shared, nq, pl, W, fp8, prefix)) {
+        pl.prefix = prefix;
         if (fp8) pl.keys = take(at, (size_t)copy);
         pl.part = take(at, (size_t)pl.prefix.partials() * kPrefixRows * prefix_dims(D) * sizeof(float));
         pl.ml = take(at, (size_t)pl.prefix.partials() * kPrefixRows * sizeof(float2));
-        pl.first = take(at, (size_t)(pl.prefix.row_tiles + 1) * sizeof(int));
-    } else {
-        attend_tc_plan(n_bq, H, cap + W, &pl.splits, &pl.keys_per_split);
-        if (pl.splits > 1) {
-            pl.part = take(at, (size_t)pl.splits * rows * D * sizeof(float));
-            pl.ml = take(at, (size_t)pl.splits * rows * sizeof(float2));
-        }
+        pl.first = take(at, (size_t)(pl.prefix.row_tiles + 2) * sizeof(int));
+    } else if (pl.splits > 1) {
+        pl.part = take(at, (size_t)pl.splits * rows * D * sizeof(float));
+        pl.ml = take(at, (size_t)pl.splits * rows * sizeof(float2));
     }
     pl.bytes = at;
     return pl;

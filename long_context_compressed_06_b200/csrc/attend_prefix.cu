@@ -102,7 +102,7 @@ struct Params {
     PrefixPlan plan;
     int n_shared;
     int linear;
-    int *first;       // [row_tiles + 1] where a row tile's cost begins, see PrefixPlan; the cost of all
+    int *first;       // [row_tiles + 2], see PrefixArgs
     FastDiv H, nq, m, page, ring;
     const uint16_t *keys;  // the pool's rows; linear: the copy's, see PrefixArgs
     int batch;
@@ -266,7 +266,7 @@ CSA_DEVINL void count_all(const Params &p, int *counts) {
 // By one warp; `write`: also where every row tile begins.
 CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool write) {
     const int lane = threadIdx.x & 31, RT = p.plan.row_tiles, subs = count_lanes(p);
-    int total = 0, n = 0, inc = 0;
+    int total = 0, units = 0, n = 0, inc = 0;
     const auto pass = [&](int r0) {  // n: cost of row tile r0 + lane; inc: of those up to it in this pass
         n = 0;
         if (r0 + 32 <= kCounts) {
@@ -290,8 +290,13 @@ CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool w
         pass(r0);
         if (write && r0 + lane < RT) p.first[r0 + lane] = total + inc - n;
         total += __shfl_sync(0xffffffffu, inc, 31);
+        units += __shfl_sync(0xffffffffu, inc, 31) - PrefixPlan::kPartCost * __popc(__ballot_sync(0xffffffffu, n > 0));
     }
-    if (write && lane == 0) p.first[RT] = total;
+    const int ranges = p.plan.ranges(units);
+    if (write && lane == 0) {
+        p.first[RT] = total;
+        p.first[RT + 1] = ranges;
+    }
     // the row tile and the unit within it of a place among all costs
     const auto find = [&](int u, int &rt, int &x, int &units) {  // units: those before it
         int base = 0, before = 0;
@@ -316,10 +321,10 @@ CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool w
         units = before;
     };
     Units u = {0, 0, 0};
-    if (total == 0) return u;
+    if (total == 0 || pair >= ranges) return u;
     int n0, n1, rt1, x1;
-    find(p.plan.begin(pair, total), u.rt, u.x, n0);
-    find(p.plan.begin(pair + 1, total), rt1, x1, n1);
+    find(range_begin(pair, ranges, total), u.rt, u.x, n0);
+    find(range_begin(pair + 1, ranges, total), rt1, x1, n1);
     u.left = n1 - n0;
     return u;
 }
@@ -393,8 +398,10 @@ CSA_DEVINL float query_squares(uint8_t *q, int r, int q4) {
 template <int DP>
 CSA_DEVINL void query_rewrite(const AttendArgs &a, uint8_t *q, int r, int q4, int t) {
     const int r0 = a.D / 8 - kRopeDim / 8;  // first rotated unit
-#pragma unroll 1
-    for (int unit = q4; unit * 8 < a.D; unit += 8) {
+    // without a gain or a sign only the rotated units change
+    const int first = a.q_gain || a.scale < 0.f ? 0 : r0;
+#pragma unroll 2
+    for (int unit = first + q4; unit * 8 < a.D; unit += 8) {
         uint4 *p0 = query_unit<DP>(q, r, unit), *p1 = query_unit<DP>(q, r, unit + 4);
         float x[8], y[8];
         unpack8(*p0, x);
@@ -749,7 +756,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int q = qs.bq0 + lane; q <= qs.bq1; q += 32) vmax = std::max(vmax, visible(p, __ldg(a.q_pos + q), p.n_shared));
             const auto query0 = [&](int b) { return std::max(qs.bq0, b * a.nq); };
             const auto query1 = [&](int b) { return std::min(qs.bq1, b * a.nq + a.nq - 1); };
-            for (int b = b0 + lane; b <= b1; b += 32) n += own_keys(p, query0(b), query1(b)).tiles();
+            // own keys of request bw + lane, 32 requests at a time
+            Own mine = {0, 0u};
+            int bw = b0;
+            const auto window = [&](int b) {
+                bw = b;
+                mine = b + lane <= b1 ? own_keys(p, query0(b + lane), query1(b + lane)) : Own{0, 0u};
+            };
+            for (int b = b0; b <= b1; b += 32) {
+                window(b);
+                n += mine.tiles();
+            }
+            if (bw != b0) window(b0);
             vmax = __reduce_max_sync(0xffffffffu, vmax);
             const int shared = (vmax + kPrefixKeys - 1) / kPrefixKeys;
             n = std::min((int)__reduce_add_sync(0xffffffffu, n) + shared - un.x, un.left);
@@ -768,8 +786,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 } else {
                     while (y >= own.tiles()) {
                         y -= own.tiles();
-                        ++b;
-                        own = own_keys(p, query0(b), query1(b));
+                        if (++b >= bw + 32) window(b);
+                        own = {__shfl_sync(0xffffffffu, mine.n_own, b - bw), __shfl_sync(0xffffffffu, mine.total, b - bw)};
                     }
                     const int first = y * kPrefixKeys;
                     e_first = p.n_shared + first;
@@ -1139,8 +1157,8 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     p.vbox = std::min(p.box, Layout<DP>::kVKeys);
     auto kern = attend_prefix_kernel<DP>;
     constexpr size_t smem = smem_bytes<DP>();
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return CSA_ERR_CUDA;
+    static SmemSet smem_set;
+    if (!smem_set((const void *)kern, smem)) return CSA_ERR_CUDA;
     // [64-dim chunk][row][64]: one copy brings several chunks of its rows (past D: zeros)
     const auto encode = [&](CUtensorMap *map, const uint16_t *base, long long rows, int box_rows, int chunks) {
         const uint64_t dims[3] = {64, (uint64_t)rows, (uint64_t)(x.a.D / 64)};

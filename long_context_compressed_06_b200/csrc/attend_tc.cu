@@ -986,8 +986,8 @@ int launch_d(const AttendArgs &a, const DevCtx &ctx, cudaStream_t st, bool pdl) 
     // at least 120 KiB so that one CTA owns an SM (it allocates all 512 TMEM columns)
     const size_t smem = std::max<size_t>(smem_bytes<D>(stages), 120 * 1024);
     auto kern = attend_tc_kernel<D, FP8, PAGED>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return CSA_ERR_CUDA;
+    static SmemSet smem_set;
+    if (!smem_set((const void *)kern, smem)) return CSA_ERR_CUDA;
     CUtensorMap qmap;
     {
         const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.H, (uint64_t)a.n_bq};

@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "quant_fp8.cuh"
+#include "tc.cuh"
 
 namespace csa {
 namespace {
@@ -281,9 +282,8 @@ int launch_plan_pages(PlanArgs a, void *ws, cudaStream_t st) {
     const unsigned blocks = (unsigned)(entry_blocks + tb);
     if (a.batch <= kFusedBatch) {
         const size_t smem = 3 * (size_t)(a.batch + 1) * sizeof(long long);
-        if (cudaFuncSetAttribute(plan_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(3 * (kFusedBatch + 1) * sizeof(long long))) != cudaSuccess)
-            return CSA_ERR_CUDA;
+        static SmemSet smem_set;
+        if (!smem_set((const void *)plan_fused_kernel, 3 * (kFusedBatch + 1) * sizeof(long long))) return CSA_ERR_CUDA;
         plan_fused_kernel<<<blocks, kPlanThreads, smem, st>>>(a, entry_blocks);
         return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
     }

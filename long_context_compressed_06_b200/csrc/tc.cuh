@@ -10,6 +10,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace csa {
@@ -233,5 +235,19 @@ bool encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, uint32_t ran
                        CUtensorMapSwizzle swizzle);
 
 int num_sms();
+
+// cudaFuncSetAttribute(kern, max dynamic shared memory, bytes), once per device and kernel (`done`: a static of
+// the launcher; two threads may both set it)
+struct SmemSet {
+    std::atomic<bool> done[64] = {};
+    bool operator()(const void *kern, size_t bytes) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return false;
+        if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return true;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+        if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+        return true;
+    }
+};
 
 }  // namespace csa
