@@ -75,7 +75,7 @@ int launch_attend_combine(const AttendArgs &a, cudaStream_t st);
 // Ranges are balanced by cost: a unit is 1, and a row tile begins with kPartCost
 // more, what a pair spends on beginning and ending one (its rows, their norms,
 // O to memory: ~10 us at D = 512 against 1.45 us a unit, 6 us against 0.9 at
-// D = 128).  So row tile r's unit k lies at first[r] + kPartCost + k.
+// D = 128).  So a row tile's unit k lies kPartCost + k after its beginning.
 // Few row tiles are not cut into as many ranges as there are pairs: with u units
 // in each of R row tiles and r ranges per row tile a unit's time is spent u / r
 // times, and the merge of r partials takes ~1/3 of it each, least at r =
@@ -116,7 +116,7 @@ struct PrefixArgs {
     int own_cap;
     float *part;           // [partials][128][DP], see above
     float2 *ml;            // [partials][128]
-    int *first;            // [row_tiles + 2] where every row tile's cost begins, the cost of all, the ranges (out)
+    int2 *meet;            // [row_tiles] the first range that meets a row tile, and how many do (out)
 };
 
 PrefixPlan prefix_plan(long long rows);

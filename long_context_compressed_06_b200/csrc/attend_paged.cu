@@ -28,20 +28,26 @@ struct MergeArgs {
     PrefixPlan plan;  // pairs > 0: the partials of attend_prefix.cu, else the splits of attend_tc.cu
     const float *part;
     const float2 *ml;
-    const int *first;
+    const int2 *meet;
+    FastDiv H;
+    int n_rows;
 };
 
-// A warp: 4 rows x 64 dims, a thread 8 dims of one row: two 16-byte pieces of each partial.
-__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const MergeArgs g) {
+// A warp: 4 rows x 64 dims, a thread 8 dims of one row: two 16-byte pieces of each partial, kAtOnce
+// partials in flight.  Bound by the partials' bytes and, few as they are per thread, by what a
+// thread does before its first load: ranges divided out by every thread, or 4 dims a thread,
+// cost 4 us of ~8 (27 MB of partials of 32 x 128 rows of 512 dims).  Rows of two or three partials
+// want warps (2 at once: 75.4 us for 64 x 128 rows against 80.7 with 4), those of a dozen want
+// loads in flight (34.4 us against 39.7).
+template <int kAtOnce>
+__global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_merge_kernel(const MergeArgs g) {
     const AttendArgs &a = g.a;
-    const int slabs = a.D / 64, lane = threadIdx.x & 31;
-    const long long wid = (long long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-    const int slab = (int)(wid % slabs);
-    const long long row = wid / slabs * 4 + (lane >> 3), n_rows = a.n_bq * a.H;  // row = bq * H + h
-    const bool active = row < n_rows;  // no early exit: the rotation's shuffles need whole warps
+    const int lane = threadIdx.x & 31, slab_bits = 31 - __clz(a.D / 64);  // D is 64 .. 512, a power of two
+    const uint32_t wid = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    const int slab = (int)(wid & ((1u << slab_bits) - 1u)), row = (int)(wid >> slab_bits) * 4 + (lane >> 3);  // bq * H + h
+    const bool active = row < g.n_rows;  // no early exit: the rotation's shuffles need whole warps
     const int d0 = slab * 64 + (lane & 7) * 8;
-    const long long bq = active ? row / a.H : 0;
-    const int h = active ? (int)(row - bq * a.H) : 0;
+    const int bq = active ? g.H.div(row) : 0, h = active ? row - bq * a.H : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int np = 0, step = 1;            // partials of the row; float4 between its two pieces
     size_t stride = 0, mstride = 0;  // between partials: float4, (m, l)
@@ -49,28 +55,25 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Merge
     const float2 *ml = nullptr;
     if (!active) {
     } else if (g.plan.pairs > 0) {
-        const int DP = prefix_dims(a.D), rt = (int)(row / kPrefixRows), rr = (int)(row % kPrefixRows);
-        const int u0 = g.first[rt], u1 = g.first[rt + 1], units = g.first[g.plan.row_tiles];
-        if (u1 > u0) {
-            const int ranges = g.first[g.plan.row_tiles + 1], p0 = range_of(u0 + PrefixPlan::kPartCost, ranges, units);
-            np = range_of(u1 - 1, ranges, units) - p0 + 1;
-            ml = g.ml + (size_t)(p0 + rt) * kPrefixRows + rr;
-            // dim d0 of row rr: [rank][piece of 4 columns][lane half x 64 rows][4]
-            const int hf = d0 / (DP / 2), col = d0 % (DP / 2);
-            src = reinterpret_cast<const float4 *>(g.part) +
-                  (((size_t)(p0 + rt) * 2 + (rr >> 6)) * (DP / 8) + col / 4) * 128 + hf * 64 + (rr & 63);
-            step = 128;
-            stride = (size_t)kPrefixRows * DP / 4;
-            mstride = kPrefixRows;
-        }
+        const int rt = row / kPrefixRows, rr = row % kPrefixRows, half_bits = slab_bits > 0 ? slab_bits + 5 : 6;
+        const int2 meet = g.meet[rt];
+        const size_t p0 = (size_t)meet.x + rt;
+        np = meet.y;
+        ml = g.ml + p0 * kPrefixRows + rr;
+        // dim d0 of row rr: [rank][piece of 4 columns][lane half x 64 rows][4]
+        const int hf = d0 >> half_bits, col = d0 & ((1 << half_bits) - 1), pieces = 1 << (half_bits - 2);
+        src = reinterpret_cast<const float4 *>(g.part) + ((p0 * 2 + (rr >> 6)) * pieces + col / 4) * 128 + hf * 64 + (rr & 63);
+        step = 128;
+        stride = (size_t)pieces * 256;
+        mstride = kPrefixRows;
     } else {
         np = a.splits;
         ml = a.part_ml + row;
-        mstride = (size_t)n_rows;
-        stride = (size_t)n_rows * a.D / 4;
+        mstride = (size_t)g.n_rows;
+        stride = (size_t)g.n_rows * a.D / 4;
         src = reinterpret_cast<const float4 *>(a.part_f + (size_t)bq * a.H * a.D);
         if (a.part_perm) {
-            src += ((size_t)(h >> 6) * slabs + slab) * 1024 + ((h & 63) >> 4) * 256 + ((d0 & 31) / 4) * 32 + (h & 15) +
+            src += ((((size_t)(h >> 6) << slab_bits) + slab) * 1024) + ((h & 63) >> 4) * 256 + ((d0 & 31) / 4) * 32 + (h & 15) +
                    ((d0 >> 5) & 1) * 16;
             step = 32;
         } else {
@@ -79,7 +82,6 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Merge
     }
     // A few partials at a time, their (m, l) and rows all in flight together (a row without a key
     // was not written: whatever is there is not used), under a running maximum.
-    constexpr int kAtOnce = 4;
     float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int i0 = 0; i0 < np; i0 += kAtOnce) {
         float2 s[kAtOnce];
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Merge
         float pv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) pv[e] = __shfl_xor_sync(0xffffffffu, o[e], 4);
-        if (slab == slabs - 1 && active) {
+        if (d0 >= a.D - kRopeDim && active) {
             const long long t = __ldg(a.q_pos + bq);
             const bool first = (lane & 4) == 0;
             const int i0 = (lane & 3) * 8;
@@ -142,7 +144,7 @@ struct PagedPlan {
     PrefixPlan prefix;  // pairs > 0: attend_prefix.cu
     int splits;
     long long keys_per_split;
-    size_t keys, part, ml, first, bytes;  // offsets
+    size_t keys, part, ml, meet, bytes;  // offsets
 };
 
 size_t take(size_t &at, size_t bytes) {
@@ -191,7 +193,7 @@ PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, l
         if (fp8) pl.keys = take(at, (size_t)copy);
         pl.part = take(at, (size_t)pl.prefix.partials() * kPrefixRows * prefix_dims(D) * sizeof(float));
         pl.ml = take(at, (size_t)pl.prefix.partials() * kPrefixRows * sizeof(float2));
-        pl.first = take(at, (size_t)(pl.prefix.row_tiles + 2) * sizeof(int));
+        pl.meet = take(at, (size_t)pl.prefix.row_tiles * sizeof(int2));
     } else if (pl.splits > 1) {
         pl.part = take(at, (size_t)pl.splits * rows * D * sizeof(float));
         pl.ml = take(at, (size_t)pl.splits * rows * sizeof(float2));
@@ -225,6 +227,8 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     a.keys_per_split = pl.keys_per_split;
     MergeArgs g = {};
     g.a = a;
+    g.H = FastDiv::by((uint32_t)a.H);
+    g.n_rows = (int)(a.n_bq * a.H);
     int rc;
     if (pl.prefix.pairs > 0) {
         PrefixArgs x = {};
@@ -241,7 +245,7 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
         }
         g.part = x.part = reinterpret_cast<float *>(w + pl.part);
         g.ml = x.ml = reinterpret_cast<float2 *>(w + pl.ml);
-        g.first = x.first = reinterpret_cast<int *>(w + pl.first);
+        g.meet = x.meet = reinterpret_cast<int2 *>(w + pl.meet);
         rc = launch_attend_prefix(x, ctx, st);
         if (rc != CSA_OK) return rc;
     } else {
@@ -264,7 +268,11 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_merge_kernel, g) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    // partials of most rows: the splits, or the ranges of a row tile and one that both its ends share
+    const int partials = pl.prefix.pairs > 0 ? pl.prefix.pairs / pl.prefix.row_tiles + 1 : pl.splits;
+    const cudaError_t e = partials <= 4 ? cudaLaunchKernelEx(&cfg, attend_merge_kernel<2>, g)
+                                        : cudaLaunchKernelEx(&cfg, attend_merge_kernel<6>, g);
+    return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 }  // namespace csa

@@ -78,31 +78,12 @@ struct Layout {
     static constexpr uint32_t kQBytes = 64 * DP * 2;      // [DP/64][64 rows][128 B]
 };
 
-// Division of 0 <= n < 2^31 by a fixed d >= 1: n / d = (n * mul) >> (32 + shift), mul =
-// ceil(2^(31 + ceil(log2 d)) / d); 1 by itself (a runtime division is ~100 cycles on the planner's
-// and the softmax warps' serial paths).
-struct FastDiv {
-    uint32_t d, mul, shift;
-    static FastDiv by(uint32_t d) {
-        FastDiv f = {d, 0, 0};
-        if (d > 1) {
-            uint32_t l = 0;
-            while ((1ull << l) < d) ++l;
-            f.mul = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
-            f.shift = l - 1;
-        }
-        return f;
-    }
-    CSA_DEVINL int div(int n) const { return d == 1 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift); }
-    CSA_DEVINL int mod(int n) const { return n - div(n) * (int)d; }
-};
-
 struct Params {
     AttendArgs a;
     PrefixPlan plan;
     int n_shared;
     int linear;
-    int *first;       // [row_tiles + 2], see PrefixArgs
+    int2 *meet;       // [row_tiles], see PrefixArgs
     FastDiv H, nq, m, page, ring;
     const uint16_t *keys;  // the pool's rows; linear: the copy's, see PrefixArgs
     int batch;
@@ -263,7 +244,7 @@ CSA_DEVINL void count_all(const Params &p, int *counts) {
     }
 }
 
-// By one warp; `write`: also where every row tile begins.
+// By one warp; `write`: also the ranges of every row tile.
 CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool write) {
     const int lane = threadIdx.x & 31, RT = p.plan.row_tiles, subs = count_lanes(p);
     int total = 0, units = 0, n = 0, inc = 0;
@@ -288,14 +269,22 @@ CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool w
     };
     for (int r0 = 0; r0 < RT; r0 += 32) {
         pass(r0);
-        if (write && r0 + lane < RT) p.first[r0 + lane] = total + inc - n;
         total += __shfl_sync(0xffffffffu, inc, 31);
         units += __shfl_sync(0xffffffffu, inc, 31) - PrefixPlan::kPartCost * __popc(__ballot_sync(0xffffffffu, n > 0));
     }
     const int ranges = p.plan.ranges(units);
-    if (write && lane == 0) {
-        p.first[RT] = total;
-        p.first[RT + 1] = ranges;
+    // for the merge: which ranges meet each row tile
+    if (write) {
+        int base = 0;
+        for (int r0 = 0; r0 < RT; r0 += 32) {
+            if (RT > 32) pass(r0);
+            const int at = base + inc - n;
+            if (r0 + lane < RT) {
+                const int q0 = n > 0 ? range_of(at + PrefixPlan::kPartCost, ranges, total) : 0;
+                p.meet[r0 + lane] = make_int2(q0, n > 0 ? range_of(at + n - 1, ranges, total) - q0 + 1 : 0);
+            }
+            base += __shfl_sync(0xffffffffu, inc, 31);
+        }
     }
     // the row tile and the unit within it of a place among all costs
     const auto find = [&](int u, int &rt, int &x, int &units) {  // units: those before it
@@ -1144,7 +1133,7 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     p.own_cap = x.own_cap;
     p.part = x.part;
     p.ml = x.ml;
-    p.first = x.first;
+    p.meet = x.meet;
     p.H = FastDiv::by((uint32_t)x.a.H);
     p.nq = FastDiv::by((uint32_t)x.a.nq);
     p.m = FastDiv::by((uint32_t)x.a.m);

@@ -62,6 +62,25 @@ CSA_DEVINL uint4 ldg_stream(const void *p) {
 
 CSA_DEVINL uint4 ldg16(const void *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1: n / d = (n * mul) >> (32 + shift), mul =
+// ceil(2^(31 + ceil(log2 d)) / d); 1 by itself (a runtime division is ~100 cycles on the planner's
+// and the softmax warps' serial paths).
+struct FastDiv {
+    uint32_t d, mul, shift;
+    static FastDiv by(uint32_t d) {  // on the host
+        FastDiv f = {d, 0, 0};
+        if (d > 1) {
+            uint32_t l = 0;
+            while ((1ull << l) < d) ++l;
+            f.mul = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
+            f.shift = l - 1;
+        }
+        return f;
+    }
+    CSA_DEVINL int div(int n) const { return d == 1 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift); }
+    CSA_DEVINL int mod(int n) const { return n - div(n) * (int)d; }
+};
+
 // 16-byte asynchronous copy; src == nullptr writes zeros (nothing is read)
 CSA_DEVINL void cp_async16_or_zero(uint32_t dst, const void *src, const void *any) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src ? src : any), "r"(src ? 16 : 0)
