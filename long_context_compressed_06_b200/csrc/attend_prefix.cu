@@ -677,19 +677,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         else if (rank == 1) {
             // -------------------------------------------------------- own rows into L2
-            const int lines = a.D / 64, lsh = 31 - __clz(lines);  // of 128 bytes per row
+            // (by TMA, 16 rows x half the dims each: a prefetch per 128 bytes took longer than the tiles)
             for (uint32_t g = 0;; ++g) {
                 const Tile *d = warp_desc_of(g);
                 if (!d) break;
                 const int flags = d->flags;
-                if (!(flags & (kEnd | kShared)))
-#pragma unroll 1
-                    for (int x = lane; x < kPrefixKeys << lsh; x += 32) {
-                        const int k = x >> lsh, line = x & (lines - 1), row = d->rows[k >> 4];
-                        const bool ring = (flags >> (kRingShift + (k >> 4))) & 1;
-                        if (row < 0 || ((d->zero[k >> 5] >> (k & 31)) & 1u)) continue;
-                        const uint16_t *src = (ring && !p.linear ? a.win : p.keys) + ((size_t)row + (k & 15)) * a.D + line * 64;
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+                if (!(flags & (kEnd | kShared)) && tc::elect_one())
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = d->rows[i];
+                        if (row < 0) continue;
+                        const CUtensorMap *map = (flags >> (kRingShift + i)) & 1 ? &maps.rv16 : &maps.v16;
+                        tc::tma_prefetch_3d(map, 0, row, 0);
+                        tc::tma_prefetch_3d(map, 0, row, Lt::kVChunks);
                     }
                 __syncwarp();
                 mbar_arrive(smem_u32(s.dempty + g % kDescs), lane == 0);
