@@ -33,20 +33,19 @@ struct MergeArgs {
     int n_rows;
 };
 
-// A warp: 4 rows x 64 dims, a thread 8 dims of one row: two 16-byte pieces of each partial, kAtOnce
-// partials in flight.  Bound by the partials' bytes and, few as they are per thread, by what a
-// thread does before its first load: ranges divided out by every thread, or 4 dims a thread,
-// cost 4 us of ~8 (27 MB of partials of 32 x 128 rows of 512 dims).  Rows of two or three partials
-// want warps (2 at once: 75.4 us for 64 x 128 rows against 80.7 with 4), those of a dozen want
-// loads in flight (34.4 us against 39.7).
+// A block: 32 rows x 64 dims; a warp 8 of the dims, a lane one row: two 16-byte pieces of each
+// partial, 512 contiguous bytes a load, kAtOnce partials in flight; the output goes through
+// shared memory (its rows are contiguous the other way).  Bound by the partials' bytes: 27 MB of
+// 32 x 128 rows of 512 dims in ~5 us (lanes along the dims, 64-byte pieces of the partials: 8.4 us).
+// Rows of two or three partials want warps, those of a dozen want loads in flight.
 template <int kAtOnce>
 __global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_merge_kernel(const MergeArgs g) {
     const AttendArgs &a = g.a;
-    const int lane = threadIdx.x & 31, slab_bits = 31 - __clz(a.D / 64);  // D is 64 .. 512, a power of two
-    const uint32_t wid = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-    const int slab = (int)(wid & ((1u << slab_bits) - 1u)), row = (int)(wid >> slab_bits) * 4 + (lane >> 3);  // bq * H + h
-    const bool active = row < g.n_rows;  // no early exit: the rotation's shuffles need whole warps
-    const int d0 = slab * 64 + (lane & 7) * 8;
+    __shared__ float tile[32][65];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slab_bits = 31 - __clz(a.D / 64);  // D is 64 .. 512, a power of two
+    const int slab = (int)(blockIdx.x & ((1u << slab_bits) - 1u)), row0 = (int)(blockIdx.x >> slab_bits) * 32;
+    const int row = row0 + lane, d0 = slab * 64 + warp * 8;  // row = bq * H + h
+    const bool active = row < g.n_rows;
     const int bq = active ? g.H.div(row) : 0, h = active ? row - bq * a.H : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int np = 0, step = 1;            // partials of the row; float4 between its two pieces
@@ -116,27 +115,27 @@ __global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_me
     }
     if (a.sinks && active) L += exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - M);
     const float inv = L > 0.f ? 1.0f / L : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile[lane][warp * 8 + e] = acc[e] * inv;
+    __syncthreads();
+    // now a thread 8 dims of row threadIdx.x / 8, eight threads 128 contiguous bytes
+    const int r = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * 8;
+    if (row0 + r >= g.n_rows) return;
     float o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = acc[e] * inv;
-    if (a.rope_cos) {
-        // conjugate rotation of the trailing 64 channels: channel D-64+j pairs with
-        // D-32+j, held by the thread 4 lanes away
-        float pv[8];
+    for (int e = 0; e < 8; ++e) o[e] = tile[r][c0 + e];
+    if (a.rope_cos && slab == (1 << slab_bits) - 1) {
+        // conjugate rotation of the trailing 64 channels: channel D-64+j pairs with D-32+j
+        const long long t = __ldg(a.q_pos + g.H.div(row0 + r));
+        const bool first = c0 < 32;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) pv[e] = __shfl_xor_sync(0xffffffffu, o[e], 4);
-        if (d0 >= a.D - kRopeDim && active) {
-            const long long t = __ldg(a.q_pos + bq);
-            const bool first = (lane & 4) == 0;
-            const int i0 = (lane & 3) * 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 cs = rope_cs(a, t, i0 + e);
-                o[e] = first ? o[e] * cs.x + pv[e] * cs.y : o[e] * cs.x - pv[e] * cs.y;
-            }
+        for (int e = 0; e < 8; ++e) {
+            const float2 cs = rope_cs(a, t, (c0 & 31) + e);
+            const float pv = tile[r][(c0 ^ 32) + e];
+            o[e] = first ? o[e] * cs.x + pv * cs.y : o[e] * cs.x - pv * cs.y;
         }
     }
-    if (active) *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.D + d0) = pack8(o);
+    *reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + r) * a.D + slab * 64 + c0) = pack8(o);
 }
 
 // Which kernel a call takes, how it splits its keys, and where its partial rows lie in the workspace.
@@ -258,9 +257,8 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
         if (rc != CSA_OK || pl.splits == 1) return rc;
         g.a = a;
     }
-    const long long warps = (a.n_bq * a.H + 3) / 4 * (a.D / 64);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32)));
+    cfg.gridDim = dim3((unsigned)((a.n_bq * a.H + 31) / 32 * (a.D / 64)));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr;
