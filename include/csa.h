@@ -416,7 +416,8 @@ int hca_attend_fp8kv(const uint16_t *q, const float *q_gain, const float *sinks,
  * elements, and NULL only for an array of no elements (CSA_ERR_INVALID);
  * batch <= 2^20, max_entries and max_tokens < 2^31 (CSA_ERR_UNSUPPORTED).
  * Workspace: csa_plan_workspace_bytes(batch), 8-byte aligned
- * (CSA_ERR_WORKSPACE; 0 bytes for batches up to 4096).
+ * (CSA_ERR_WORKSPACE; 0 bytes for batches up to 16384).  A step's tokens, and its
+ * entries, number less than 2^32 in all.
  */
 size_t csa_plan_workspace_bytes(int batch);
 int csa_plan_pages(const int *old_len, const int *new_len, int batch, int m, int page, int ring_rows,

@@ -113,7 +113,7 @@ struct PlanArgs {
 };
 
 size_t plan_workspace_bytes(int batch);
-int launch_plan_pages(PlanArgs a, void *ws, cudaStream_t st);
+int launch_plan_pages(const PlanArgs &a, void *ws, cudaStream_t st);
 
 // rows [n][d] to rows slots[i] of pool (bf16) or of codes / exps (FP8 rows, codes set)
 int launch_paged_write(const uint16_t *rows, const long long *slots, long long n, int d, uint16_t *pool, uint8_t *codes,

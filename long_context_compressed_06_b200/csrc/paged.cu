@@ -11,9 +11,12 @@
 //
 // Up to kFusedBatch requests one launch does it all: every block forms the
 // three prefix sums over the whole batch in its shared memory (the lengths are
-// 8 bytes a request, read from L2) and fills its own range of the outputs;
-// above that a one-block launch writes the sums to global memory first and the
-// filling blocks search them there.
+// 8 bytes a request, read from L2; the sums saturate at 2^32 - 1 there, past
+// every place that is filled) and fills its own range of the outputs.  Above
+// that a one-block launch writes the sums to global memory first and the filling
+// blocks search them there.  5000 requests of up to 3 tokens each take 10 us
+// (27 us in two launches: 14 for one block's sums, the rest mostly the
+// thirteen dependent loads from L2 of every search).
 #include "common.cuh"
 #include "kernels.h"
 #include "quant_fp8.cuh"
@@ -23,35 +26,30 @@ namespace csa {
 namespace {
 
 constexpr int kPlanThreads = 512;
-constexpr int kFusedBatch = 4096;  // three int64 sums per request: 96 KiB of shared memory
-constexpr int kPlanItems = 2048;   // outputs per filling block
+constexpr int kFusedBatch = 16384;  // three 32-bit sums per request: 192 KiB of shared memory
+constexpr int kPlanItems = 1024;    // outputs per filling block
 
-struct Req {
-    long long o, n, e0, e1, held, fresh;  // tokens, entries, pages before, pages taken
+struct Plan : PlanArgs {
+    FastDiv fm, fpage, fring;  // m, page, ring
 };
 
-CSA_DEVINL Req request(const PlanArgs &a, int b) {
+struct Req {
+    int o, n, e0, e1, held, fresh, cut;  // tokens, entries, pages before, pages taken, pages without a column
+};
+
+CSA_DEVINL Req request(const Plan &a, int b) {
     Req r;
     r.o = __ldg(a.old_len + b);
     r.n = __ldg(a.new_len + b);
-    if (r.o < 0 || r.n < 0 || r.o + r.n > 0x7fffffffLL) r.o = r.n = 0;  // an empty slot of the batch
-    r.e0 = (uint32_t)r.o / (uint32_t)a.m;
-    r.e1 = (uint32_t)(r.o + r.n) / (uint32_t)a.m;
-    // ceil, without passing 32 bits
-    const uint32_t pg = (uint32_t)a.page;
-    const long long h = (uint32_t)r.e0 / pg + ((uint32_t)r.e0 % pg ? 1 : 0);
-    const long long p = (uint32_t)r.e1 / pg + ((uint32_t)r.e1 % pg ? 1 : 0);
-    r.held = h < a.max_pages ? h : a.max_pages;
-    r.fresh = (p < a.max_pages ? p : a.max_pages) - r.held;
+    if (r.o < 0 || r.n < 0 || (long long)r.o + r.n > 0x7fffffffLL) r.o = r.n = 0;  // an empty slot of the batch
+    r.e0 = a.fm.div(r.o);
+    r.e1 = a.fm.div(r.o + r.n);
+    const int h0 = a.fpage.div(r.e0), p0 = a.fpage.div(r.e1);  // ceil, without passing 31 bits
+    const int h = h0 + (r.e0 - h0 * a.page ? 1 : 0), p = p0 + (r.e1 - p0 * a.page ? 1 : 0);
+    r.held = min(h, a.max_pages);
+    r.fresh = min(p, a.max_pages) - r.held;
+    r.cut = p - h - r.fresh;
     return r;
-}
-
-// pages that the table has no column for
-CSA_DEVINL long long pages_cut(const PlanArgs &a, const Req &r) {
-    const uint32_t pg = (uint32_t)a.page;
-    const long long p = (uint32_t)r.e1 / pg + ((uint32_t)r.e1 % pg ? 1 : 0);
-    const long long h = (uint32_t)r.e0 / pg + ((uint32_t)r.e0 % pg ? 1 : 0);
-    return p - h - r.fresh;
 }
 
 struct Sums {
@@ -65,16 +63,22 @@ CSA_DEVINL Sums shfl_up(const Sums &v, int d) {
             __shfl_up_sync(0xffffffffu, v.p, d), __shfl_up_sync(0xffffffffu, v.cut, d)};
 }
 
+struct Nothing {};  // a sum that is not kept
+CSA_DEVINL void put_sum(Nothing *, long long) {}
+CSA_DEVINL void put_sum(long long *at, long long v) { *at = v; }
+CSA_DEVINL void put_sum(uint32_t *at, long long v) { *at = v < 0xffffffffLL ? (uint32_t)v : 0xffffffffu; }
+
 // Exclusive prefix sums over the batch into cu_* ([batch + 1] each), by one
 // block; every thread returns the totals.  A thread owns consecutive requests.
-CSA_DEVINL Sums scan_batch(const PlanArgs &a, long long *cu_t, long long *cu_e, long long *cu_p) {
+template <typename T, typename P>
+CSA_DEVINL Sums scan_batch(const Plan &a, T *cu_t, T *cu_e, P *cu_p) {
     __shared__ Sums warp_tot[kPlanThreads / 32];
     const int per = (a.batch + kPlanThreads - 1) / kPlanThreads;
     const int b0 = (int)min((long long)threadIdx.x * per, (long long)a.batch), b1 = min(b0 + per, a.batch);
     Sums mine = {0, 0, 0, 0};
     for (int b = b0; b < b1; ++b) {
         const Req r = request(a, b);
-        mine = mine + Sums{r.n, r.e1 - r.e0, r.fresh, pages_cut(a, r)};
+        mine = mine + Sums{r.n, r.e1 - r.e0, r.fresh, r.cut};
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Sums inc = mine;
@@ -94,20 +98,20 @@ CSA_DEVINL Sums scan_batch(const PlanArgs &a, long long *cu_t, long long *cu_e, 
     Sums at = {base.t + inc.t - mine.t, base.e + inc.e - mine.e, base.p + inc.p - mine.p, 0};
     for (int b = b0; b < b1; ++b) {
         const Req r = request(a, b);
-        cu_t[b] = at.t;
-        cu_e[b] = at.e;
-        cu_p[b] = at.p;
+        put_sum(cu_t + b, at.t);
+        put_sum(cu_e + b, at.e);
+        put_sum(cu_p + b, at.p);
         at = at + Sums{r.n, r.e1 - r.e0, r.fresh, 0};
     }
     if (threadIdx.x == 0) {
-        cu_t[a.batch] = total.t;
-        cu_e[a.batch] = total.e;
-        cu_p[a.batch] = total.p;
+        put_sum(cu_t + a.batch, total.t);
+        put_sum(cu_e + a.batch, total.e);
+        put_sum(cu_p + a.batch, total.p);
     }
     return total;
 }
 
-CSA_DEVINL void write_counts(const PlanArgs &a, const Sums &total) {
+CSA_DEVINL void write_counts(const Plan &a, const Sums &total) {
     const long long lacking = total.p > a.n_free ? total.p - a.n_free : 0;
     a.counts[0] = total.t;
     a.counts[1] = total.e;
@@ -116,11 +120,12 @@ CSA_DEVINL void write_counts(const PlanArgs &a, const Sums &total) {
 }
 
 // the request whose range of the prefix sums holds item i < cu[batch]
-CSA_DEVINL int owner(const long long *cu, int batch, long long i) {
+template <typename T>
+CSA_DEVINL int owner(const T *cu, int batch, long long i) {
     int lo = 0, hi = batch;  // cu[lo] <= i < cu[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= i) lo = mid;
+        if ((long long)cu[mid] <= i) lo = mid;
         else hi = mid;
     }
     return lo;
@@ -129,8 +134,8 @@ CSA_DEVINL int owner(const long long *cu, int batch, long long i) {
 // Fills one range of kPlanItems outputs: blocks [0, entry_blocks) the entry
 // slots (and the table's new columns, by the thread of a page's first new
 // entry), the others the token outputs.
-CSA_DEVINL void fill(const PlanArgs &a, int block, int entry_blocks, const long long *cu_t, const long long *cu_e,
-                     const long long *cu_p) {
+template <typename T>
+CSA_DEVINL void fill(const Plan &a, int block, int entry_blocks, const T *cu_t, const T *cu_e, const T *cu_p) {
     if (block < entry_blocks) {
         const long long total = cu_e[a.batch];
         // every entry of the batch has its page noted, also those past the slot map's room
@@ -144,8 +149,8 @@ CSA_DEVINL void fill(const PlanArgs &a, int block, int entry_blocks, const long 
                     const int b = owner(cu_e, a.batch, i);
                     const Req r = request(a, b);
                     const long long c0 = cu_e[b];
-                    const uint32_t e = (uint32_t)(r.e0 + (i - c0)), j = e / (uint32_t)a.page, off = e % (uint32_t)a.page;
-                    if (j < (uint32_t)a.max_pages) {
+                    const int e = r.e0 + (int)(i - c0), j = a.fpage.div(e), off = e - j * a.page;
+                    if (j < a.max_pages) {
                         int *cell = a.table + (size_t)b * a.max_pages + j;
                         int id;
                         if (j < r.held) {
@@ -171,99 +176,95 @@ CSA_DEVINL void fill(const PlanArgs &a, int block, int entry_blocks, const long 
         long long slot = -1;
         if (i < total) {
             const int b = owner(cu_t, a.batch, i);
-            const long long p = (long long)__ldg(a.old_len + b) + (i - cu_t[b]);
-            pos = (int)p;
+            const int p = __ldg(a.old_len + b) + (int)(i - (long long)cu_t[b]);
+            pos = p;
             // of tokens that share a ring row only the newest is kept
             if (p >= (long long)__ldg(a.old_len + b) + __ldg(a.new_len + b) - a.ring)
-                slot = (long long)b * a.ring + (uint32_t)p % (uint32_t)a.ring;
+                slot = (long long)b * a.ring + a.fring.mod(p);
         }
         a.tok_pos[i] = pos;
         a.win_slots[i] = slot;
     }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_fused_kernel(const PlanArgs a, int entry_blocks) {
-    extern __shared__ long long cu[];
-    long long *cu_t = cu, *cu_e = cu + (a.batch + 1), *cu_p = cu + 2 * (a.batch + 1);
-    const Sums total = scan_batch(a, cu_t, cu_e, cu_p);
-    __syncthreads();
-    if (blockIdx.x == 0) {
-        for (int b = threadIdx.x; b <= a.batch; b += kPlanThreads) {
-            a.cu_tokens[b] = cu_t[b];
-            a.cu_entries[b] = cu_e[b];
-        }
+__global__ void __launch_bounds__(kPlanThreads) plan_fused_kernel(const Plan a, int entry_blocks) {
+    extern __shared__ uint32_t cu[];
+    uint32_t *cu_t = cu, *cu_e = cu + (a.batch + 1), *cu_p = cu + 2 * (a.batch + 1);
+    // the last block also writes the sums, in full
+    if (blockIdx.x == gridDim.x - 1) {
+        const Sums total = scan_batch(a, a.cu_tokens, a.cu_entries, (Nothing *)nullptr);
         if (threadIdx.x == 0) write_counts(a, total);
+        return;
     }
+    scan_batch(a, cu_t, cu_e, cu_p);
+    __syncthreads();
     fill(a, blockIdx.x, entry_blocks, cu_t, cu_e, cu_p);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const Plan a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Sums total = scan_batch(a, a.cu_tokens, a.cu_entries, a.cu_pages);
     if (threadIdx.x == 0) write_counts(a, total);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_fill_kernel(const PlanArgs a, int entry_blocks) {
+__global__ void __launch_bounds__(kPlanThreads) plan_fill_kernel(const Plan a, int entry_blocks) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums of plan_scan_kernel
     fill(a, blockIdx.x, entry_blocks, a.cu_tokens, a.cu_entries, a.cu_pages);
 }
 
 // ---------------------------------------------------------------- writes
 constexpr int kWriteThreads = 256;
-constexpr int kWriteUnits = 4;  // 16-byte units per thread, all in flight before the first store
+// 16-byte units per thread, all in flight before the first store: 2 (13.0 us for 32770 FP8 rows of
+// 512; 4: 14.3, 8: 16.6; one decode step's 256 rows 1.8, 2.5 and 4.1 us)
+constexpr int kWriteUnits = 2;
 
-// Unit u (8 elements) of the packed rows goes to row slots[u / upr] of the pool.
-__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const uint4 *__restrict__ rows, uint32_t upr,
-                                                                    long long units,
-                                                                    const long long *__restrict__ slots,
-                                                                    long long n_slots, uint4 *__restrict__ pool) {
-    const long long u0 = (long long)blockIdx.x * (kWriteThreads * kWriteUnits) + threadIdx.x;
+// A thread's units (8 elements each) of the packed rows, and where in the pool they go (-1: nowhere):
+// unit u of the rows is unit u % upr of row slots[u / upr].
+struct WriteUnits {
     uint4 v[kWriteUnits];
     long long dst[kWriteUnits];
+    CSA_DEVINL WriteUnits(const uint4 *__restrict__ rows, const FastDiv &upr, int units, const long long *__restrict__ slots,
+                          long long n_slots) {
+        const int u0 = (int)blockIdx.x * (kWriteThreads * kWriteUnits) + (int)threadIdx.x;
 #pragma unroll
-    for (int k = 0; k < kWriteUnits; ++k) {
-        const long long u = u0 + k * kWriteThreads;
-        dst[k] = -1;
-        if (u < units) {
-            v[k] = ldg_stream(rows + u);
-            const long long row = u / upr, s = __ldg(slots + row);
-            if (s >= 0 && s < n_slots) dst[k] = s * upr + (u - row * upr);
+        for (int k = 0; k < kWriteUnits; ++k) {
+            const int u = u0 + k * kWriteThreads;
+            dst[k] = -1;
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (u < units) {
+                v[k] = ldg_stream(rows + u);
+                const int row = upr.div(u);
+                const long long s = __ldg(slots + row);
+                if (s >= 0 && s < n_slots) dst[k] = s * upr.d + (u - row * (int)upr.d);
+            }
         }
     }
+};
+
+__global__ void __launch_bounds__(kWriteThreads)
+    paged_write_kernel(const uint4 *__restrict__ rows, const FastDiv upr, int units, const long long *__restrict__ slots,
+                       long long n_slots, uint4 *__restrict__ pool) {
+    const WriteUnits w(rows, upr, units, slots, n_slots);
 #pragma unroll
     for (int k = 0; k < kWriteUnits; ++k)
-        if (dst[k] >= 0) pool[dst[k]] = v[k];
+        if (w.dst[k] >= 0) pool[w.dst[k]] = w.v[k];
 }
 
 // The same with the rows quantised on the way (csa_quantize_fp8_kv's codes and
 // exponents): the 16 units of a 128-channel block are 16 consecutive lanes.
 __global__ void __launch_bounds__(kWriteThreads)
-    paged_write_fp8_kernel(const uint4 *__restrict__ rows, uint32_t upr, long long units,
-                           const long long *__restrict__ slots, long long n_slots, uint2 *__restrict__ codes,
-                           uint8_t *__restrict__ exps) {
-    const long long u0 = (long long)blockIdx.x * (kWriteThreads * kWriteUnits) + threadIdx.x;
-    uint4 v[kWriteUnits];
-    long long dst[kWriteUnits];
-#pragma unroll
-    for (int k = 0; k < kWriteUnits; ++k) {
-        const long long u = u0 + k * kWriteThreads;
-        dst[k] = -1;
-        v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (u < units) {
-            v[k] = ldg_stream(rows + u);
-            const long long row = u / upr, s = __ldg(slots + row);
-            if (s >= 0 && s < n_slots) dst[k] = s * upr + (u - row * upr);
-        }
-    }
+    paged_write_fp8_kernel(const uint4 *__restrict__ rows, const FastDiv upr, int units, const long long *__restrict__ slots,
+                           long long n_slots, uint2 *__restrict__ codes, uint8_t *__restrict__ exps) {
+    const WriteUnits w(rows, upr, units, slots, n_slots);
 #pragma unroll
     for (int k = 0; k < kWriteUnits; ++k) {
         float f[8];
-        unpack8(v[k], f);
+        unpack8(w.v[k], f);
         int e;
-        const uint2 w = quantize_fp8_unit(f, e);  // every lane (shuffles)
-        if (dst[k] >= 0) {
-            codes[dst[k]] = w;
-            if ((dst[k] & 15) == 0) exps[dst[k] >> 4] = (uint8_t)(e + 127);
+        const uint2 q = quantize_fp8_unit(f, e);  // every lane (shuffles)
+        if (w.dst[k] >= 0) {
+            codes[w.dst[k]] = q;
+            if ((w.dst[k] & 15) == 0) exps[w.dst[k] >> 4] = (uint8_t)(e + 127);
         }
     }
 }
@@ -274,17 +275,22 @@ size_t plan_workspace_bytes(int batch) {
     return batch > kFusedBatch ? (size_t)(batch + 1) * sizeof(long long) : 0;
 }
 
-int launch_plan_pages(PlanArgs a, void *ws, cudaStream_t st) {
+int launch_plan_pages(const PlanArgs &args, void *ws, cudaStream_t st) {
+    Plan a;
+    static_cast<PlanArgs &>(a) = args;
     const long long eb = (a.max_entries + kPlanItems - 1) / kPlanItems;
     const long long tb = (a.max_tokens + kPlanItems - 1) / kPlanItems;
     // one entry block at least: the new columns are noted also without a slot map
     const int entry_blocks = (int)(eb < 1 ? 1 : eb);
     const unsigned blocks = (unsigned)(entry_blocks + tb);
+    a.fm = FastDiv::by((uint32_t)a.m);
+    a.fpage = FastDiv::by((uint32_t)a.page);
+    a.fring = FastDiv::by((uint32_t)a.ring);
     if (a.batch <= kFusedBatch) {
-        const size_t smem = 3 * (size_t)(a.batch + 1) * sizeof(long long);
+        const size_t smem = 3 * (size_t)(a.batch + 1) * sizeof(uint32_t);
         static SmemSet smem_set;
-        if (!smem_set((const void *)plan_fused_kernel, 3 * (kFusedBatch + 1) * sizeof(long long))) return CSA_ERR_CUDA;
-        plan_fused_kernel<<<blocks, kPlanThreads, smem, st>>>(a, entry_blocks);
+        if (!smem_set((const void *)plan_fused_kernel, 3 * (kFusedBatch + 1) * sizeof(uint32_t))) return CSA_ERR_CUDA;
+        plan_fused_kernel<<<blocks + 1, kPlanThreads, smem, st>>>(a, entry_blocks);
         return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
     }
     a.cu_pages = static_cast<long long *>(ws);
@@ -304,18 +310,21 @@ int launch_plan_pages(PlanArgs a, void *ws, cudaStream_t st) {
 
 int launch_paged_write(const uint16_t *rows, const long long *slots, long long n, int d, uint16_t *pool, uint8_t *codes,
                        uint8_t *exps, long long n_slots, cudaStream_t st) {
-    const long long units = n * (d / 8);
-    if (units == 0) return CSA_OK;
-    const long long blocks = (units + kWriteThreads * kWriteUnits - 1) / (kWriteThreads * kWriteUnits);
-    if (blocks > 0x7fffffffLL) return CSA_ERR_UNSUPPORTED;
-    const uint4 *src = reinterpret_cast<const uint4 *>(rows);
-    if (codes)
-        paged_write_fp8_kernel<<<(unsigned)blocks, kWriteThreads, 0, st>>>(src, (uint32_t)(d / 8), units, slots, n_slots,
-                                                                           reinterpret_cast<uint2 *>(codes), exps);
-    else
-        paged_write_kernel<<<(unsigned)blocks, kWriteThreads, 0, st>>>(src, (uint32_t)(d / 8), units, slots, n_slots,
-                                                                       reinterpret_cast<uint4 *>(pool));
-    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    const FastDiv upr = FastDiv::by((uint32_t)(d / 8));
+    const long long most = (1LL << 30) / (d / 8);  // rows per launch: units in 31 bits
+    for (long long r0 = 0; r0 < n; r0 += most) {
+        const int units = (int)((n - r0 < most ? n - r0 : most) * (d / 8));
+        const unsigned blocks = (unsigned)(units + kWriteThreads * kWriteUnits - 1) / (kWriteThreads * kWriteUnits);
+        const uint4 *src = reinterpret_cast<const uint4 *>(rows + r0 * d);
+        if (codes)
+            paged_write_fp8_kernel<<<blocks, kWriteThreads, 0, st>>>(src, upr, units, slots + r0, n_slots,
+                                                                     reinterpret_cast<uint2 *>(codes), exps);
+        else
+            paged_write_kernel<<<blocks, kWriteThreads, 0, st>>>(src, upr, units, slots + r0, n_slots,
+                                                                 reinterpret_cast<uint4 *>(pool));
+        if (cudaGetLastError() != cudaSuccess) return CSA_ERR_CUDA;
+    }
+    return CSA_OK;
 }
 
 }  // namespace csa

@@ -101,9 +101,9 @@ def check_plan(csa, old, new, fr, table, m, page, ring, max_tokens, max_entries)
     (37, 1000, 1, 1, 16, 131),
     (97, 700, 300, 128, 3, 16),
     (513, 90, 40, 4, 5, 16),
-    (4096, 50, 3, 1, 16, 8),
-    (4097, 50, 3, 1, 16, 8),      # the two-launch form
     (6001, 9, 9, 3, 2, 5),
+    (16384, 50, 3, 1, 16, 8),
+    (16385, 50, 3, 1, 16, 8),     # the two-launch form
 ])
 def test_plan_pages(cuda, batch, old, new, m, page, ring):
     o, n, fr, table = plan_case(batch, old, new, m, page, ring, batch + new)
@@ -118,8 +118,8 @@ def test_plan_pages(cuda, batch, old, new, m, page, ring):
 def test_plan_pages_out_of_pages_and_columns(cuda):
     o, n, fr, table = plan_case(20, 400, 300, 4, 16, 128, 3, max_pages=9, free=5)
     check_plan(cuda, o, n, fr, table, 4, 16, 128, int(n.sum()), 3000)
-    o, n, fr, table = plan_case(5000, 40, 30, 4, 2, 128, 4, max_pages=6, free=100)
-    check_plan(cuda, o, n, fr, table, 4, 2, 128, int(n.sum()), 60000)
+    o, n, fr, table = plan_case(17000, 40, 30, 4, 2, 128, 4, max_pages=6, free=100)
+    check_plan(cuda, o, n, fr, table, 4, 2, 128, int(n.sum()), 70000)
 
 
 def test_plan_pages_bad_lengths_count_as_empty(cuda):
