@@ -483,7 +483,7 @@ def csa_plan_pages(old_len, new_len, free_pages, block_table, m: int, page: int,
             raise ValueError("max_tokens and max_entries must not be negative")
         # the int64 ones share an allocation (an allocation each took a third of the call)
         cu_t, cu_e, slots, win, counts = torch.empty(2 * batch + 6 + max_entries + max_tokens, dtype=torch.int64,
-                                                     device=old_len.device).split(
+                                                     device=old_len.device).unsafe_split_with_sizes(
             (batch + 1, batch + 1, max_entries, max_tokens, 4))
         out = (cu_t, cu_e, slots, torch.empty(max_tokens, dtype=torch.int32, device=old_len.device), win, counts)
     else:

@@ -185,47 +185,49 @@ def test_paged_write_fp8kv(cuda, n, d, slots):
 
 # ----------------------------------------------------------------------------- paged attention
 def dequant(codes, exps):
-    v = codes.cpu().view(torch.float8_e4m3fn).double().unflatten(-1, (-1, 128))
-    return (v * torch.exp2(exps.cpu().double() - 127).unsqueeze(-1)).flatten(-2).numpy()
+    v = codes.view(torch.float8_e4m3fn).float().double().unflatten(-1, (-1, 128))
+    return (v * torch.exp2(exps.double() - 127).unsqueeze(-1)).flatten(-2)
 
 
 def attend_ref(q, pool, table, m, ring, pos, Wn, scale, eps, gain, sinks, rope):
-    """-> (out, A, e): see the tolerance above.  pool and ring in 64 bits; rows outside the key sets may be NaN."""
+    """-> (out, A, e): see the tolerance above.  64-bit tensors on the GPU; pool and ring rows outside the key sets may
+    be NaN."""
     B, nq, H, D = q.shape
     n_pages, page = pool.shape[:2]
-    out, mag, eps_s = np.zeros(q.shape), np.zeros(q.shape), np.zeros((B, nq, H, 1))
+    out, mag, eps_s = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(q[..., :1])
     for b in range(B):
         for i in range(nq):
             t = int(pos[b, i])
             if t < 0:
                 continue
-            ids = [(int(table[b, j // page]), j % page) for j in range(min((t + 1) // m, table.shape[1] * page))]
-            rows = [pool[p, r] for p, r in ids if 0 <= p < n_pages]
-            rows += [ring[b, u % ring.shape[1]] for u in range(max(0, t - Wn + 1), t + 1)]
-            x = np.array(rows)
-            y = q[b, i] / np.sqrt((q[b, i] ** 2).mean(-1, keepdims=True) + eps)
+            j = torch.arange(min((t + 1) // m, table.shape[1] * page), device=DEV)
+            ids = table[b].long()[j // page]
+            there = (ids >= 0) & (ids < n_pages)
+            u = torch.arange(max(0, t - Wn + 1), t + 1, device=DEV)
+            x = torch.cat([pool[ids[there], j[there] % page], ring[b, u % ring.shape[1]]])
+            y = q[b, i] / (q[b, i].pow(2).mean(-1, keepdim=True) + eps).sqrt()
             if gain is not None:
                 y = y * gain
             rot = rope is not None and t < rope[0].shape[0]
             if rot:
                 c, s = rope[0][t], rope[1][t]
-                u, v = y[:, -64:-32].copy(), y[:, -32:].copy()
+                u, v = y[:, -64:-32].clone(), y[:, -32:].clone()
                 y[:, -64:-32], y[:, -32:] = u * c - v * s, v * c + u * s
             z = y @ x.T * scale
-            top = z.max(-1, keepdims=True)
+            top = z.amax(-1, keepdim=True)
             if sinks is not None:
-                top = np.maximum(top, sinks[:, None])
-            p = np.exp(z - top)
-            L = p.sum(-1, keepdims=True) + (np.exp(sinks[:, None] - top) if sinks is not None else 0)
-            o, a = p @ x / L, p @ np.abs(x) / L
+                top = torch.maximum(top, sinks[:, None])
+            p = (z - top).exp()
+            total = p.sum(-1, keepdim=True) + ((sinks[:, None] - top).exp() if sinks is not None else 0)
+            o, a = p @ x / total, p @ x.abs() / total
             if rot:
-                u, v = o[:, -64:-32].copy(), o[:, -32:].copy()
+                u, v = o[:, -64:-32].clone(), o[:, -32:].clone()
                 o[:, -64:-32], o[:, -32:] = u * c + v * s, v * c - u * s
-                u, v = a[:, -64:-32].copy(), a[:, -32:].copy()
-                a[:, -64:-32], a[:, -32:] = u * abs(c) + v * abs(s), v * abs(c) + u * abs(s)
+                u, v = a[:, -64:-32].clone(), a[:, -32:].clone()
+                a[:, -64:-32], a[:, -32:] = u * c.abs() + v * s.abs(), v * c.abs() + u * s.abs()
             out[b, i], mag[b, i] = o, a
             if gain is not None or rope is not None:
-                eps_s[b, i] = 2.0 ** -8 * abs(scale) * (np.abs(y) @ np.abs(x).T).max(-1, keepdims=True)
+                eps_s[b, i] = 2.0 ** -8 * abs(scale) * (y.abs() @ x.abs().T).amax(-1, keepdim=True)
     return out, mag, eps_s
 
 
@@ -288,7 +290,7 @@ class Case:
                 pool[torch.tensor(~used)] = float("nan")
                 ring[torch.tensor(~rows)] = float("nan")
             self.pool, self.ring = pool, ring
-            self.pool64, self.ring64 = f64(pool), f64(ring)
+            self.pool64, self.ring64 = pool.double(), ring.double()
         self.pos = torch.tensor(ts, device=DEV)
         self.scale = D ** -0.5 if scale is None else scale
         self.gain = W.uniform_f32((D,), seed + 400, DEV) + 0.5 if gain else None
@@ -307,18 +309,30 @@ class Case:
         return csa.hca_attend_paged(self.q, self.pool, self.table, self.m, self.ring, self.pos, self.Wn, self.scale, **kw)
 
     def ref(self):
-        g = None if self.gain is None else f64(self.gain)
-        s = None if self.sinks is None else f64(self.sinks)
-        r = None if self.rope is None else tuple(x.astype(np.float64) for x in self.rope_np)
-        return attend_ref(f64(self.q), self.pool64, self.table.cpu().numpy(), self.m, self.ring64, self.pos.cpu().numpy(),
-                          self.Wn, self.scale, 1e-6, g, s, r)
+        def d(x):
+            return None if x is None else x.double()
+        return attend_ref(self.q.double(), self.pool64, self.table, self.m, self.ring64, self.pos.cpu(), self.Wn, self.scale,
+                          1e-6, d(self.gain), d(self.sinks), None if self.rope is None else tuple(d(x) for x in self.rope))
 
     def check(self, got, ref=None):
         out, mag, e = ref or self.ref()
-        tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + np.expm1(2 * e) + 2.0 ** -10) * mag
-        err = np.abs(f64(got) - out)
-        assert np.isfinite(f64(got)).all()
-        assert (err <= tol).all(), (float((err - tol).max()), np.argwhere(err > tol)[:4].tolist())
+        tol = 2.0 ** -8 * out.abs() + (2.0 ** -8 + torch.expm1(2 * e) + 2.0 ** -10) * mag
+        err = (got.double() - out).abs()
+        assert got.isfinite().all()
+        assert (err <= tol).all(), (float((err - tol).max()), (err > tol).nonzero()[:4].tolist())
+
+    def by_row_tiles(self, n_shared=None):
+        """Whether the call takes the kernel over row tiles of the whole batch: its workspace holds a partial per pair
+        of SMs and row tile."""
+        n_shared = self.n_shared if n_shared is None else n_shared
+        B, nq, H, D = self.q.shape
+        tiles = -(-B * nq * H // 128)
+        parts = torch.cuda.get_device_properties(0).multi_processor_count // 2 + tiles
+        want = [parts * 128 * max(D, 128) * 4, parts * 128 * 8, tiles * 8]
+        if self.fp8:
+            want.append((n_shared + B * (self.max_pages * self.page - n_shared + self.ring.shape[1])) * D * 2)
+        return csa_pkg.attend_paged_workspace_bytes(B, nq, H, D, self.page, self.max_pages, n_shared, self.ring.shape[1],
+                                                    self.Wn, self.fp8) == sum(-(-w // 256) * 256 for w in want)
 
 
 CASES = {
@@ -380,3 +394,242 @@ def test_attend_paged(cuda, name):
         c.check(got, ref)
     empty = (c.pos < 0).cpu()
     assert (got.cpu()[empty] == 0).all()
+
+
+def spread(lo, hi, n, nq=1, also=()):
+    """n sequences' positions from lo to hi, every few of them one of `also`."""
+    ts = [lo + (hi - lo) * ((i * 37) % n) // n for i in range(n)]
+    for i, t in enumerate(also):
+        ts[(i * 7 + 3) % n] = t
+    return [[t - nq + 1 + k if t >= nq - 1 else (t if k == nq - 1 else -1) for k in range(nq)] for t in ts]
+
+
+# Sizes at which the estimate prefers the kernel over row tiles; its tile edges, masks and hand-overs.
+ROW_TILES = {
+    "d64_h8": dict(ts=spread(4103, 4600, 64), H=8, D=64, m=2, page=16, n_shared=2048, Wn=16),
+    "d64_h3": dict(ts=spread(4103, 4600, 150), H=3, D=64, m=2, page=48, n_shared=1968, Wn=5, sinks=True),
+    "d64_h1": dict(ts=spread(4103, 4300, 200, nq=2), H=1, D=64, m=2, page=32, n_shared=2048, Wn=16),
+    "d128_h16": dict(ts=spread(4103, 5600, 64), H=16, D=128, m=2, page=64, n_shared=2048, Wn=128, ring_extra=3),
+    "d128_h40_rope": dict(ts=spread(2103, 2700, 60), H=40, D=128, m=1, page=80, n_shared=2080, Wn=16, rope=True),
+    "d128_h64_nq4": dict(ts=spread(2103, 2700, 20, nq=4), H=64, D=128, m=1, page=16, n_shared=2000, Wn=33, gain=True,
+                         sinks=True),
+    "d256_h100": dict(ts=spread(2103, 2700, 40), H=100, D=256, m=1, page=32, n_shared=2016, Wn=16, rope=1000, gain=True),
+    "d256_h64": dict(ts=spread(2103, 2700, 40), H=64, D=256, m=1, page=64, n_shared=1984, Wn=128),
+    "d512_h128": dict(ts=spread(2103, 2700, 24), H=128, D=512, m=1, page=64, n_shared=2048, Wn=128),
+    "d512_h128_page16": dict(ts=spread(2103, 2500, 24), H=128, D=512, m=1, page=16, n_shared=1936, Wn=100, ring_extra=7),
+    "d512_h128_nq4": dict(ts=spread(2103, 2300, 8, nq=4), H=128, D=512, m=1, page=32, n_shared=2016, Wn=128, rope=True,
+                          gain=True, sinks=True),
+    "d512_h72": dict(ts=spread(2103, 2300, 40), H=72, D=512, m=1, page=128, n_shared=1920, Wn=16),
+    "d512_own_only": dict(ts=spread(300, 3500, 24), H=128, D=512, m=1, page=64, n_shared=0, Wn=128),
+    "d128_own_only": dict(ts=spread(300, 5500, 40, also=(-1, 0, 1, 15, 16)), H=64, D=128, m=1, page=16, n_shared=0, Wn=17),
+    # few entries seen, or none; entries that nobody sees hold NaN
+    "part_seen_128": dict(ts=spread(2103, 2300, 60, also=(-1, 0, 1, 127, 128, 129, 255, 1000, -1)), H=40, D=128, m=1, page=16,
+                          n_shared=2000, Wn=16),
+    "part_seen_512": dict(ts=spread(900, 1100, 40, also=(-1, 0, 1, 127, 128, 511)), H=128, D=512, m=1, page=64, n_shared=2048,
+                          Wn=16),
+    "part_seen_256": dict(ts=spread(900, 1100, 60, also=(-1, 0, 1, 127, 128, 511)), H=64, D=256, m=1, page=16, n_shared=1600,
+                          Wn=16),
+    "part_seen_64": dict(ts=spread(1000, 1200, 100, also=(-1, 0, 1, 127, 128, 511)), H=8, D=64, m=1, page=32, n_shared=3200,
+                         Wn=16, sinks=True),
+    "short_windows": dict(ts=spread(2048, 2060, 64, also=(0, 3, 14, 15)), H=16, D=128, m=1, page=16, n_shared=2048, Wn=100,
+                          ring_extra=50),
+    "missing_128": dict(ts=spread(2103, 2300, 60), H=40, D=128, m=1, page=16, n_shared=2000, Wn=16,
+                        drop=((None, 3, -1), (None, 90, 10 ** 6), (1, 126, -7), (59, 128, 10 ** 6))),
+    "missing_512": dict(ts=spread(2103, 2300, 24), H=128, D=512, m=1, page=64, n_shared=1984, Wn=16,
+                        drop=((None, 1, -1), (5, 32, -1))),
+    "big_scale": dict(ts=spread(2103, 2300, 60), H=40, D=128, m=1, page=16, n_shared=2000, Wn=16, scale=3.0),
+    "negative_scale": dict(ts=spread(2103, 2300, 60), H=40, D=128, m=1, page=16, n_shared=2000, Wn=16, scale=-0.3, rope=True),
+    "zero_scale": dict(ts=spread(2103, 2300, 60, also=(5,)), H=40, D=128, m=1, page=16, n_shared=2000, Wn=16, scale=0.0),
+    "fp8_128": dict(ts=spread(1103, 1300, 60, also=(-1, 0, 100)), H=40, D=128, m=1, page=16, n_shared=1008, Wn=16, fp8=True,
+                    drop=((None, 3, -1), (2, 65, -1))),
+    "fp8_512": dict(ts=spread(2103, 2300, 24), H=128, D=512, m=2, page=48, n_shared=960, Wn=128, fp8=True, rope=True),
+    "fp8_256_own": dict(ts=spread(300, 2300, 60), H=64, D=256, m=1, page=32, n_shared=0, Wn=30, fp8=True),
+}
+
+
+@pytest.mark.parametrize("name", sorted(ROW_TILES))
+def test_attend_paged_row_tiles(cuda, name):
+    c = Case(**ROW_TILES[name])
+    assert c.by_row_tiles()
+    # whatever workspace and output held before
+    ws = torch.full((csa_pkg.attend_paged_workspace_bytes(*c.q.shape, c.page, c.max_pages, c.n_shared, c.ring.shape[1], c.Wn,
+                                                          c.fp8),), 0xFF, dtype=torch.uint8, device=DEV)
+    out = torch.full_like(c.q, float("nan"))
+    got = c.run(cuda, workspace=ws, out=out)
+    assert cuda.csa_sync_status() == 0
+    assert got.data_ptr() == out.data_ptr()
+    c.check(got)
+    again = c.run(cuda)
+    assert torch.equal(again.view(torch.int16), got.view(torch.int16))  # the same sums in the same order
+    assert (got[c.pos < 0] == 0).all()
+
+
+@pytest.mark.parametrize("name", ["d512_h128", "d128_h16", "fp8_512"])
+def test_attend_paged_graph_follows_its_inputs(cuda, name):
+    """Captured on a side stream, replayed with other positions, queries and pages; beside another graph of its own."""
+    c, other = Case(**ROW_TILES[name]), Case(**dict(ROW_TILES["d64_h8"], seed=9))
+    B, nq = c.pos.shape
+    ws = torch.empty(csa_pkg.attend_paged_workspace_bytes(B, nq, c.q.shape[2], c.q.shape[3], c.page, c.max_pages, c.n_shared,
+                                                          c.ring.shape[1], c.Wn, c.fp8), dtype=torch.uint8, device=DEV)
+    out, out2 = torch.empty_like(c.q), torch.empty_like(other.q)
+    c.run(cuda, workspace=ws, out=out)
+    other.run(cuda, out=out2)
+    torch.cuda.synchronize()
+    g, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s1):
+        c.run(cuda, workspace=ws, out=out)
+    with torch.cuda.graph(g2, stream=s2):
+        other.run(cuda, out=out2)
+    # fewer entries seen, other queries, the batch's rows in another order
+    order = torch.randperm(B, device=DEV)
+    c.q.copy_(torch.randn_like(c.q, dtype=torch.float32))
+    c.table.copy_(c.table[order])
+    c.ring.copy_(c.ring[order])
+    if c.fp8:
+        c.re.copy_(c.re[order])
+    c.ring64 = c.ring64[order]
+    c.pos.copy_(c.pos[order])
+    out.fill_(float("nan"))
+    out2.fill_(float("nan"))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s1):
+        g.replay()
+        g.replay()
+    with torch.cuda.stream(s2):
+        g2.replay()
+    torch.cuda.synchronize()
+    assert cuda.csa_sync_status() == 0
+    c.check(out)
+    other.check(out2)
+
+
+def test_attend_paged_refusals(cuda):
+    c = Case(**CASES["shared_tile"])
+    def bad(exc, **kw):
+        with pytest.raises(exc):
+            c.run(cuda, **kw)
+    bad(csa_pkg.CsaError, n_shared=64)          # not whole pages
+    bad(csa_pkg.CsaError, n_shared=128 * 100)   # past the table
+    bad(csa_pkg.CsaError, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    bad(ValueError, out=torch.empty_like(c.q[:1]))
+    big = Case(**CASES["shared_tile"])
+    big.pos = big.pos.cpu()
+    with pytest.raises(TypeError):
+        big.run(cuda)
+    big = Case(**CASES["shared_tile"])
+    big.ring = big.ring[:, :8].contiguous()     # fewer rows than the window
+    with pytest.raises(csa_pkg.CsaError):
+        big.run(cuda)
+    big = Case(**CASES["shared_tile"])
+    big.table = big.table[:1].contiguous()
+    with pytest.raises(ValueError):
+        big.run(cuda)
+    big = Case(**CASES["shared_tile"])
+    big.gain = torch.ones(3, device=DEV)
+    with pytest.raises(ValueError):
+        big.run(cuda)
+    with pytest.raises(ValueError):             # one slot per row
+        cuda.csa_paged_write(c.q[0, 0].contiguous(), torch.zeros(3, dtype=torch.int64, device=DEV), c.pool)
+    with pytest.raises(TypeError):
+        cuda.csa_plan_pages(*(torch.zeros(3, dtype=torch.int64, device=DEV),) * 3, c.table, 4, 16, 16, 9, 9)
+    with pytest.raises(ValueError):             # negative room
+        z = torch.zeros(3, dtype=torch.int32, device=DEV)
+        cuda.csa_plan_pages(z, z, z, torch.zeros(3, 4, dtype=torch.int32, device=DEV), 4, 16, 16, -1, 9)
+
+
+# ----------------------------------------------------------------------------- the operators as a server runs them
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("batch", [5, 40])
+def test_prefill_and_decode_over_pages(cuda, batch, fp8):
+    """Requests with a common prompt: its pages are written once and noted in every row of the table, then a ragged
+    prefill and decode steps: plan, writes of the entries and of the window rows through its slot maps, attention."""
+    H, D, m, page, Wn, ring_rows = 8, 128, 4, 16, 24, 40
+    rng = np.random.default_rng(batch)
+    prompt = 64 * page * m                       # tokens of the shared prompt: 64 pages
+    total = prompt + 400
+    streams = W.normal_bf16((batch, total, D), 70, DEV)                 # window rows of every position
+    entries = W.normal_bf16((batch, total // m, D), 71, DEV)
+    streams[:, :prompt], entries[:, :prompt // m] = streams[:1, :prompt], entries[:1, :prompt // m]
+    n_pages = 64 + batch * 8 + 5
+    pool = torch.full((n_pages, page, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ring = torch.full((batch, ring_rows, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    if fp8:
+        pool8 = [torch.full((n_pages, page, D), 0x7F, dtype=torch.uint8, device=DEV),
+                 torch.full((n_pages, page, D // 128), 255, dtype=torch.uint8, device=DEV)]
+        ring8 = [torch.full((batch, ring_rows, D), 0x7F, dtype=torch.uint8, device=DEV),
+                 torch.full((batch, ring_rows, D // 128), 255, dtype=torch.uint8, device=DEV)]
+        round_trip = lambda x: dequant(*cuda.csa_quantize_fp8_kv(x.contiguous()))  # noqa: E731
+        streams64, entries64 = round_trip(streams), round_trip(entries)
+    else:
+        streams64, entries64 = streams.double(), entries.double()
+    ids = torch.tensor(rng.permutation(n_pages).astype(np.int32), device=DEV)
+    table = torch.full((batch, 80), -1, dtype=torch.int32, device=DEV)
+
+    def write(rows, slots, dst, dst8):
+        if fp8:
+            cuda.csa_paged_write_fp8kv(rows, slots, *dst8)
+        else:
+            cuda.csa_paged_write(rows, slots, dst)
+
+    def step(old, new, free):
+        """One step of every request; returns the pages taken."""
+        tokens, n_entries = int(new.sum()), int(((old + new) // m - old // m).sum())
+        t = lambda x: torch.tensor(x.astype(np.int32), device=DEV)  # noqa: E731
+        cu_t, cu_e, slots, pos, win, counts = cuda.csa_plan_pages(t(old), t(new), free, table, m, page, ring_rows,
+                                                                  tokens + 3, n_entries + 5)
+        assert counts.tolist()[:2] == [tokens, n_entries] and counts.tolist()[3] == 0
+        cu_t, cu_e = cu_t.tolist(), cu_e.tolist()
+        er = torch.cat([entries[b, old[b] // m:(old[b] + new[b]) // m] for b in range(len(old))] + [entries[0, :5]])
+        sr = torch.cat([streams[b, old[b]:old[b] + new[b]] for b in range(len(old))] + [streams[0, :3]])
+        write(er, slots, pool, pool8 if fp8 else None)
+        write(sr, win, ring, ring8 if fp8 else None)
+        assert pos.tolist()[:tokens] == [int(u) for b in range(len(old)) for u in range(old[b], old[b] + new[b])]
+        return int(counts[2])
+
+    # the prompt, by the first request; the others note its pages
+    zero = np.zeros(batch, np.int64)
+    first = zero.copy()
+    first[0] = prompt
+    used = step(zero, first, ids)
+    assert used == 64
+    table[1:, :64] = table[:1, :64]
+    # the window rows of the prompt's end, for every request
+    tail = torch.arange(prompt - Wn, prompt, device=DEV)
+    slots = (torch.arange(batch, device=DEV)[:, None] * ring_rows + tail % ring_rows).flatten()
+    write(streams[0, tail].repeat(batch, 1), slots, ring, ring8 if fp8 else None)
+    cached = zero + prompt
+    news = [rng.integers(1, 61, batch), np.ones(batch, np.int64), np.ones(batch, np.int64), rng.integers(0, 3, batch)]
+    for new in news:
+        used += step(cached, new, ids[used:])
+        cached = cached + new
+        q = torch.randn(batch, 1, H, D, device=DEV).to(torch.bfloat16)
+        pos = torch.tensor((cached - 1).astype(np.int32)[:, None], device=DEV)
+        for n_shared in (0, 64 * page):
+            if fp8:
+                out = cuda.hca_attend_paged_fp8kv(q, *pool8, table, m, *ring8, pos, Wn, D ** -0.5, n_shared=n_shared)
+            else:
+                out = cuda.hca_attend_paged(q, pool, table, m, ring, pos, Wn, D ** -0.5, n_shared=n_shared)
+            assert cuda.csa_sync_status() == 0
+            for b in range(batch):
+                t = int(cached[b]) - 1
+                x = torch.cat([entries64[b, :(t + 1) // m], streams64[b, max(0, t - Wn + 1):t + 1]])
+                y = q[b, 0].double()
+                y = y / (y.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt()
+                p = torch.softmax(y @ x.T * D ** -0.5, -1)
+                o, a = p @ x, p @ x.abs()
+                tol = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -10) * a
+                assert ((out[b, 0].double() - o).abs() <= tol).all(), (b, t, n_shared)
+
+
+def test_attend_paged_on_another_stream_and_two_at_once(cuda):
+    cs = [Case(**dict(ROW_TILES["d128_h16"], seed=s)) for s in (1, 2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for c, s in zip(cs, streams):
+        with torch.cuda.stream(s):
+            outs.append(c.run(cuda))
+    torch.cuda.synchronize()
+    for c, o in zip(cs, outs):
+        c.check(o)
