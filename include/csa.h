@@ -484,7 +484,7 @@ int csa_paged_write_fp8kv(const uint16_t *rows, const long long *slots, long lon
  * Workspace: with fp8 = 1.
  */
 size_t csa_attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared,
-                                        int ring_rows, int W, int fp8);
+                                        int ring_rows, int W, int fp8, int rewrite);
 int hca_attend_paged(const uint16_t *q, const float *q_gain, const float *sinks, const float *rope_cos,
                      const float *rope_sin, long long rope_positions, const uint16_t *pool, long long n_pages,
                      int page, const int *block_table, int max_pages, long long n_shared, int m,

@@ -67,7 +67,7 @@ def load() -> ctypes.CDLL:
         "csa_plan_pages": ([P, P, i32, i32, i32, i32, P, i64, P, i32, P, P, P, i64, P, P, i64, P, P, sz, P], i32),
         "csa_paged_write": ([P, P, i64, i32, P, i64, P], i32),
         "csa_paged_write_fp8kv": ([P, P, i64, i32, P, P, i64, P], i32),
-        "csa_attend_paged_workspace_bytes": ([i32, i32, i32, i32, i32, i32, i64, i32, i32, i32], sz),
+        "csa_attend_paged_workspace_bytes": ([i32, i32, i32, i32, i32, i32, i64, i32, i32, i32, i32], sz),
         "hca_attend_paged": ([P, P, P, P, P, i64, P, i64, i32, P, i32, i64, i32, P, i32, i32, P, i32, i32, i32, i32, f32,
                               f32, P, P, sz, P], i32),
         "hca_attend_paged_fp8kv": ([P, P, P, P, P, i64, P, P, i64, i32, P, i32, i64, i32, P, P, i32, i32, P, i32, i32,
@@ -532,8 +532,10 @@ def csa_paged_write_fp8kv(rows, slots, codes, exps):
 
 
 def attend_paged_workspace_bytes(batch: int, nq: int, H: int, D: int, page: int, max_pages: int, n_shared: int,
-                                 ring_rows: int, W: int, fp8: bool = False) -> int:
-    return int(load().csa_attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, ring_rows, W, int(fp8)))
+                                 ring_rows: int, W: int, fp8: bool = False, rewrite: bool = False) -> int:
+    """rewrite: the call has a q_gain, rope or a negative scale."""
+    return int(load().csa_attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, ring_rows, W, int(fp8),
+                                                       int(rewrite)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -571,8 +573,8 @@ def hca_attend_paged(q, pool, block_table, m: int, ring, q_pos, W: int, scale: f
     _need(ring, torch.bfloat16, "ring", 3)
     batch, nq, H, D, out = _paged(q, block_table, q_pos, pool, ring, q_gain, out)
     n_pages, page, max_pages = pool.shape[0], pool.shape[1], block_table.shape[1]
-    ws, wsb = _workspace(_attend_paged_bytes(_device(), batch, nq, H, D, page, max_pages, n_shared, ring.shape[1], W), q.device,
-                         workspace)
+    ws, wsb = _workspace(_attend_paged_bytes(_device(), batch, nq, H, D, page, max_pages, n_shared, ring.shape[1], W, False,
+                                             q_gain is not None or rope is not None or scale < 0), q.device, workspace)
     _check(L.hca_attend_paged(_p(q), _p(q_gain), _sinks(sinks, H), *_rope(rope, D), _p(pool), n_pages, page,
                               _p(block_table), max_pages, n_shared, m, _p(ring), ring.shape[1], W, _p(q_pos), batch,
                               nq, H, D, float(scale), float(eps), _p(out), _p(ws), wsb, _stream()), "hca_attend_paged")
@@ -588,8 +590,8 @@ def hca_attend_paged_fp8kv(q, pool8, pool8_exp, block_table, m: int, ring8, ring
     _fp8_rows(ring8, ring8_exp, "ring8")
     batch, nq, H, D, out = _paged(q, block_table, q_pos, pool8, ring8, q_gain, out)
     n_pages, page, max_pages = pool8.shape[0], pool8.shape[1], block_table.shape[1]
-    ws, wsb = _workspace(_attend_paged_bytes(_device(), batch, nq, H, D, page, max_pages, n_shared, ring8.shape[1], W, True),
-                         q.device, workspace)
+    ws, wsb = _workspace(_attend_paged_bytes(_device(), batch, nq, H, D, page, max_pages, n_shared, ring8.shape[1], W, True,
+                                             q_gain is not None or rope is not None or scale < 0), q.device, workspace)
     _check(L.hca_attend_paged_fp8kv(_p(q), _p(q_gain), _sinks(sinks, H), *_rope(rope, D), _p(pool8), _p(pool8_exp),
                                     n_pages, page, _p(block_table), max_pages, n_shared, m, _p(ring8), _p(ring8_exp),
                                     ring8.shape[1], W, _p(q_pos), batch, nq, H, D, float(scale), float(eps), _p(out),

@@ -413,13 +413,13 @@ static int validate_paged(const csa::PagedArgs &a) {
     if ((long long)a.ring_rows < (long long)a.W + a.nq - 1) return CSA_ERR_INVALID;
     if (a.n_pages > 0x7fffffffLL / a.page || cap > 0x7fffffffLL || (long long)a.batch * a.ring_rows > 0x7fffffffLL)
         return CSA_ERR_UNSUPPORTED;
-    if (a.H > 128 || !(a.D == 64 || a.D == 128 || a.D == 256 || a.D == 512)) return CSA_ERR_UNSUPPORTED;
+    if (a.H > 128 || (long long)a.batch * a.nq > 0x7fffff00LL / a.H || !(a.D == 64 || a.D == 128 || a.D == 256 || a.D == 512)) return CSA_ERR_UNSUPPORTED;
     return CSA_OK;
 }
 
 static int run_paged(const csa::PagedArgs &a, void *workspace, size_t workspace_bytes, void *stream) {
     const size_t need = csa::attend_paged_workspace_bytes(a.batch, a.nq, a.H, a.D, a.page, a.max_pages, a.n_shared,
-                                                          a.ring_rows, a.W, a.fp8.kv != nullptr);
+                                                          a.ring_rows, a.W, a.fp8.kv != nullptr, csa::paged_rewrite(a));
     if (need > 0 && (!al16(workspace) || workspace_bytes < need)) return CSA_ERR_WORKSPACE;
     csa::DevCtx ctx;
     if (!ctx_for_launch(&ctx)) return CSA_ERR_CUDA;
@@ -427,11 +427,11 @@ static int run_paged(const csa::PagedArgs &a, void *workspace, size_t workspace_
 }
 
 size_t csa_attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared,
-                                        int ring_rows, int W, int fp8) {
+                                        int ring_rows, int W, int fp8, int rewrite) {
     if (batch < 1 || nq < 1 || H < 1 || H > 128 || page < 1 || max_pages < 1 || n_shared < 0 || ring_rows < 1 || W < 1 ||
         !(D == 64 || D == 128 || D == 256 || D == 512) || n_shared > (long long)max_pages * page)
         return 0;
-    return csa::attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, ring_rows, W, fp8 != 0);
+    return csa::attend_paged_workspace_bytes(batch, nq, H, D, page, max_pages, n_shared, ring_rows, W, fp8 != 0, rewrite != 0);
 }
 
 int hca_attend_paged(const uint16_t *q, const float *q_gain, const float *sinks, const float *rope_cos,

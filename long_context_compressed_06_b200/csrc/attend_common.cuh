@@ -114,12 +114,15 @@ struct PrefixArgs {
     // entries in order, then own_cap rows of each request's own entries, then the rings
     const uint16_t *keys;
     int own_cap;
+    uint16_t *hi, *lo;     // the query rows under gain, sign and RoPE as hi + lo (null: a.q itself),
+    float *rq;             // and their factors (launch_query_rows)
     float *part;           // [partials][128][DP], see above
     float2 *ml;            // [partials][128]
     int2 *meet;            // [row_tiles] the first range that meets a row tile, and how many do (out)
 };
 
 PrefixPlan prefix_plan(long long rows);
+int launch_query_rows(const PrefixArgs &p, cudaStream_t st);
 int launch_expand_rows(const PrefixArgs &p, uint16_t *out, cudaStream_t st);  // that copy
 int launch_attend_prefix(const PrefixArgs &p, const DevCtx &ctx, cudaStream_t st);
 

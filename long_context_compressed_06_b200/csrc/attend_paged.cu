@@ -143,7 +143,7 @@ struct PagedPlan {
     PrefixPlan prefix;  // pairs > 0: attend_prefix.cu
     int splits;
     long long keys_per_split;
-    size_t keys, part, ml, meet, bytes;  // offsets
+    size_t keys, hi, lo, rq, part, ml, meet, bytes;  // offsets
 };
 
 size_t take(size_t &at, size_t bytes) {
@@ -176,8 +176,10 @@ bool prefix_pays(long long n_bq, int H, int D, long long n_shared, long long own
     return t_prefix < t_gather;
 }
 
+// rewrite: a gain, RoPE or a negative scale changes the query rows.  The row-tile kernel keeps them in 16 bits, the
+// gather kernel rounds them to 8: with them the former is taken wherever it can be.
 PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared, int ring_rows, int W,
-                     bool fp8) {
+                     bool fp8, bool rewrite) {
     PagedPlan pl = {};
     const long long n_bq = (long long)batch * nq, rows = n_bq * H, cap = (long long)max_pages * page;
     const long long copy = fp8 ? (n_shared + batch * (cap - n_shared + ring_rows)) * D * (long long)sizeof(uint16_t) : 0;
@@ -187,8 +189,13 @@ PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, l
     attend_tc_plan(n_bq, H, cap + W, &pl.splits, &pl.keys_per_split);
     const PrefixPlan prefix = prefix_plan(std::min(rows, 0x7fffffffLL));
     if (rows <= 0x7fffffffLL - kPrefixRows && copy <= kMaxCopyBytes && tiles <= 0x7fffffffLL / (rows / kPrefixRows + 1) &&
-        prefix_pays(n_bq, H, D, n_shared, cap - n_shared, nq, pl, W, fp8, prefix)) {
+        (rewrite || prefix_pays(n_bq, H, D, n_shared, cap - n_shared, nq, pl, W, fp8, prefix))) {
         pl.prefix = prefix;
+        if (rewrite) {
+            pl.hi = take(at, (size_t)rows * D * sizeof(uint16_t));
+            pl.lo = take(at, (size_t)rows * D * sizeof(uint16_t));
+            pl.rq = take(at, (size_t)rows * sizeof(float));
+        }
         if (fp8) pl.keys = take(at, (size_t)copy);
         pl.part = take(at, (size_t)pl.prefix.partials() * kPrefixRows * prefix_dims(D) * sizeof(float));
         pl.ml = take(at, (size_t)pl.prefix.partials() * kPrefixRows * sizeof(float2));
@@ -204,8 +211,8 @@ PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, l
 }  // namespace
 
 size_t attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared,
-                                    int ring_rows, int W, bool fp8) {
-    return paged_plan(batch, nq, H, D, page, max_pages, n_shared, ring_rows, W, fp8).bytes;
+                                    int ring_rows, int W, bool fp8, bool rewrite) {
+    return paged_plan(batch, nq, H, D, page, max_pages, n_shared, ring_rows, W, fp8, rewrite).bytes;
 }
 
 int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const DevCtx &ctx, cudaStream_t st) {
@@ -219,7 +226,7 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     a.table = p.table; a.max_pages = p.max_pages; a.page = p.page; a.n_pages = p.n_pages;
     a.win_rows = p.ring_rows; a.W = p.W; a.q_pos = p.q_pos; a.nq = p.nq; a.n_bq = (long long)p.batch * p.nq;
     a.H = p.H; a.D = p.D; a.scale = p.scale; a.eps = p.eps; a.out = p.out;
-    const PagedPlan pl = paged_plan(p.batch, a.nq, a.H, a.D, a.page, a.max_pages, p.n_shared, p.ring_rows, a.W, fp8);
+    const PagedPlan pl = paged_plan(p.batch, a.nq, a.H, a.D, a.page, a.max_pages, p.n_shared, p.ring_rows, a.W, fp8, paged_rewrite(p));
     if (pl.bytes > 0 && (!ws || ws_bytes < pl.bytes)) return CSA_ERR_WORKSPACE;
     char *w = static_cast<char *>(ws);
     a.splits = pl.splits;
@@ -236,6 +243,13 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
         x.n_shared = p.n_shared;
         x.keys = p.pool;
         x.own_cap = fp8 ? (int)(a.N - p.n_shared) : -1;
+        if (paged_rewrite(p)) {
+            x.hi = reinterpret_cast<uint16_t *>(w + pl.hi);
+            x.lo = reinterpret_cast<uint16_t *>(w + pl.lo);
+            x.rq = reinterpret_cast<float *>(w + pl.rq);
+            rc = launch_query_rows(x, st);
+            if (rc != CSA_OK) return rc;
+        }
         if (fp8) {
             uint16_t *keys = reinterpret_cast<uint16_t *>(w + pl.keys);
             rc = launch_expand_rows(x, keys, st);

@@ -25,6 +25,13 @@
 // The tensor cores' operand reads (224 KiB), these loads and P share the
 // 128 B/cycle of shared memory, which bounds the kernel at D = 512.
 //
+// A gain, RoPE or a negative scale changes the query rows first, and rounding
+// them to bf16 again would cost as much accuracy as the output's own rounding
+// does (2.5e-3 instead of 2.0e-3 in all, against 64 bits).  A launch before
+// writes them as a sum of two bf16 numbers (hi + lo, 16 bits), and S gets both
+// products; lo passes through K's ring beside each piece of K, since at D = 512
+// shared memory has no room for it.
+//
 // Warps: 0 and 1 producers of K, 2 and 3 of V, 4 and 5 MMA issuers of Q K^T and of
 // P V on the pair's leader (one thread for both was busy for longer than the
 // tensor cores: a satisfied barrier wait takes ~140 cycles, an MMA ~20), 6
@@ -83,6 +90,9 @@ struct Params {
     PrefixPlan plan;
     int n_shared;
     int linear;
+    int lo;           // the query rows are hi + lo, and rq holds their factors
+    int dependent;    // launched as a programmatic dependent of what writes the copies
+    const float *rq;
     int2 *meet;       // [row_tiles], see PrefixArgs
     FastDiv H, nq, m, page, ring;
     const uint16_t *keys;  // the pool's rows; linear: the copy's, see PrefixArgs
@@ -110,7 +120,7 @@ struct Tile {
     int rows[8];       // row of key 16 i in the pool, the rings or (linear) the copy; < 0: none, reads as zeros
     uint32_t zero[4];  // keys that a copy brings and no row takes: cleared in V
     CSA_DEVINL int ent() const { return ent_rt & 255; }
-    CSA_DEVINL int rt() const { return ent_rt >> 8; }
+    CSA_DEVINL int rt() const { return (int)((uint32_t)ent_rt >> 8); }
 };
 
 struct Smem {
@@ -381,38 +391,10 @@ CSA_DEVINL float query_squares(uint8_t *q, int r, int q4) {
     return ss[0] + ss[1];
 }
 
-// Rewrites the same units: the gain and the scale's sign, then the rotation of the
-// trailing kRopeDim channels (unit j of the slice pairs with j + 4, also this
-// thread's); rounded to bf16, as the tensor cores' operand is.
-template <int DP>
-CSA_DEVINL void query_rewrite(const AttendArgs &a, uint8_t *q, int r, int q4, int t) {
-    const int r0 = a.D / 8 - kRopeDim / 8;  // first rotated unit
-    // without a gain or a sign only the rotated units change
-    const int first = a.q_gain || a.scale < 0.f ? 0 : r0;
-#pragma unroll 2
-    for (int unit = first + q4; unit * 8 < a.D; unit += 8) {
-        uint4 *p0 = query_unit<DP>(q, r, unit), *p1 = query_unit<DP>(q, r, unit + 4);
-        float x[8], y[8];
-        unpack8(*p0, x);
-        unpack8(*p1, y);
-        const float sign = a.scale < 0.f ? -1.f : 1.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] *= a.q_gain ? sign * __ldg(a.q_gain + unit * 8 + e) : sign;
-            y[e] *= a.q_gain ? sign * __ldg(a.q_gain + unit * 8 + 32 + e) : sign;
-        }
-        if (a.rope_cos && unit >= r0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 cs = rope_cs(a, t, (unit - r0) * 8 + e);
-                const float x0 = x[e], y0 = y[e];
-                x[e] = x0 * cs.x - y0 * cs.y;
-                y[e] = y0 * cs.x + x0 * cs.y;
-            }
-        }
-        *p0 = pack8(x);
-        *p1 = pack8(y);
-    }
+// 1 / RMS of a row of these squares times the softmax scale (its sign is the query
+// rows'), in log2 units; above 0, so that a masked score stays -inf
+CSA_DEVINL float row_factor(const AttendArgs &a, float ss) {
+    return fmaxf((1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
 }
 
 // the first n of 32 bits
@@ -455,7 +437,7 @@ CSA_DEVINL uint32_t key_mask(const Params &p, const Tile &d, int off, const Row 
 
 // The tensor maps of one call, [64-dim chunk][row][64] each.
 struct Maps {
-    CUtensorMap q;         // 64 rows x 2 chunks
+    CUtensorMap q, lo;     // 64 rows x 2 chunks
     CUtensorMap k, v;      // pool or copy: box rows x 2 chunks (box 64) or 1, vbox rows x an SM's half of V
     CUtensorMap k16, v16;  // pool, 16 rows x 1 chunk, 16 rows x an SM's half
     CUtensorMap rk16, rv16;  // the rings, the same
@@ -471,8 +453,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const AttendArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)tc::cluster_rank(), pair = blockIdx.x >> 1;
-    // the query tile is rewritten for a gain, RoPE or a negative scale (its sign goes to the rows)
-    const bool q_rw = a.q_gain != nullptr || a.rope_cos != nullptr || a.scale < 0.f;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * kSlots; ++i) {
@@ -489,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(s.rbar + i, kSoftWarps / 2);
         }
         mbar_init(s.qland, 1);
-        mbar_init(s.qready, q_rw ? 2 * kSoftWarps : 2);  // leader
+        mbar_init(s.qready, 2);  // leader: each CTA's query warp
         mbar_init(s.qempty, 1 + kSoftWarps);
         for (int i = 0; i < 2; ++i) mbar_init(s.vfix + i, 1);
         for (int i = 0; i < kDescs; ++i) {
@@ -527,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ producers
         // TMA copies are issued by one thread inside an elect_one branch (one issued by every lane
         // under a guard, or by a diverged lane, took ~200 cycles: more than the MMAs that it feeds).
-        if (p.linear) asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' copy
+        if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
         const bool v = warp >= 2;  // K's or V's ring
         const int ring = v ? kSlots : 0;
         const uint32_t full0 = tc::map_to_rank(smem_u32(s.full + ring), 0), slots = smem_u32(s.slots) + ring * kSlotBytes;
@@ -539,9 +519,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!(ok = dp != nullptr)) break;
             const Tile &d = *dp;
             if (d.flags & kEnd) break;
+            const int lo = v ? 0 : p.lo;  // K's ring: a piece of K, (lo) the query rows' piece beside it
 #pragma unroll 1
-            for (int w = 0; w < Lt::kPieces && ok; ++w, ++it) {
+            for (int x = 0; x < Lt::kPieces << lo && ok; ++x, ++it) {
                 if ((it ^ (uint32_t)warp) & 1u) continue;
+                const int w = x >> lo;
                 const uint32_t sl = it % kSlots, par = ((it / kSlots) & 1u) ^ 1u, empty = smem_u32(s.empty + ring + sl);
                 const uint32_t dst = slots + sl * kSlotBytes, full = full0 + sl * 8;
                 if (!(ok = warp_wait(empty, par, p.ctx, s.abort_flag))) break;
@@ -550,16 +532,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!v) {
                     if (tc::elect_one()) {
                         mbar_arrive_expect_tx_cluster(full, kSlotBytes);
-                        if (p.box == 64 && !mixed) {
+                        if (lo && (x & 1)) {
+                            tc::tma_load_3d_2sm(dst, &maps.lo, full, 0, d.rt() * kPrefixRows + rank * 64, 2 * w);
+                        } else if (p.box == 64 && !mixed) {
                             tc::tma_load_3d_2sm(dst, &maps.k, full, 0, d.rows[rank * 4], 2 * w);
                         } else {
                             const int box = mixed ? 16 : p.box;
-                            for (int x = 0; x < 64; x += box) {
-                                const int i = rank * 4 + x / 16, row = d.rows[i];
+                            for (int y = 0; y < 64; y += box) {
+                                const int i = rank * 4 + y / 16, row = d.rows[i];
                                 const CUtensorMap *map =
                                     !mixed ? &maps.k : (d.flags >> (kRingShift + i)) & 1 ? &maps.rk16 : &maps.k16;
-                                tc::tma_load_3d_2sm(dst + x * 128, map, full, 0, row, 2 * w);
-                                tc::tma_load_3d_2sm(dst + 8192 + x * 128, map, full, 0, row, 2 * w + 1);
+                                tc::tma_load_3d_2sm(dst + y * 128, map, full, 0, row, 2 * w);
+                                tc::tma_load_3d_2sm(dst + 8192 + y * 128, map, full, 0, row, 2 * w + 1);
                             }
                         }
                     }
@@ -574,11 +558,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (tc::elect_one()) {
                     const uint32_t bar = fix ? tc::map_to_rank(vfix, rank) : full;
                     mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
-                    for (int x = 0; x < Lt::kVKeys; x += vbox) {
-                        const int i = (w * Lt::kVKeys + x) / 16;
+                    for (int y = 0; y < Lt::kVKeys; y += vbox) {
+                        const int i = (w * Lt::kVKeys + y) / 16;
                         const CUtensorMap *map =
                             !mixed ? &maps.v : (d.flags >> (kRingShift + i)) & 1 ? &maps.rv16 : &maps.v16;
-                        tc::tma_load_3d_2sm(dst + x * (Lt::kVChunks * 128), map, bar, 0, d.rows[i], rank * Lt::kVChunks);
+                        tc::tma_load_3d_2sm(dst + y * (Lt::kVChunks * 128), map, bar, 0, d.rows[i], rank * Lt::kVChunks);
                     }
                 }
                 __syncwarp();
@@ -630,6 +614,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint32_t off = (k >> 2) * 8192 + (k & 3) * 32;
                         tc::mma_f16_2sm(tmem + kSCols + b * 64, qdesc + ((w * 16384 + off) >> 4),
                                         kdesc + ((sl * kSlotBytes + off) >> 4), p.idesc_qk, (w | k) ? 1u : 0u);
+                    }
+                    if (p.lo) {
+                        ++it;
+                        const uint32_t ll = it % kSlots;
+                        if (!(ok = bar_wait(smem_u32(s.full + ll), (it / kSlots) & 1u, p.ctx, s.abort_flag))) break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t off = (k >> 2) * 8192 + (k & 3) * 32;
+                            tc::mma_f16_2sm(tmem + kSCols + b * 64, kdesc + ((ll * kSlotBytes + off) >> 4),
+                                            kdesc + ((sl * kSlotBytes + off) >> 4), p.idesc_qk, 1u);
+                        }
+                        tc::mma_commit_2sm(smem_u32(s.empty + ll));
                     }
                     tc::mma_commit_2sm(smem_u32(s.empty + sl));
                 }
@@ -698,6 +695,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == kQueryWarp) {
         // ------------------------------------------------------------ query tiles
         const uint32_t qland = tc::map_to_rank(smem_u32(s.qland), rank), qready0 = tc::map_to_rank(smem_u32(s.qready), 0);
+        if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
         uint32_t nq = 0;
         bool ok = true;
         for (uint32_t g = 0; ok; ++g) {
@@ -716,7 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (!(ok = warp_wait(smem_u32(s.qland), nq & 1u, p.ctx, s.abort_flag))) break;
-            if (!q_rw) mbar_arrive_cluster(qready0, lane == 0);  // else the softmax warps rewrite the tile first
+            mbar_arrive_cluster(qready0, lane == 0);
             ++nq;
         }
         copies = !ok;
@@ -832,7 +830,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) {
                     d->flags = flags;
-                    d->ent_rt = ent | un.rt << 8;
+                    d->ent_rt = (int)((uint32_t)ent | (uint32_t)un.rt << 8);
                     d->n = n;
                     d->b = b;
                     d->e_first = e_first;
@@ -863,8 +861,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t rbar_n = 0;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t sempty0 = tc::map_to_rank(smem_u32(s.sempty), 0), pfull0 = tc::map_to_rank(smem_u32(s.pfull), 0);
-        const uint32_t qready0 = tc::map_to_rank(smem_u32(s.qready), 0);
         const int n_rows = (int)(a.n_bq * a.H);
+        if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
         uint32_t nq = 0;
         Row rw = {-1, 0, 0, {0, 0}};
         int vis_min = 0;  // the fewest entries that a row of this warp sees
@@ -910,20 +908,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             vis_min = __reduce_min_sync(0xffffffffu, rw.vis);
             if (!wait(s.qland, nq & 1u)) break;
             ++nq;
-            sums[q4 * 32 + lane] = query_squares<DP>(s.q, r, q4);
-            if (q_rw) {
-                query_rewrite<DP>(a, s.q, r, q4, rw.t);
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                mbar_arrive_cluster(qready0, lane == 0);
-            }
+            if (!p.lo) sums[q4 * 32 + lane] = query_squares<DP>(s.q, r, q4);
             __syncwarp();
             mbar_arrive(smem_u32(s.qempty), lane == 0);
             if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
-            const float ss = (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]);
-            // 1 / RMS times the softmax scale (without its sign), in log2 units; above 0, so that a
-            // masked score stays -inf
-            rq = fmaxf((1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
+            if (p.lo) {
+                if (row < n_rows) rq = p.rq[row];
+            } else {
+                const float ss = (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]);
+                rq = row_factor(a, ss);
+            }
+            if (rw.t < 0) rq = 1.f;  // an empty slot's query may hold anything: no NaN for its masked scores
             m = m_l = -INFINITY;
             l = 0.f;
             if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
@@ -1070,6 +1065,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
+// Query rows under a gain, the scale's sign and RoPE (channel D-64+j of the slice
+// rotates with D-32+j), as hi + lo in bf16, and their factors.  A warp per row.
+__global__ void __launch_bounds__(256)
+    query_rows_kernel(const AttendArgs a, const FastDiv H, int n_rows, uint16_t *__restrict__ hi, uint16_t *__restrict__ lo,
+                      float *__restrict__ rq) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, row = (int)(blockIdx.x * 8 + (threadIdx.x >> 5)), units = a.D / 8;
+    if (row >= n_rows) return;
+    const float sign = a.scale < 0.f ? -1.f : 1.f;
+    const long long t = __ldg(a.q_pos + H.div(row));
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.q) + (size_t)row * units;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // units lane, lane + 32 (D = 512); the rotated ones are the last 8 of a row
+        const int u = lane + i * 32;
+        if (i * 32 >= units) break;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (u < units) unpack8(ldg16(src + u), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ss = fmaf(x[e], x[e], ss);
+            x[e] *= a.q_gain && u < units ? sign * __ldg(a.q_gain + u * 8 + e) : sign;
+        }
+        if (a.rope_cos) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __shfl_xor_sync(0xffffffffu, x[e], 4);
+            if (u >= units - 8 && u < units) {
+                const bool first = u < units - 4;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 cs = rope_cs(a, t, ((u - (units - 8)) & 3) * 8 + e);
+                    x[e] = first ? x[e] * cs.x - y[e] * cs.y : x[e] * cs.x + y[e] * cs.y;
+                }
+            }
+        }
+        if (u < units) {
+            const uint4 h = pack8(x);
+            float back[8];
+            unpack8(h, back);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] -= back[e];
+            reinterpret_cast<uint4 *>(hi)[(size_t)row * units + u] = h;
+            reinterpret_cast<uint4 *>(lo)[(size_t)row * units + u] = pack8(x);
+        }
+    }
+    ss = warp_sum(ss);
+    if (lane == 0) rq[row] = row_factor(a, ss);
+}
+
 // The rows of an FP8 cache that a call reads, as bf16 (exact) in the order of
 // PrefixArgs; entries without a page are zero, those that no query sees stay as
 // they are (nothing reads them).
@@ -1127,6 +1172,9 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     p.plan = x.plan;
     p.n_shared = (int)x.n_shared;
     p.linear = x.own_cap >= 0 ? 1 : 0;
+    p.lo = x.lo ? 1 : 0;
+    p.rq = x.rq;
+    p.dependent = p.linear || p.lo;
     p.keys = x.keys;
     p.batch = (int)(x.a.n_bq / x.a.nq);
     p.own_cap = x.own_cap;
@@ -1159,7 +1207,8 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     const long long key_rows = p.linear ? x.n_shared + batch * x.own_cap + rings : x.a.n_pages * x.a.page;
     constexpr int kChunks = Layout<DP>::kVChunks;
     Maps maps = {};
-    if (!encode(&maps.q, x.a.q, x.a.n_bq * x.a.H, 64, 2) ||
+    if (!encode(&maps.q, x.lo ? x.hi : x.a.q, x.a.n_bq * x.a.H, 64, 2) ||
+        (x.lo && !encode(&maps.lo, x.lo, x.a.n_bq * x.a.H, 64, 2)) ||
         !encode(&maps.k, x.keys, key_rows, p.box, p.box == 64 ? 2 : 1) ||
         !encode(&maps.v, x.keys, key_rows, p.vbox, kChunks))
         return CSA_ERR_CUDA;
@@ -1177,7 +1226,7 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = p.linear ? 1 : 0;  // a dependent of the rows' copy
+    cfg.numAttrs = p.dependent ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, maps, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
@@ -1188,6 +1237,12 @@ PrefixPlan prefix_plan(long long rows) {
     pl.row_tiles = (int)((rows + kPrefixRows - 1) / kPrefixRows);
     pl.pairs = std::max(num_sms() / 2, 1);
     return pl;
+}
+
+int launch_query_rows(const PrefixArgs &x, cudaStream_t st) {
+    const int rows = (int)(x.a.n_bq * x.a.H);
+    query_rows_kernel<<<(unsigned)(rows + 7) / 8, 256, 0, st>>>(x.a, FastDiv::by((uint32_t)x.a.H), rows, x.hi, x.lo, x.rq);
+    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 int launch_expand_rows(const PrefixArgs &x, uint16_t *out, cudaStream_t st) {

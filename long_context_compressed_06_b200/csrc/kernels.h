@@ -92,7 +92,8 @@ struct PagedArgs {
 };
 
 size_t attend_paged_workspace_bytes(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared,
-                                    int ring_rows, int W, bool fp8);
+                                    int ring_rows, int W, bool fp8, bool rewrite);
+inline bool paged_rewrite(const PagedArgs &a) { return a.q_gain || a.rope_cos || a.scale < 0.f; }
 int launch_attend_paged(const PagedArgs &a, void *ws, size_t ws_bytes, const DevCtx &ctx, cudaStream_t st);
 
 // Block tables and slot maps (csa_plan_pages); the pointers' shapes are the ABI's.

@@ -3,8 +3,9 @@
 Tolerance of the attention, element by element, from its roundings (bf16: half a step is 2^-8 of the value):
   * the output is rounded once:                                        2^-8 |o|
   * the weights p_j are rounded to bf16 for the second product:       2^-8 A,  A = sum_j p_j |x_j| / sum_j p_j
-  * with a gain or RoPE the query is rounded to bf16 first, which moves every score by at most
-    e = 2^-8 scale sum_d |q_d x_d| and the normalised weights by at most exp(2 e) - 1:  (exp(2 e) - 1) A
+  * with a gain or RoPE the query is rounded first, to the sum of two bf16 numbers (query by query, without row tiles:
+    to one), which moves every score by at most e = 2^-16 (2^-8) scale sum_d |q_d x_d|, plus 2^-20 of it for the 32-bit
+    arithmetic, and the normalised weights by at most exp(2 e) - 1:  (exp(2 e) - 1) A
   * products and sums in 32 bits (512 terms, truncating tensor-core sums included): 2^-10 A
 A rotated output mixes pairs of channels: their A enters by |cos| and |sin|.
 """
@@ -227,7 +228,7 @@ def attend_ref(q, pool, table, m, ring, pos, Wn, scale, eps, gain, sinks, rope):
                 a[:, -64:-32], a[:, -32:] = u * c.abs() + v * s.abs(), v * c.abs() + u * s.abs()
             out[b, i], mag[b, i] = o, a
             if gain is not None or rope is not None:
-                eps_s[b, i] = 2.0 ** -8 * abs(scale) * (y.abs() @ x.abs().T).amax(-1, keepdim=True)
+                eps_s[b, i] = (2.0 ** -16 + 2.0 ** -20) * abs(scale) * (y.abs() @ x.abs().T).amax(-1, keepdim=True)
     return out, mag, eps_s
 
 
@@ -308,18 +309,29 @@ class Case:
                                               self.Wn, self.scale, **kw)
         return csa.hca_attend_paged(self.q, self.pool, self.table, self.m, self.ring, self.pos, self.Wn, self.scale, **kw)
 
-    def ref(self):
+    def ref(self, at=slice(None)):
         def d(x):
             return None if x is None else x.double()
-        return attend_ref(self.q.double(), self.pool64, self.table, self.m, self.ring64, self.pos.cpu(), self.Wn, self.scale,
-                          1e-6, d(self.gain), d(self.sinks), None if self.rope is None else tuple(d(x) for x in self.rope))
+        return attend_ref(self.q[at].double(), self.pool64, self.table[at], self.m, self.ring64[at], self.pos[at].cpu(),
+                          self.Wn, self.scale, 1e-6, d(self.gain), d(self.sinks),
+                          None if self.rope is None else tuple(d(x) for x in self.rope))
 
-    def check(self, got, ref=None):
+    def check(self, got, ref=None, n_shared=None):
         out, mag, e = ref or self.ref()
+        if not self.by_row_tiles(n_shared):
+            e = e * 256
         tol = 2.0 ** -8 * out.abs() + (2.0 ** -8 + torch.expm1(2 * e) + 2.0 ** -10) * mag
         err = (got.double() - out).abs()
         assert got.isfinite().all()
         assert (err <= tol).all(), (float((err - tol).max()), (err > tol).nonzero()[:4].tolist())
+
+    def workspace_bytes(self, n_shared=None):
+        return csa_pkg.attend_paged_workspace_bytes(*self.q.shape, self.page, self.max_pages,
+                                                    self.n_shared if n_shared is None else n_shared, self.ring.shape[1],
+                                                    self.Wn, self.fp8, self.rewrite())
+
+    def rewrite(self):
+        return self.gain is not None or self.rope is not None or self.scale < 0
 
     def by_row_tiles(self, n_shared=None):
         """Whether the call takes the kernel over row tiles of the whole batch: its workspace holds a partial per pair
@@ -329,10 +341,11 @@ class Case:
         tiles = -(-B * nq * H // 128)
         parts = torch.cuda.get_device_properties(0).multi_processor_count // 2 + tiles
         want = [parts * 128 * max(D, 128) * 4, parts * 128 * 8, tiles * 8]
+        if self.rewrite():
+            want += [B * nq * H * D * 2, B * nq * H * D * 2, B * nq * H * 4]
         if self.fp8:
             want.append((n_shared + B * (self.max_pages * self.page - n_shared + self.ring.shape[1])) * D * 2)
-        return csa_pkg.attend_paged_workspace_bytes(B, nq, H, D, self.page, self.max_pages, n_shared, self.ring.shape[1],
-                                                    self.Wn, self.fp8) == sum(-(-w // 256) * 256 for w in want)
+        return self.workspace_bytes(n_shared) == sum(-(-w // 256) * 256 for w in want)
 
 
 CASES = {
@@ -391,7 +404,7 @@ def test_attend_paged(cuda, name):
     for n_shared in sorted({0, c.n_shared}):
         got = c.run(cuda, n_shared=n_shared)
         assert cuda.csa_sync_status() == 0
-        c.check(got, ref)
+        c.check(got, ref, n_shared)
     empty = (c.pos < 0).cpu()
     assert (got.cpu()[empty] == 0).all()
 
@@ -452,8 +465,7 @@ def test_attend_paged_row_tiles(cuda, name):
     c = Case(**ROW_TILES[name])
     assert c.by_row_tiles()
     # whatever workspace and output held before
-    ws = torch.full((csa_pkg.attend_paged_workspace_bytes(*c.q.shape, c.page, c.max_pages, c.n_shared, c.ring.shape[1], c.Wn,
-                                                          c.fp8),), 0xFF, dtype=torch.uint8, device=DEV)
+    ws = torch.full((c.workspace_bytes(),), 0xFF, dtype=torch.uint8, device=DEV)
     out = torch.full_like(c.q, float("nan"))
     got = c.run(cuda, workspace=ws, out=out)
     assert cuda.csa_sync_status() == 0
@@ -464,13 +476,47 @@ def test_attend_paged_row_tiles(cuda, name):
     assert (got[c.pos < 0] == 0).all()
 
 
-@pytest.mark.parametrize("name", ["d512_h128", "d128_h16", "fp8_512"])
+@pytest.mark.parametrize("kw", [
+    CASES["own_only"], CASES["part_seen"], ROW_TILES["part_seen_128"], ROW_TILES["d128_own_only"], ROW_TILES["fp8_128"],
+    dict(ROW_TILES["part_seen_512"], rope=True, gain=True, sinks=True), dict(ROW_TILES["part_seen_64"], gain=True)])
+def test_attend_paged_empty_slots_hold_anything(cuda, kw):
+    """The query of an empty slot of the batch may be NaN or infinite: its output is zero, the others' theirs."""
+    c = Case(**kw)
+    empty = c.pos < 0
+    assert empty.any()
+    c.q[empty] = torch.where(torch.arange(c.q.shape[-1], device=DEV) % 2 == 0, float("nan"), float("inf")).to(c.q.dtype)
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    assert (got[empty] == 0).all()
+    c.check(got)
+
+
+def test_attend_paged_very_many_row_tiles(cuda):
+    """More row tiles than the kernel counts at once."""
+    c = Case(ts=[[390 + 11 * b + i for i in range(64)] for b in range(130)], H=128, D=64, m=8, page=16, n_shared=48, Wn=9)
+    assert c.by_row_tiles()
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    assert got.isfinite().all()
+    at = torch.tensor([0, 1, 63, 127, 128, 129], device=DEV)  # row tiles from 8192 on among them
+    c.check(got[at], c.ref(at))
+
+
+def test_attend_paged_fp8_beyond_the_copy(cuda):
+    """Tables so wide that the FP8 rows are not copied: query by query."""
+    c = Case(**ROW_TILES["fp8_512"], gain=True, cols=2900)
+    assert not c.by_row_tiles()
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    c.check(got)
+
+
+@pytest.mark.parametrize("name", ["d512_h128", "d128_h16", "fp8_512", "d512_h128_nq4"])
 def test_attend_paged_graph_follows_its_inputs(cuda, name):
     """Captured on a side stream, replayed with other positions, queries and pages; beside another graph of its own."""
     c, other = Case(**ROW_TILES[name]), Case(**dict(ROW_TILES["d64_h8"], seed=9))
-    B, nq = c.pos.shape
-    ws = torch.empty(csa_pkg.attend_paged_workspace_bytes(B, nq, c.q.shape[2], c.q.shape[3], c.page, c.max_pages, c.n_shared,
-                                                          c.ring.shape[1], c.Wn, c.fp8), dtype=torch.uint8, device=DEV)
+    B = c.pos.shape[0]
+    ws = torch.empty(c.workspace_bytes(), dtype=torch.uint8, device=DEV)
     out, out2 = torch.empty_like(c.q), torch.empty_like(other.q)
     c.run(cuda, workspace=ws, out=out)
     other.run(cuda, out=out2)

@@ -88,7 +88,8 @@ def test_attend_paged_refuses(lib, changed):
 
 @pytest.mark.parametrize("changed", [
     dict(H=129), dict(D=96), dict(D=1024), dict(n_pages=2 ** 31 // 16 + 1), dict(max_pages=2 ** 31 // 16),
-    dict(batch=2 ** 24, ring_rows=130)])
+    dict(batch=2 ** 24, ring_rows=130), dict(batch=2 ** 23, nq=2, H=128, ring_rows=129),
+    dict(batch=2 ** 30, nq=2 ** 30, ring_rows=2 ** 30 + 127)])
 def test_attend_paged_unsupported(lib, changed):
     assert call(lib.hca_attend_paged, BF, BF_OK, **changed) == UNS
     assert call(lib.hca_attend_paged_fp8kv, F8, F8_OK, **changed) == UNS
@@ -111,6 +112,9 @@ def test_attend_paged_workspace(lib):
         fn, names, ok = (lib.hca_attend_paged_fp8kv, F8, F8_OK) if fp8 else (lib.hca_attend_paged, BF, BF_OK)
         assert call(fn, names, ok, **change) == WS
         assert call(fn, names, ok, **dict(change, wsb=need, ws=M8)) == WS
+    # a gain, RoPE or a negative scale needs its own
+    assert csa.attend_paged_workspace_bytes(64, 1, 16, 128, 64, 300, 8192, 128, 128, False, True) >= \
+        csa.attend_paged_workspace_bytes(64, 1, 16, 128, 64, 300, 8192, 128, 128) + 2 * 64 * 16 * 128 * 2
     assert csa.attend_paged_workspace_bytes(0, 1, 16, 128, 64, 300, 8192, 128, 128) == 0
     assert csa.attend_paged_workspace_bytes(2, 1, 16, 100, 64, 300, 8192, 128, 128) == 0
 
