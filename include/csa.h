@@ -458,12 +458,18 @@ int csa_paged_write_fp8kv(const uint16_t *rows, const long long *slots, long lon
  * used, whatever they hold (unallocated pages may hold NaN).
  *
  * n_shared: the first n_shared entries are the same pages in every row of the
- * table (a multiple of page; 0 = none).  They are read through row 0 of the
- * table, once for all requests: the query rows of the whole batch are stacked
- * into one product with the shared entries, and the result is merged with each
- * request's own entries and window.  A query at t with floor((t+1)/m) <
- * n_shared sees only the entries below that bound, as without sharing; shared
- * entries it does not see must then hold finite numbers.
+ * table (a multiple of page; 0 = none), rows of empty slots too: they are read
+ * through row 0 where the batch shares them.  A query at t with floor((t+1)/m) <
+ * n_shared sees only the entries below that bound, as without sharing.
+ * The rows of all queries of the batch are taken as one product with the
+ * entries, 128 rows x 128 entries at a time, with each request's own entries and
+ * ring behind the shared ones, where that is estimated to take less time than
+ * the queries one by one; which of the two it is follows from the sizes alone.
+ * A gain, RoPE or a negative scale changes the query rows: they are held as sums
+ * of two bf16 numbers for it, which costs one product more (the one by one form
+ * rounds them to bf16, and is taken with them only where the other cannot be:
+ * FP8 caches of more than 2^30 bytes as bf16, batch times table width times D,
+ * and tables and batches whose tiles number 2^31).
  *   q [batch][nq][H][D] bf16      pool [n_pages][page][D] bf16
  *   block_table [batch][max_pages] int32 (ids outside [0, n_pages): no entry)
  *   ring [batch][ring_rows][D] bf16     q_pos [batch][nq] int32
@@ -472,10 +478,11 @@ int csa_paged_write_fp8kv(const uint16_t *rows, const long long *slots, long lon
  * n_pages >= 1, max_pages >= 1, 0 <= n_shared <= max_pages * page with n_shared
  * % page == 0, ring_rows >= W + nq - 1 (the rings hold the windows of nq
  * consecutive queries) (CSA_ERR_INVALID); n_pages * page, max_pages * page and
- * batch * ring_rows < 2^31 (CSA_ERR_UNSUPPORTED).  Workspace: csa_attend_paged_workspace_bytes,
- * 16-byte aligned, with the same arguments (fp8 = 0).  Calls that may overlap
- * on the device, replays of captured graphs among them, need workspaces of
- * their own.
+ * batch * ring_rows < 2^31, batch * nq * H < 2^31 - 256 (CSA_ERR_UNSUPPORTED).
+ * Workspace: csa_attend_paged_workspace_bytes, 16-byte aligned, with the same
+ * arguments, fp8 = 0, and rewrite = 1 if there is a gain or RoPE or scale < 0,
+ * else 0 (CSA_ERR_WORKSPACE).  Calls that may overlap on the device, replays of
+ * captured graphs among them, need workspaces of their own.
  *
  * hca_attend_paged_fp8kv -- the same over FP8 rows: pool8 [n_pages][page][D] and
  * ring8 [batch][ring_rows][D] e4m3 codes with exponents [..][..][D/128]
