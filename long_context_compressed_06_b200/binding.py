@@ -102,16 +102,18 @@ def _p(t: Optional[torch.Tensor]):
 _device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-def _stream():
-    if hasattr(torch._C, "_cuda_getCurrentRawStream"):
-        return torch._C._cuda_getCurrentRawStream(_device())
-    return torch.cuda.current_stream().cuda_stream
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    def _stream(raw=torch._C._cuda_getCurrentRawStream):
+        return raw(_device())
+else:
+    def _stream():
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _need(t: torch.Tensor, dtype, name: str, ndim: Optional[int] = None) -> torch.Tensor:
     try:
-        if (t.is_cuda and t.dtype == dtype and (ndim is None or t.dim() == ndim) and t.is_contiguous()
-                and t.get_device() == _device()):
+        if (t.is_cuda and t.dtype is dtype and t.get_device() == _device() and t.is_contiguous()
+                and (ndim is None or t.dim() == ndim)):
             return t
     except AttributeError:
         pass
@@ -274,7 +276,8 @@ def _workspace(nbytes: int, device, workspace):
     if nbytes == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    _need(workspace, workspace.dtype, "workspace")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -482,10 +485,10 @@ def csa_plan_pages(old_len, new_len, free_pages, block_table, m: int, page: int,
         if max_tokens < 0 or max_entries < 0:
             raise ValueError("max_tokens and max_entries must not be negative")
         # the int64 ones share an allocation (an allocation each took a third of the call)
-        cu_t, cu_e, slots, win, counts = torch.empty(2 * batch + 6 + max_entries + max_tokens, dtype=torch.int64,
-                                                     device=old_len.device).unsafe_split_with_sizes(
-            (batch + 1, batch + 1, max_entries, max_tokens, 4))
-        out = (cu_t, cu_e, slots, torch.empty(max_tokens, dtype=torch.int32, device=old_len.device), win, counts)
+        cu_t, cu_e, slots, win, counts = old_len.new_empty(
+            2 * batch + 6 + max_entries + max_tokens, dtype=torch.int64).unsafe_split_with_sizes(
+                (batch + 1, batch + 1, max_entries, max_tokens, 4))
+        out = (cu_t, cu_e, slots, old_len.new_empty(max_tokens), win, counts)
     else:
         for i, (x, n) in enumerate(zip(out, sizes)):
             if _need(x, torch.int32 if i == 3 else torch.int64, "out", 1).shape[0] != n:

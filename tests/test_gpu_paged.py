@@ -558,6 +558,7 @@ def test_attend_paged_refusals(cuda):
     bad(csa_pkg.CsaError, n_shared=64)          # not whole pages
     bad(csa_pkg.CsaError, n_shared=128 * 100)   # past the table
     bad(csa_pkg.CsaError, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    bad(TypeError, workspace=torch.empty(1 << 24, dtype=torch.uint8))  # host memory
     bad(ValueError, out=torch.empty_like(c.q[:1]))
     big = Case(**CASES["shared_tile"])
     big.pos = big.pos.cpu()
