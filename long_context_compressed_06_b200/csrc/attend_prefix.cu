@@ -725,8 +725,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         // An entry is free for tile g once tile g - kDescs is done with everywhere: once the
         // softmax warps are done with tile g - kDescs + 2, whose P went where the P of that tile was.
+        // With one V slot a tile (DP = 128) a V producer passes every other tile by, and the phase of an
+        // entry's barrier must not get two ahead of it (it would wait for good): one tile more, so that
+        // P.V of the tile after, which that producer brought, is over.
+        constexpr uint32_t kDone = Lt::kPieces == 1 ? 3 : 2;
         const auto entry = [&]() -> Tile * {
-            if (g + 2 >= kDescs) ok = warp_wait(smem_u32(s.dempty + (g + 2) % kDescs), ((g + 2) / kDescs + 1) & 1u, p.ctx, s.abort_flag);
+            const uint32_t t = g + kDone;
+            if (t >= kDescs) ok = warp_wait(smem_u32(s.dempty + t % kDescs), (t / kDescs + 1) & 1u, p.ctx, s.abort_flag);
             return ok ? s.desc + g % kDescs : nullptr;
         };
         const auto publish = [&] {
@@ -735,7 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++g;
         };
         const int win_rows = (int)a.win_rows;
-        while (un.left > 0 && ok) {
+        while (un.left > 0 && ok && un.rt < p.plan.row_tiles) {
             const Queries qs = queries_of(p, un.rt);
             const int b0 = p.nq.div(qs.bq0), b1 = p.nq.div(qs.bq1);
             int vmax = 0, n = 0;
@@ -770,7 +775,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     e_first = x * kPrefixKeys;
                     ent = std::min(vmax - e_first, +kPrefixKeys);
                 } else {
-                    while (y >= own.tiles()) {
+                    while (y >= own.tiles() && b <= b1) {
                         y -= own.tiles();
                         if (++b >= bw + 32) window(b);
                         own = {__shfl_sync(0xffffffffu, mine.n_own, b - bw), __shfl_sync(0xffffffffu, mine.total, b - bw)};
@@ -1022,9 +1027,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             const uint32_t lb = last & 1u, lph = (last >> 1) & 1u;
-            if (lb != (uint32_t)wg) {  // the last tile's maxima, too; the phase before the one awaited is over
+            if (lb != (uint32_t)wg) {
+                // The last tile's maxima, too.  They were written after the P.V before it of its parity was
+                // over, so that lph is the phase awaited below (waiting for that one here would be a wait for
+                // good once the last P.V is over, too).
                 float other;
-                if (!tile_max(last, other) || !wait(s.pvdone + lb, lph ^ 1u)) break;
+                if (!tile_max(last, other)) break;
                 m = raise(m, other);
             }
             if (!wait(s.pvdone + lb, lph)) break;

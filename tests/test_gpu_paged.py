@@ -3,8 +3,8 @@
 Tolerance of the attention, element by element, from its roundings (bf16: half a step is 2^-8 of the value):
   * the output is rounded once:                                        2^-8 |o|
   * the weights p_j are rounded to bf16 for the second product:       2^-8 A,  A = sum_j p_j |x_j| / sum_j p_j
-  * with a gain or RoPE the query is rounded first, to the sum of two bf16 numbers (query by query, without row tiles:
-    to one), which moves every score by at most e = 2^-16 (2^-8) scale sum_d |q_d x_d|, plus 2^-20 of it for the 32-bit
+  * with a gain or RoPE the query is rounded first, to the sum of two bf16 numbers (query by query: to
+    one), which moves every score by at most e = 2^-16 (2^-8) scale sum_d |q_d x_d|, plus 2^-20 of it for the 32-bit
     arithmetic, and the normalised weights by at most exp(2 e) - 1:  (exp(2 e) - 1) A
   * products and sums in 32 bits (512 terms, truncating tensor-core sums included): 2^-10 A
 A rotated output mixes pairs of channels: their A enters by |cos| and |sin|.
@@ -500,6 +500,20 @@ def test_attend_paged_very_many_row_tiles(cuda):
     assert got.isfinite().all()
     at = torch.tensor([0, 1, 63, 127, 128, 129], device=DEV)  # row tiles from 8192 on among them
     c.check(got[at], c.ref(at))
+
+
+@pytest.mark.parametrize("D,nq,gain", [(64, 64, False), (128, 32, True), (256, 16, False), (512, 16, True)])
+def test_attend_paged_many_short_row_tiles(cuda, D, nq, gain):
+    """Many row tiles a pair of SMs with few keys each, time and again: no hand-over from one to the next may be missed
+    (one in some 70,000 was, when a wait could look for a phase that was over)."""
+    c = Case(ts=[[390 + 11 * b + i for i in range(nq)] for b in range(130)], H=128, D=D, m=8, page=16, n_shared=48, Wn=9,
+             gain=gain)
+    assert c.by_row_tiles()
+    first = c.run(cuda)
+    for _ in range(40):
+        got = c.run(cuda)
+        assert cuda.csa_sync_status() == 0
+        assert torch.equal(got.view(torch.int16), first.view(torch.int16))
 
 
 def test_attend_paged_fp8_beyond_the_copy(cuda):
