@@ -176,8 +176,8 @@ bool prefix_pays(long long n_bq, int H, int D, long long n_shared, long long own
     return t_prefix < t_gather;
 }
 
-// rewrite: a gain, RoPE or a negative scale changes the query rows.  The row-tile kernel keeps them in 16 bits, the
-// gather kernel rounds them to 8: with them the former is taken wherever it can be.
+// rewrite: a gain, RoPE or a negative scale changes the query rows.  Either kernel keeps them in 16 bits, but the
+// gather kernel at D = 512, where there is no room and they are rounded to 8: it is not taken for them if it need not.
 PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, long long n_shared, int ring_rows, int W,
                      bool fp8, bool rewrite) {
     PagedPlan pl = {};
@@ -189,7 +189,7 @@ PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, l
     attend_tc_plan(n_bq, H, cap + W, &pl.splits, &pl.keys_per_split);
     const PrefixPlan prefix = prefix_plan(std::min(rows, 0x7fffffffLL));
     if (rows <= 0x7fffffffLL - kPrefixRows && copy <= kMaxCopyBytes && tiles <= 0x7fffffffLL / (rows / kPrefixRows + 1) &&
-        (rewrite || prefix_pays(n_bq, H, D, n_shared, cap - n_shared, nq, pl, W, fp8, prefix))) {
+        ((rewrite && D == 512) || prefix_pays(n_bq, H, D, n_shared, cap - n_shared, nq, pl, W, fp8, prefix))) {
         pl.prefix = prefix;
         if (rewrite) {
             pl.hi = take(at, (size_t)rows * D * sizeof(uint16_t));

@@ -71,6 +71,7 @@ struct AttTcParams {
     int kv_tma;         // dense key set over bf16 rows: whole tiles of entries arrive by TMA
     int HH;             // head halves per query (1 or 2)
     int stages;
+    int lo;             // rewritten query rows are s.q + s.qlo
     uint32_t idesc_qk, idesc_pv;
     long long n_work;   // n_bq * splits * HH
     DevCtx ctx;
@@ -85,8 +86,14 @@ struct Layout {
     static constexpr int kPvN = D < 256 ? D : 256;               // N of one P.V MMA
 };
 
+// Paged calls: room beside two stages for a second query tile, what rounding the
+// rewritten rows to bf16 leaves (16 more MMAs a tile; without it that rounding
+// costs as much accuracy as the output's)
+template <int D>
+constexpr bool kQLo = D <= 256;
+
 struct Smem {
-    uint8_t *q, *k, *p;
+    uint8_t *q, *k, *p, *qlo;
     uint64_t *kfull, *kempty, *sfull, *sempty, *pfull, *pempty, *oready, *qready, *qempty, *qfull, *qqready;
     uint64_t *kmask;  // [stage] validity of the 64 keys in the stage
     uint32_t *tmem_slot;
@@ -94,14 +101,15 @@ struct Smem {
 };
 
 template <int D>
-CSA_DEVINL Smem carve(uint8_t *raw, int stages) {
+CSA_DEVINL Smem carve(uint8_t *raw, int stages, int lo) {
     using Lt = Layout<D>;
     Smem s;
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     s.q = base;
     s.k = s.q + Lt::kQBytes;
     s.p = s.k + (size_t)stages * Lt::kStageBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(s.p + 2 * Lt::kPBytes);
+    s.qlo = s.p + 2 * Lt::kPBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(s.qlo + (lo ? Lt::kQBytes : 0));
     s.kfull = bars;
     s.kempty = bars + kMaxStages;
     s.sfull = bars + 2 * kMaxStages;
@@ -120,9 +128,9 @@ CSA_DEVINL Smem carve(uint8_t *raw, int stages) {
 }
 
 template <int D>
-size_t smem_bytes(int stages) {
+size_t smem_bytes(int stages, int lo) {
     using Lt = Layout<D>;
-    return 1024 + Lt::kQBytes + (size_t)stages * Lt::kStageBytes + 2 * Lt::kPBytes + (3 * kMaxStages + 14) * 8 + 16;
+    return 1024 + (lo ? 2 : 1) * Lt::kQBytes + (size_t)stages * Lt::kStageBytes + 2 * Lt::kPBytes + (3 * kMaxStages + 14) * 8 + 16;
 }
 
 // ---------------------------------------------------------------- TMEM, 16-lane access shape
@@ -299,7 +307,7 @@ struct QLanes {
 // unit slot, since kRopeDim <= D) rotate after the gain: unit r0 + j pairs
 // with r0 + j + 4, held by lane ^ 4 in the same slot, so one shuffle fetches
 // the partner values.
-template <int D>
+template <int D, bool LO>
 CSA_DEVINL void rewrite_q(const AttendArgs &a, const Smem &s, int sw, const float (&g)[QLanes<D>::UPL][8],
                           long long t) {
     using QL = QLanes<D>;
@@ -338,7 +346,17 @@ CSA_DEVINL void rewrite_q(const AttendArgs &a, const Smem &s, int sw, const floa
             }
         }
 #pragma unroll
-        for (int u = 0; u < QL::UPL; ++u) *ptr[u] = pack8(x[u]);
+        for (int u = 0; u < QL::UPL; ++u) {
+            const uint4 hi = pack8(x[u]);
+            if constexpr (LO) {
+                float r[8];
+                unpack8(hi, r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r[e] = x[u][e] - r[e];
+                *reinterpret_cast<uint4 *>(s.qlo + (reinterpret_cast<uint8_t *>(ptr[u]) - s.q)) = pack8(r);
+            }
+            *ptr[u] = hi;
+        }
     }
 }
 
@@ -375,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const AttTcParams p) {
     using Lt = Layout<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const Smem s = carve<D>(smem_raw, p.stages);
+    const Smem s = carve<D>(smem_raw, p.stages, PAGED && kQLo<D> ? p.lo : 0);
     const AttendArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -639,10 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ MMA issuers
         // Event driven: P.V for tile i as soon as P_i is written, QK for the
         // next tile as soon as its keys have landed and an S buffer is free.
-        // The whole warp runs the loop and polls (decisions are lane 0's, made
-        // warp-uniform by a shuffle); lane 0 issues through guarded
-        // instructions, never a branch.  Descriptors are built
-        // once and advanced by constant offsets.
+        // The whole warp runs the loop and polls (decisions are warp-uniform); one
+        // elected thread issues a tile's MMAs (issued by lane 0 under a guard that
+        // every lane ran, the decode attention took 17.0 us instead of 16.5).
+        // Descriptors are built once and advanced by constant offsets.
         // Two issuers (warp 0 and warp 8) run the same loop: one thread issues a
         // tcgen05.mma only every ~100 cycles (measured), so each issues half of
         // every product -- Q Q^T and QK split along the head dimension into two
@@ -656,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pv0 = kPvSplit ? iss * (D / 2) : (iss == 0 ? 0 : D), pv1 = kPvSplit ? pv0 + D / 2 : D;
         const uint32_t s_off = iss ? kIss2Cols : 0u;
         const uint64_t qdesc = tc::smem_desc(smem_u32(s.q), 1024, tc::kLayoutSw128);
+        const uint64_t lodesc = tc::smem_desc(smem_u32(s.qlo), 1024, tc::kLayoutSw128);
         const uint64_t kdesc0 = tc::smem_desc(smem_u32(s.k), 1024, tc::kLayoutSw128);
         const uint64_t vdesc0 = tc::smem_desc_lbo(smem_u32(s.k), kTileKeys * 128, 1024, tc::kLayoutSw128);
         const uint64_t pdesc0 = tc::smem_desc(smem_u32(s.p), 1024, tc::kLayoutSw128);
@@ -697,19 +716,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int st = (int)(g % p.stages), sb = (int)(g & 1);
                     const bool k_in = mbar_test_wait(smem_u32(s.kfull + st), (uint32_t)((g / p.stages) & 1));
                     const bool s_free = mbar_test_wait(smem_u32(s.sempty + sb), (uint32_t)(((g >> 1) & 1) ^ 1));
-                    if (ready(k_in && s_free)) {
-                        const bool issuer = lane == 0;
-                        tc::fence_proxy_async_smem();  // cp.async data -> tensor-core reads
-                        tc::fence_after_sync();
-                        const uint64_t kd = kdesc0 + ((uint64_t)(st * Lt::kStageBytes) >> 4);
-                        for (int t = qk0; t < qk1; ++t) {
-                            const int c = t >> 2, kk = t & 3;
-                            tc::mma_f16(tmem_s + s_off + sb * kTileKeys, qdesc + ((c * kHeads * 128 + kk * 32) >> 4),
-                                        kd + ((c * kTileKeys * 128 + kk * 32) >> 4), p.idesc_qk, t > qk0 ? 1u : 0u,
-                                        issuer);
+                    if (__all_sync(0xffffffffu, k_in && s_free)) {
+                        if (tc::elect_one()) {
+                            tc::fence_proxy_async_smem();  // cp.async data -> tensor-core reads
+                            tc::fence_after_sync();
+                            const uint64_t kd = kdesc0 + ((uint64_t)(st * Lt::kStageBytes) >> 4);
+                            for (int t = qk0; t < qk1; ++t) {
+                                const int c = t >> 2, kk = t & 3;
+                                tc::mma_f16(tmem_s + s_off + sb * kTileKeys, qdesc + ((c * kHeads * 128 + kk * 32) >> 4),
+                                            kd + ((c * kTileKeys * 128 + kk * 32) >> 4), p.idesc_qk, t > qk0 ? 1u : 0u,
+                                            true);
+                            }
+                            if constexpr (PAGED && kQLo<D>)
+                                if (p.lo)  // the rest of the query rows (rewrite_q)
+                                    for (int t = qk0; t < qk1; ++t) {
+                                        const int c = t >> 2, kk = t & 3;
+                                        tc::mma_f16(tmem_s + s_off + sb * kTileKeys,
+                                                    lodesc + ((c * kHeads * 128 + kk * 32) >> 4),
+                                                    kd + ((c * kTileKeys * 128 + kk * 32) >> 4), p.idesc_qk, 1u, true);
+                                    }
+                            tc::mma_commit(smem_u32(s.sfull + sb), true);
+                            if (nqk + 1 == it.ntiles) tc::mma_commit(smem_u32(s.qempty), true);  // query tile no longer read
                         }
-                        tc::mma_commit(smem_u32(s.sfull + sb), issuer);
-                        if (nqk + 1 == it.ntiles) tc::mma_commit(smem_u32(s.qempty), issuer);  // query tile no longer read
+                        __syncwarp();
                         ++nqk;
                         progressed = true;
                     }
@@ -717,22 +746,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (npv < nqk) {
                     const long long g = jt + npv;
                     const int pb = (int)(g & 1), st = (int)(g % p.stages);
-                    if (ready(mbar_test_wait(smem_u32(s.pfull + pb), (uint32_t)((g >> 1) & 1)))) {
-                        const bool issuer = lane == 0;
-                        tc::fence_after_sync();
-                        const uint64_t pd = pdesc0 + ((uint64_t)(pb * Lt::kPBytes) >> 4);
-                        const uint64_t vd = vdesc0 + ((uint64_t)(st * Lt::kStageBytes) >> 4);
+                    if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(s.pfull + pb), (uint32_t)((g >> 1) & 1)))) {
+                        if (tc::elect_one()) {
+                            tc::fence_after_sync();
+                            const uint64_t pd = pdesc0 + ((uint64_t)(pb * Lt::kPBytes) >> 4);
+                            const uint64_t vd = vdesc0 + ((uint64_t)(st * Lt::kStageBytes) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < kTileKeys / 16; ++kk)
-                            for (int n0 = pv0; n0 < pv1; n0 += Lt::kPvN)
-                                // V[keys][dims] read MN-major: 64-dim groups kTileKeys*128 bytes
-                                // apart (LBO), 8-key groups 1024 bytes apart (SBO); K step = 16 keys
-                                tc::mma_f16(tmem_o + n0, pd + ((kk * 32) >> 4),
-                                            vd + (((n0 / 64) * kTileKeys * 128 + kk * 16 * 128) >> 4), p.idesc_pv,
-                                            (npv == 0 && kk == 0) ? 0u : 1u, issuer);
-                        tc::mma_commit(smem_u32(s.kempty + st), issuer);
-                        tc::mma_commit(smem_u32(s.pempty + pb), issuer);
-                        tc::mma_commit(smem_u32(s.oready + pb), issuer);
+                            for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                                for (int n0 = pv0; n0 < pv1; n0 += Lt::kPvN)
+                                    // V[keys][dims] read MN-major: 64-dim groups kTileKeys*128 bytes
+                                    // apart (LBO), 8-key groups 1024 bytes apart (SBO); K step = 16 keys
+                                    tc::mma_f16(tmem_o + n0, pd + ((kk * 32) >> 4),
+                                                vd + (((n0 / 64) * kTileKeys * 128 + kk * 16 * 128) >> 4), p.idesc_pv,
+                                                (npv == 0 && kk == 0) ? 0u : 1u, true);
+                            tc::mma_commit(smem_u32(s.kempty + st), true);
+                            tc::mma_commit(smem_u32(s.pempty + pb), true);
+                            tc::mma_commit(smem_u32(s.oready + pb), true);
+                        }
+                        __syncwarp();
                         ++npv;
                         progressed = true;
                     }
@@ -794,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::fence_before_sync();
             if (q_rw) {
-                rewrite_q<D>(a, s, sp, qg, tq);
+                rewrite_q<D, PAGED && kQLo<D>>(a, s, sp, qg, tq);
                 tc::fence_proxy_async_smem();
             }
             mbar_arrive(smem_u32(s.qready));
@@ -981,13 +1012,14 @@ int launch_d(const AttendArgs &a, const DevCtx &ctx, cudaStream_t st, bool pdl) 
     p.idesc_pv = idesc_m64(Layout<D>::kPvN, true);
     p.n_work = a.n_bq * a.splits * p.HH;
     int stages = kMaxStages;
-    while (stages > 2 && smem_bytes<D>(stages) > 225 * 1024) --stages;
+    p.lo = PAGED && kQLo<D> && (a.q_gain || a.rope_cos) ? 1 : 0;
+    while (stages > 2 && smem_bytes<D>(stages, p.lo) > 225 * 1024) --stages;
     p.stages = stages;
     // at least 120 KiB so that one CTA owns an SM (it allocates all 512 TMEM columns)
-    const size_t smem = std::max<size_t>(smem_bytes<D>(stages), 120 * 1024);
+    const size_t smem = std::max<size_t>(smem_bytes<D>(stages, p.lo), 120 * 1024);
     auto kern = attend_tc_kernel<D, FP8, PAGED>;
     static SmemSet smem_set;
-    if (!smem_set((const void *)kern, smem)) return CSA_ERR_CUDA;
+    if (!smem_set((const void *)kern, 227 * 1024)) return CSA_ERR_CUDA;  // (the most of any call)
     CUtensorMap qmap;
     {
         const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.H, (uint64_t)a.n_bq};

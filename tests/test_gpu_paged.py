@@ -3,7 +3,7 @@
 Tolerance of the attention, element by element, from its roundings (bf16: half a step is 2^-8 of the value):
   * the output is rounded once:                                        2^-8 |o|
   * the weights p_j are rounded to bf16 for the second product:       2^-8 A,  A = sum_j p_j |x_j| / sum_j p_j
-  * with a gain or RoPE the query is rounded first, to the sum of two bf16 numbers (query by query: to
+  * with a gain or RoPE the query is rounded first, to the sum of two bf16 numbers (query by query at D = 512: to
     one), which moves every score by at most e = 2^-16 (2^-8) scale sum_d |q_d x_d|, plus 2^-20 of it for the 32-bit
     arithmetic, and the normalised weights by at most exp(2 e) - 1:  (exp(2 e) - 1) A
   * products and sums in 32 bits (512 terms, truncating tensor-core sums included): 2^-10 A
@@ -318,7 +318,7 @@ class Case:
 
     def check(self, got, ref=None, n_shared=None):
         out, mag, e = ref or self.ref()
-        if not self.by_row_tiles(n_shared):
+        if self.q.shape[-1] == 512 and not self.by_row_tiles(n_shared):
             e = e * 256
         tol = 2.0 ** -8 * out.abs() + (2.0 ** -8 + torch.expm1(2 * e) + 2.0 ** -10) * mag
         err = (got.double() - out).abs()
