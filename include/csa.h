@@ -466,10 +466,11 @@ int csa_paged_write_fp8kv(const uint16_t *rows, const long long *slots, long lon
  * ring behind the shared ones, where that is estimated to take less time than
  * the queries one by one; which of the two it is follows from the sizes alone.
  * A gain, RoPE or a negative scale changes the query rows: they are held as sums
- * of two bf16 numbers for it, which costs one product more (the one by one form
- * rounds them to bf16, and is taken with them only where the other cannot be:
- * FP8 caches of more than 2^30 bytes as bf16, batch times table width times D,
- * and tables and batches whose tiles number 2^31).
+ * of two bf16 numbers, which costs one product more.  At D = 512 the queries one
+ * by one leave no room for that: calls with them take the other form there, and
+ * rows are rounded to bf16 only where it cannot be taken (FP8 caches of more than
+ * 2^30 bytes as bf16: batch times table width times D; tables and batches whose
+ * tiles number 2^31).
  *   q [batch][nq][H][D] bf16      pool [n_pages][page][D] bf16
  *   block_table [batch][max_pages] int32 (ids outside [0, n_pages): no entry)
  *   ring [batch][ring_rows][D] bf16     q_pos [batch][nq] int32

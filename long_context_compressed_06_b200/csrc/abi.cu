@@ -413,7 +413,8 @@ static int validate_paged(const csa::PagedArgs &a) {
     if ((long long)a.ring_rows < (long long)a.W + a.nq - 1) return CSA_ERR_INVALID;
     if (a.n_pages > 0x7fffffffLL / a.page || cap > 0x7fffffffLL || (long long)a.batch * a.ring_rows > 0x7fffffffLL)
         return CSA_ERR_UNSUPPORTED;
-    if (a.H > 128 || (long long)a.batch * a.nq > 0x7fffff00LL / a.H || !(a.D == 64 || a.D == 128 || a.D == 256 || a.D == 512)) return CSA_ERR_UNSUPPORTED;
+    if (a.H > 128 || !(a.D == 64 || a.D == 128 || a.D == 256 || a.D == 512)) return CSA_ERR_UNSUPPORTED;
+    if ((long long)a.batch * a.nq > 0x7fffff00LL / a.H) return CSA_ERR_UNSUPPORTED;  // rows are numbered in 32 bits
     return CSA_OK;
 }
 

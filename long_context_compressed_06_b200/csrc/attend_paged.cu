@@ -226,7 +226,8 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     a.table = p.table; a.max_pages = p.max_pages; a.page = p.page; a.n_pages = p.n_pages;
     a.win_rows = p.ring_rows; a.W = p.W; a.q_pos = p.q_pos; a.nq = p.nq; a.n_bq = (long long)p.batch * p.nq;
     a.H = p.H; a.D = p.D; a.scale = p.scale; a.eps = p.eps; a.out = p.out;
-    const PagedPlan pl = paged_plan(p.batch, a.nq, a.H, a.D, a.page, a.max_pages, p.n_shared, p.ring_rows, a.W, fp8, paged_rewrite(p));
+    const PagedPlan pl =
+        paged_plan(p.batch, a.nq, a.H, a.D, a.page, a.max_pages, p.n_shared, p.ring_rows, a.W, fp8, paged_rewrite(p));
     if (pl.bytes > 0 && (!ws || ws_bytes < pl.bytes)) return CSA_ERR_WORKSPACE;
     char *w = static_cast<char *>(ws);
     a.splits = pl.splits;

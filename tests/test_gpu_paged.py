@@ -525,6 +525,46 @@ def test_attend_paged_fp8_beyond_the_copy(cuda):
     c.check(got)
 
 
+@pytest.mark.parametrize("kw", [ROW_TILES["d512_h128"], ROW_TILES["fp8_512"], CASES["shared_512"], CASES["fp8_512"]])
+def test_attend_paged_in_a_large_pool(cuda, kw):
+    """Pages whose rows lie past 2^31 elements and 2^32 bytes of the pool; the others are not initialised."""
+    c = Case(**kw)
+    ref = c.ref()
+    before = c.run(cuda)
+    first = (2 ** 32 + 2 ** 22) // (c.page * 512 * (1 if c.fp8 else 2))
+    def moved(x):
+        big = torch.empty((first + x.shape[0],) + x.shape[1:], dtype=x.dtype, device=DEV)
+        big[first:] = x
+        return big
+    c.pool = moved(c.pool)
+    if c.fp8:
+        c.pe = moved(c.pe)
+    c.table = torch.where(c.table >= 0, c.table + first, c.table)
+    for n_shared in (c.n_shared, 0):
+        got = c.run(cuda, n_shared=n_shared)
+        assert cuda.csa_sync_status() == 0
+        c.check(got, ref, n_shared)
+    assert torch.equal(c.run(cuda).view(torch.int16), before.view(torch.int16))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_paged_write_into_a_large_pool(cuda, fp8):
+    d, n = 512, 40
+    n_slots = (2 ** 32 + 2 ** 22) // (d if fp8 else 2 * d)
+    rows = W.normal_bf16((n, d), 5, DEV)
+    slots = torch.cat([torch.arange(n // 2), torch.arange(n_slots - n // 2, n_slots)]).to(DEV)
+    if fp8:
+        codes = torch.empty((n_slots, d), dtype=torch.uint8, device=DEV)
+        exps = torch.empty((n_slots, d // 128), dtype=torch.uint8, device=DEV)
+        cuda.csa_paged_write_fp8kv(rows, slots, codes, exps)
+        c, e = cuda.csa_quantize_fp8_kv(rows)
+        assert torch.equal(codes[slots], c) and torch.equal(exps[slots], e)
+    else:
+        pool = torch.empty((n_slots, d), dtype=torch.bfloat16, device=DEV)
+        cuda.csa_paged_write(rows, slots, pool)
+        assert torch.equal(pool[slots], rows)
+
+
 @pytest.mark.parametrize("name", ["d512_h128", "d128_h16", "fp8_512", "d512_h128_nq4"])
 def test_attend_paged_graph_follows_its_inputs(cuda, name):
     """Captured on a side stream, replayed with other positions, queries and pages; beside another graph of its own."""
