@@ -38,13 +38,19 @@ struct MergeArgs {
 // shared memory (its rows are contiguous the other way).  Bound by the partials' bytes: 27 MB of
 // 32 x 128 rows of 512 dims in ~5 us (lanes along the dims, 64-byte pieces of the partials: 8.4 us).
 // Rows of two or three partials want warps, those of a dozen want loads in flight.
-template <int kAtOnce>
+// kGroups = 4, for few rows of many partials: a block 32 rows x 2 x 8 dims (those that RoPE
+// pairs), four warps a quarter of the partials each; their sums meet in shared memory.
+template <int kAtOnce, int kGroups>
 __global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_merge_kernel(const MergeArgs g) {
     const AttendArgs &a = g.a;
     __shared__ float tile[32][65];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slab_bits = 31 - __clz(a.D / 64);  // D is 64 .. 512, a power of two
-    const int slab = (int)(blockIdx.x & ((1u << slab_bits) - 1u)), row0 = (int)(blockIdx.x >> slab_bits) * 32;
-    const int row = row0 + lane, d0 = slab * 64 + warp * 8;  // row = bq * H + h
+    constexpr int kSlices = 8 / kGroups;  // of 8 dims, in a block
+    const int slice = warp % kSlices, group = warp / kSlices;
+    const int sub = (int)blockIdx.x % kGroups, at = (int)blockIdx.x / kGroups;
+    const int slab = at & ((1 << slab_bits) - 1), row0 = (at >> slab_bits) * 32;
+    const int row = row0 + lane;  // bq * H + h
+    const int d0 = slab * 64 + (kGroups == 1 ? slice * 8 : sub * 8 + slice * 32);
     const bool active = row < g.n_rows;
     const int bq = active ? g.H.div(row) : 0, h = active ? row - bq * a.H : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -82,17 +88,17 @@ __global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_me
     // A few partials at a time, their (m, l) and rows all in flight together (a row without a key
     // was not written: whatever is there is not used), under a running maximum.
     float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < np; i0 += kAtOnce) {
+    for (int i0 = group; i0 < np; i0 += kAtOnce * kGroups) {
         float2 s[kAtOnce];
         float4 x[kAtOnce], y[kAtOnce];
         float top = M;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
             s[i] = make_float2(-INFINITY, 0.f);
-            if (i0 + i < np) {
-                s[i] = ml[(i0 + i) * mstride];
-                x[i] = src[(i0 + i) * stride];
-                y[i] = src[(i0 + i) * stride + step];
+            if (i0 + i * kGroups < np) {
+                s[i] = ml[(i0 + i * kGroups) * mstride];
+                x[i] = src[(i0 + i * kGroups) * stride];
+                y[i] = src[(i0 + i * kGroups) * stride + step];
             }
         }
 #pragma unroll
@@ -113,14 +119,43 @@ __global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_me
                 acc[6] = fmaf(w, y[i].z, acc[6]); acc[7] = fmaf(w, y[i].w, acc[7]);
             }
     }
+    if constexpr (kGroups > 1) {
+        // group 0 adds up the others' in their order: [group - 1][slice][M, L, 8 sums][row]
+        __shared__ float met[kGroups - 1][kSlices][10][32];
+        if (group > 0) {
+            met[group - 1][slice][0][lane] = M;
+            met[group - 1][slice][1][lane] = L;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) met[group - 1][slice][2 + e][lane] = acc[e];
+        }
+        __syncthreads();
+        if (group == 0) {
+            float top = M;
+#pragma unroll
+            for (int i = 0; i < kGroups - 1; ++i) top = fmaxf(top, met[i][slice][0][lane]);
+            const float f = M == top ? 1.f : exp2f(M - top);
+            M = top;
+            L *= f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll
+            for (int i = 0; i < kGroups - 1; ++i) {
+                const float m = met[i][slice][0][lane], w = m == -INFINITY ? 0.f : exp2f(m - M);
+                L = fmaf(w, met[i][slice][1][lane], L);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, met[i][slice][2 + e][lane], acc[e]);
+            }
+        }
+    }
     if (a.sinks && active) L += exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - M);
     const float inv = L > 0.f ? 1.0f / L : 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) tile[lane][warp * 8 + e] = acc[e] * inv;
+    for (int e = 0; e < 8; ++e)
+        if (group == 0) tile[lane][d0 % 64 + e] = acc[e] * inv;
     __syncthreads();
-    // now a thread 8 dims of row threadIdx.x / 8, eight threads 128 contiguous bytes
-    const int r = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * 8;
-    if (row0 + r >= g.n_rows) return;
+    // now a thread 8 dims of row threadIdx.x / 8, eight threads 128 contiguous bytes (with groups: two threads a row)
+    const int r = (int)threadIdx.x / kSlices, c0 = kGroups == 1 ? (int)(threadIdx.x & 7) * 8 : sub * 8 + (int)(threadIdx.x & 1) * 32;
+    if (r >= 32 || row0 + r >= g.n_rows) return;
     float o[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = tile[r][c0 + e];
@@ -283,8 +318,16 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     cfg.numAttrs = 1;
     // partials of most rows: the splits, or the ranges of a row tile and one that both its ends share
     const int partials = pl.prefix.pairs > 0 ? pl.prefix.pairs / pl.prefix.row_tiles + 1 : pl.splits;
-    const cudaError_t e = partials <= 4 ? cudaLaunchKernelEx(&cfg, attend_merge_kernel<2>, g)
-                                        : cudaLaunchKernelEx(&cfg, attend_merge_kernel<6>, g);
+    cudaError_t e;
+    // groups while their blocks leave SMs idle: 32 rows x 64 dims of 74 partials 12.5 -> 10.4 us (the whole call),
+    // 256 x 256 of 37 23.4 -> 20.5; but 512 x 512 of some ten 26.7 -> 28.7, 1536 x 128 41.6 -> 43.1
+    if (partials > 6 && 2 * cfg.gridDim.x <= (unsigned)num_sms()) {
+        cfg.gridDim.x *= 4;
+        e = cudaLaunchKernelEx(&cfg, attend_merge_kernel<4, 4>, g);
+    } else {
+        e = partials <= 4 ? cudaLaunchKernelEx(&cfg, attend_merge_kernel<2, 1>, g)
+                          : cudaLaunchKernelEx(&cfg, attend_merge_kernel<6, 1>, g);
+    }
     return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
