@@ -1,6 +1,7 @@
 """Thin Python binding of libcsa.so (include/csa.h), same names as the C ABI.
 
-Argument marshalling only: every step runs in the library's CUDA kernels.
+Argument marshalling only: every step runs in the library's CUDA kernels.  The paged calls marshal their regular case
+in C++ (_native.so, built beside the library); the Python below is what they do otherwise, checks and errors included.
 Tensors are torch CUDA tensors (PyTorch supplies device memory and the current
 stream); outputs are allocated here when not given.  If the shared library is
 missing the first call raises -- there is no fallback.
@@ -20,6 +21,19 @@ LIB_PATH = os.path.join(_PKG, "libcsa.so")
 CSA_OK, CSA_ERR_INVALID, CSA_ERR_UNSUPPORTED, CSA_ERR_CUDA, CSA_ERR_WORKSPACE, CSA_ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
 
 _lib = None
+
+
+class _Unbound:
+    """_native before load(): no call is regular yet."""
+
+    @staticmethod
+    def _none(*args):
+        return load() and None
+
+    plan_pages = paged_write = attend_paged = _none
+
+
+_native = _Unbound
 
 
 class CsaError(RuntimeError):
@@ -80,6 +94,10 @@ def load() -> ctypes.CDLL:
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = res
+    from . import _native as native  # (raises if it was not built)
+    native.bind(LIB_PATH)
+    global _native
+    _native = native
     _lib = L
     return L
 
@@ -472,6 +490,10 @@ def csa_plan_pages(old_len, new_len, free_pages, block_table, m: int, page: int,
     (cu_tokens [b+1], cu_entries [b+1], entry_slots [max_entries], tok_pos [max_tokens] int32,
     win_slots [max_tokens], counts [4]), int64 unless noted, places past the totals -1.  out: those six tensors of
     an earlier call, written again."""
+    if out is None and workspace is None:
+        out = _native.plan_pages(old_len, new_len, free_pages, block_table, m, page, ring_rows, max_tokens, max_entries)
+        if out is not None:
+            return out
     L = load()
     _need(old_len, torch.int32, "old_len", 1)
     _need(new_len, torch.int32, "new_len", 1)
@@ -511,6 +533,8 @@ def _write_rows(rows, slots, d):
 def csa_paged_write(rows, slots, pool):
     """pool [..., d] bf16 (its leading dimensions are the slots): row slots[i] becomes rows[i] ([n][d] bf16) for
     every slot (int64) inside the pool.  The slots inside are distinct."""
+    if _native.paged_write(rows, slots, pool):
+        return pool
     L = load()
     _need(pool, torch.bfloat16, "pool")
     d = pool.shape[-1]
@@ -522,6 +546,8 @@ def csa_paged_write(rows, slots, pool):
 
 def csa_paged_write_fp8kv(rows, slots, codes, exps):
     """csa_paged_write into FP8 rows: codes [..., d] u8 and exps [..., d/128] u8 (csa_quantize_fp8_kv's format)."""
+    if _native.paged_write(rows, slots, codes, exps):
+        return codes, exps
     L = load()
     _need(codes, torch.uint8, "codes")
     _need(exps, torch.uint8, "exps")
@@ -571,6 +597,10 @@ def hca_attend_paged(q, pool, block_table, m: int, ring, q_pos, W: int, scale: f
     [b][ring_rows][D] (position u at row u % ring_rows), q [b][nq][H][D], q_pos [b][nq] int32 (-1: an empty slot,
     zero rows) -> out [b][nq][H][D] bf16.  n_shared: leading entries whose pages every row of the table shares
     (a multiple of page); the batch's attention over them is computed as one product."""
+    if out is None and workspace is None:
+        got = _native.attend_paged(q, pool, None, block_table, m, ring, None, q_pos, W, scale, eps, q_gain, n_shared, sinks, rope)
+        if got is not None:
+            return got
     L = load()
     _need(pool, torch.bfloat16, "pool", 3)
     _need(ring, torch.bfloat16, "ring", 3)
@@ -588,6 +618,11 @@ def hca_attend_paged_fp8kv(q, pool8, pool8_exp, block_table, m: int, ring8, ring
                            eps: float = 1e-6, q_gain=None, out=None, workspace=None, n_shared: int = 0, sinks=None,
                            rope=None):
     """hca_attend_paged over FP8 rows: pool8 / ring8 e4m3 codes, exponents [..][..][D/128] (csa_paged_write_fp8kv)."""
+    if out is None and workspace is None:
+        got = _native.attend_paged(q, pool8, pool8_exp, block_table, m, ring8, ring8_exp, q_pos, W, scale, eps, q_gain, n_shared,
+                                   sinks, rope)
+        if got is not None:
+            return got
     L = load()
     _fp8_rows(pool8, pool8_exp, "pool8")
     _fp8_rows(ring8, ring8_exp, "ring8")

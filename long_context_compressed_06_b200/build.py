@@ -2,7 +2,8 @@
 
 Each .cu under csrc/ is compiled to an object in _build/ (parallel, skipped
 when up to date) and linked into long_context_compressed_06_b200/libcsa.so
-against the shared CUDA runtime.
+against the shared CUDA runtime.  csrc/binding_native.cpp, the C++ side of the
+binding, is compiled with g++ against torch's headers into _native.so beside it.
 """
 import concurrent.futures as cf
 import glob
@@ -15,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libcsa.so")
+NATIVE_SRC, NATIVE = os.path.join(CSRC, "binding_native.cpp"), os.path.join(PKG, "_native.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -42,8 +44,36 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def build_native(force: bool = False) -> str:
+    import sysconfig
+
+    import torch
+    # (built against these headers: another torch or interpreter means another file)
+    stamp, now = os.path.join(BUILD, "_native.stamp"), "%s %s" % (torch.__version__, sys.version)
+    if (not force and os.path.exists(NATIVE) and os.path.exists(stamp) and open(stamp).read() == now
+            and os.path.getmtime(NATIVE) >= _deps_mtime(NATIVE_SRC)):
+        return NATIVE
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), "-I", os.path.join(ROOT, "include")]
+    for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+              sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", d]
+    cmd += [NATIVE_SRC, "-o", NATIVE + ".tmp", "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (NATIVE_SRC, r.stdout, r.stderr))
+    os.replace(NATIVE + ".tmp", NATIVE)
+    with open(stamp, "w") as f:
+        f.write(now)
+    return NATIVE
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    build_native(force)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):

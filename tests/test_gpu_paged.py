@@ -604,6 +604,67 @@ def test_attend_paged_graph_follows_its_inputs(cuda, name):
     other.check(out2)
 
 
+@pytest.mark.parametrize("kw", [
+    CASES["own_only"], CASES["fp8_512"], CASES["shared_rope_128"], CASES["shared_rope_512"], ROW_TILES["d512_h128_nq4"],
+    ROW_TILES["fp8_512"], ROW_TILES["negative_scale"], dict(CASES["own_only"], scale=-1.0, sinks=True)])
+def test_native_marshalling_makes_the_same_call(cuda, kw):
+    from long_context_compressed_06_b200 import binding
+    c = Case(**kw)
+    got = c.run(cuda)
+    keep = binding._native
+    assert keep.__name__.endswith("_native")
+    args = (c.q, c.pool, c.pe if c.fp8 else None, c.table, c.m, c.ring, c.re if c.fp8 else None, c.pos, c.Wn, c.scale, 1e-6,
+            c.gain, c.n_shared, c.sinks, c.rope)
+    native = keep.attend_paged(*args)
+    assert native.dtype == torch.bfloat16 and native.shape == c.q.shape and native.is_contiguous()
+    try:
+        binding._native = binding._Unbound
+        long_way = c.run(cuda)
+    finally:
+        binding._native = keep
+    for x in (native, long_way):
+        assert torch.equal(x.view(torch.int16), got.view(torch.int16))
+    class Sub(torch.Tensor):
+        pass
+
+    # not regular: another order of the rows, another type, another rank, a subclass, an odd number
+    for i, x in ((0, c.q.transpose(1, 2)), (0, c.q.float()), (3, c.table.long()), (7, c.pos[0]), (0, c.q.as_subclass(Sub)),
+                 (4, True), (4, 2 ** 40), (7, c.pos.cpu()), (14, (1, 2)), (12, c.page + 1)):
+        assert keep.attend_paged(*args[:i], x, *args[i + 1:]) is None, i
+
+
+def test_native_plan_and_write_make_the_same_calls(cuda):
+    from long_context_compressed_06_b200 import binding
+    keep = binding._native
+    results = []
+    for native in (True, False):
+        old = torch.tensor([0, 5, 100, 63, 0], dtype=torch.int32, device=DEV)
+        new = torch.tensor([70, 1, 0, 2, 0], dtype=torch.int32, device=DEV)
+        free = torch.arange(9, 0, -1, dtype=torch.int32, device=DEV)
+        table = torch.full((5, 6), -1, dtype=torch.int32, device=DEV)
+        table[1, 0], table[2, :2], table[3, 0] = 20, torch.tensor([21, 22]), 23
+        pool = torch.zeros((30 * 16, 128), dtype=torch.bfloat16, device=DEV)
+        rows = W.normal_bf16((25, 128), 3, DEV)
+        codes, exps = torch.zeros((480, 128), dtype=torch.uint8, device=DEV), torch.zeros((480, 1), dtype=torch.uint8, device=DEV)
+        try:
+            if not native:
+                binding._native = binding._Unbound
+            plan = cuda.csa_plan_pages(old, new, free, table, 4, 16, 32, 81, 25)
+            assert cuda.csa_paged_write(rows, plan[2], pool) is pool
+            assert cuda.csa_paged_write_fp8kv(rows, plan[2], codes, exps) == (codes, exps)
+        finally:
+            binding._native = keep
+        assert [x.dtype for x in plan] == [torch.int64] * 3 + [torch.int32] + [torch.int64] * 2
+        results.append([x.clone() for x in plan] + [table, pool, codes, exps])
+        plan[3].fill_(7)                        # outputs of one allocation, each its own
+        assert all(torch.equal(a, b) for k, (a, b) in enumerate(zip(plan, results[-1])) if k != 3)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    # nothing appended, no room
+    z = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = cuda.csa_plan_pages(z, z, z[:0], torch.full((1, 1), -1, dtype=torch.int32, device=DEV), 4, 16, 16, 0, 0)
+    assert [x.numel() for x in out] == [2, 2, 0, 0, 0, 4] and out[5].tolist() == [0, 0, 0, 0]
+
+
 def test_attend_paged_refusals(cuda):
     c = Case(**CASES["shared_tile"])
     def bad(exc, **kw):

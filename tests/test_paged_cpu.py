@@ -127,3 +127,24 @@ def test_binding_refuses_host_tensors():
         csa.csa_paged_write("rows", torch.zeros(16, dtype=torch.int64), None)
     with pytest.raises(TypeError):
         csa.hca_attend_paged(x, x, x, 4, x, x, 16, 0.1)
+
+
+def test_native_marshalling_takes_regular_calls_only(lib):
+    """What it does not take it leaves to the long way, which raises."""
+    from long_context_compressed_06_b200 import binding
+    n = binding._native
+    x = torch.zeros(4, 16, 64, dtype=torch.bfloat16)
+    i = torch.zeros(4, dtype=torch.int32)
+    assert n.paged_write(x[0], torch.zeros(16, dtype=torch.int64), x) is None          # host memory
+    assert n.paged_write() is None and n.paged_write(1, 2, 3) is None and n.paged_write(None, None, None, None) is None
+    assert n.plan_pages(i, i, i, torch.zeros(4, 8, dtype=torch.int32), 4, 16, 16, 9, 9) is None
+    assert n.plan_pages(i, i, i) is None and n.plan_pages(*[None] * 9) is None
+    assert n.attend_paged(*[None] * 15) is None and n.attend_paged() is None
+    assert n.attend_paged(x[None], x, None, i[:, None], 4, x, None, i[:, None], 16, 1.0, 1e-6, None, 0, None, None) is None
+    with pytest.raises(RuntimeError):
+        n.bind("/nowhere/libcsa.so")
+    assert n.paged_write(x[0], torch.zeros(16, dtype=torch.int64), x) is None
+    with pytest.raises(TypeError):
+        csa.csa_plan_pages(i, i, i, torch.zeros(4, 8, dtype=torch.int32), 4, 16, 16, 9, 9)
+    with pytest.raises(TypeError):
+        csa.hca_attend_paged(x[None], x, i[:, None], 4, x, i[:, None], 16, 1.0)
