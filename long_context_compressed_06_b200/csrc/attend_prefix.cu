@@ -212,9 +212,9 @@ CSA_DEVINL Queries queries_of(const Params &p, int rt) {
     return r;
 }
 
-// Units of row tile rt, by `subs` consecutive lanes that share its requests (the
-// sum is every lane's); rt past the last: 0.
-CSA_DEVINL int count_units(const Params &p, int rt, int subs) {
+// Units of row tile rt (x) and how many shared entries its rows see (y), by `subs`
+// consecutive lanes that share its requests (every lane has both); rt past the last: 0.
+CSA_DEVINL int2 count_units(const Params &p, int rt, int subs) {
     int vmax = 0, n = 0;
     if (rt < p.plan.row_tiles) {
         const Queries r = queries_of(p, rt);
@@ -229,16 +229,17 @@ CSA_DEVINL int count_units(const Params &p, int rt, int subs) {
         n += __shfl_xor_sync(0xffffffffu, n, d);
         vmax = std::max(vmax, __shfl_xor_sync(0xffffffffu, vmax, d));
     }
-    return n + (vmax + kPrefixKeys - 1) / kPrefixKeys;
+    return make_int2(n + (vmax + kPrefixKeys - 1) / kPrefixKeys, vmax);
 }
 
-// A pair's units: `left` of them from number x of row tile rt on.
+// A pair's units: `left` of them from number x of row tile rt on, whose counts are n.
 struct Units {
     int left, rt, x;
+    int2 n;
 };
 
 // Units of the row tiles, by the whole block, to `counts` (at most kCounts of them).
-constexpr int kCounts = (int)(2 * kPBytes / sizeof(int));
+constexpr int kCounts = (int)(2 * kPBytes / sizeof(int2));
 
 CSA_DEVINL int count_lanes(const Params &p) {  // lanes per row tile: about its requests
     int subs = 1;
@@ -246,31 +247,33 @@ CSA_DEVINL int count_lanes(const Params &p) {  // lanes per row tile: about its 
     return subs;
 }
 
-CSA_DEVINL void count_all(const Params &p, int *counts) {
+CSA_DEVINL void count_all(const Params &p, int2 *counts) {
     const int subs = count_lanes(p), RT = std::min(p.plan.row_tiles, +kCounts), step = kThreads / subs;
     for (int r0 = 0; r0 < RT; r0 += step) {
-        const int rt = r0 + (int)threadIdx.x / subs, n = count_units(p, rt, subs);
+        const int rt = r0 + (int)threadIdx.x / subs;
+        const int2 n = count_units(p, rt, subs);
         if (rt < RT && (threadIdx.x & (subs - 1)) == 0) counts[rt] = n;
     }
 }
 
 // By one warp; `write`: also the ranges of every row tile.
-CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool write) {
+CSA_DEVINL Units deal_units(const Params &p, const int2 *counts, int pair, bool write) {
     const int lane = threadIdx.x & 31, RT = p.plan.row_tiles, subs = count_lanes(p);
-    int total = 0, units = 0, n = 0, inc = 0;
-    const auto pass = [&](int r0) {  // n: cost of row tile r0 + lane; inc: of those up to it in this pass
-        n = 0;
+    int total = 0, units = 0, cost = 0, inc = 0;
+    int2 n = {0, 0};
+    const auto pass = [&](int r0) {  // n: counts of row tile r0 + lane; its cost; inc: costs up to it in this pass
+        n = make_int2(0, 0);
         if (r0 + 32 <= kCounts) {
             if (r0 + lane < RT) n = counts[r0 + lane];
         } else {
             for (int l0 = 0; l0 < 32; l0 += 32 / subs) {
-                const int c = count_units(p, r0 + l0 + lane / subs, subs);
-                const int of = __shfl_sync(0xffffffffu, c, (lane - l0) * subs & 31);
-                if (lane >= l0 && lane < l0 + 32 / subs) n = of;
+                const int2 c = count_units(p, r0 + l0 + lane / subs, subs);
+                const int from = (lane - l0) * subs & 31, x = __shfl_sync(0xffffffffu, c.x, from), y = __shfl_sync(0xffffffffu, c.y, from);
+                if (lane >= l0 && lane < l0 + 32 / subs) n = make_int2(x, y);
             }
         }
-        if (n > 0) n += PrefixPlan::kPartCost;
-        inc = n;
+        cost = n.x > 0 ? n.x + PrefixPlan::kPartCost : 0;
+        inc = cost;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, inc, d);
@@ -279,8 +282,9 @@ CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool w
     };
     for (int r0 = 0; r0 < RT; r0 += 32) {
         pass(r0);
-        total += __shfl_sync(0xffffffffu, inc, 31);
-        units += __shfl_sync(0xffffffffu, inc, 31) - PrefixPlan::kPartCost * __popc(__ballot_sync(0xffffffffu, n > 0));
+        const int sum = __shfl_sync(0xffffffffu, inc, 31);
+        total += sum;
+        units += sum - PrefixPlan::kPartCost * __popc(__ballot_sync(0xffffffffu, cost > 0));
     }
     const int ranges = p.plan.ranges(units);
     // for the merge: which ranges meet each row tile
@@ -288,43 +292,33 @@ CSA_DEVINL Units deal_units(const Params &p, const int *counts, int pair, bool w
         int base = 0;
         for (int r0 = 0; r0 < RT; r0 += 32) {
             if (RT > 32) pass(r0);
-            const int at = base + inc - n;
+            const int at = base + inc - cost;
             if (r0 + lane < RT) {
-                const int q0 = n > 0 ? range_of(at + PrefixPlan::kPartCost, ranges, total) : 0;
-                p.meet[r0 + lane] = make_int2(q0, n > 0 ? range_of(at + n - 1, ranges, total) - q0 + 1 : 0);
+                const int q0 = cost > 0 ? range_of(at + PrefixPlan::kPartCost, ranges, total) : 0;
+                p.meet[r0 + lane] = make_int2(q0, cost > 0 ? range_of(at + cost - 1, ranges, total) - q0 + 1 : 0);
             }
             base += __shfl_sync(0xffffffffu, inc, 31);
         }
     }
-    // the row tile and the unit within it of a place among all costs
-    const auto find = [&](int u, int &rt, int &x, int &units) {  // units: those before it
-        int base = 0, before = 0;
-        rt = RT;
-        x = units = 0;
-        for (int r0 = 0; r0 < RT; r0 += 32) {
-            if (RT > 32) pass(r0);
-            const uint32_t here = __ballot_sync(0xffffffffu, base + inc - n <= u && u < base + inc);
-            const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
-            const int end = __shfl_sync(0xffffffffu, inc, 31);
-            if (here) {
-                const int l = __ffs(here) - 1, off = u - base - __shfl_sync(0xffffffffu, inc - n, l);
-                rt = r0 + l;
-                x = std::max(off - PrefixPlan::kPartCost, 0);
-                units = before + __shfl_sync(0xffffffffu, inc - n, l) -
-                        PrefixPlan::kPartCost * __popc(some & ((1u << l) - 1u)) + x;
-                return;
-            }
-            before += end - PrefixPlan::kPartCost * __popc(some);
-            base += end;
-        }
-        units = before;
-    };
-    Units u = {0, 0, 0};
+    Units u = {0, 0, 0, {0, 0}};
     if (total == 0 || pair >= ranges) return u;
-    int n0, n1, rt1, x1;
-    find(range_begin(pair, ranges, total), u.rt, u.x, n0);
-    find(range_begin(pair + 1, ranges, total), rt1, x1, n1);
-    u.left = n1 - n0;
+    // the units between two places among all costs
+    const int u0 = range_begin(pair, ranges, total), u1 = range_begin(pair + 1, ranges, total);
+    for (int r0 = 0, base = 0; r0 < RT && base < u1; r0 += 32) {
+        if (RT > 32) pass(r0);
+        const int start = base + inc - cost;
+        const int c0 = std::min(std::max(u0 - start - PrefixPlan::kPartCost, 0), n.x);  // its units before u0, u1
+        const int c1 = std::min(std::max(u1 - start - PrefixPlan::kPartCost, 0), n.x);
+        u.left += __reduce_add_sync(0xffffffffu, c1 - c0);
+        const uint32_t here = __ballot_sync(0xffffffffu, start <= u0 && u0 < start + cost);
+        if (here) {
+            const int l = __ffs(here) - 1;
+            u.rt = r0 + l;
+            u.x = __shfl_sync(0xffffffffu, c0, l);
+            u.n = make_int2(__shfl_sync(0xffffffffu, n.x, l), __shfl_sync(0xffffffffu, n.y, l));
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+    }
     return u;
 }
 
@@ -483,11 +477,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::prefetch_tmap(&maps.v);
     }
     if (threadIdx.x < 256) s.xch[threadIdx.x] = 0xffffffffu;  // no tile's
-    count_all(p, reinterpret_cast<int *>(s.p));  // (P is written long after the planner has read them)
+    count_all(p, reinterpret_cast<int2 *>(s.p));  // (P is written long after the planner has read them)
     if (warp == kQueryWarp) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
     tc::fence_before_sync();
     __syncthreads();
-    tc::cluster_sync();  // both CTAs' barriers exist
+    tc::cluster_arrive();  // both CTAs' barriers exist past the wait (the planner's are its own CTA's)
+    if (warp != kPlanWarp) tc::cluster_wait();
     tc::fence_after_sync();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = *s.tmem_slot;
@@ -720,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         copies = !ok;
     } else if (warp == kPlanWarp) {
         // ------------------------------------------------------------ planner
-        Units un = deal_units(p, reinterpret_cast<const int *>(s.p), pair, blockIdx.x == 0);
+        Units un = deal_units(p, reinterpret_cast<const int2 *>(s.p), pair, blockIdx.x == 0);
         uint32_t g = 0;
         bool ok = true;
         // An entry is free for tile g once tile g - kDescs is done with everywhere: once the
@@ -740,28 +735,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++g;
         };
         const int win_rows = (int)a.win_rows;
+        bool counted = true;  // un.n are the row tile's
         while (un.left > 0 && ok && un.rt < p.plan.row_tiles) {
             const Queries qs = queries_of(p, un.rt);
             const int b0 = p.nq.div(qs.bq0), b1 = p.nq.div(qs.bq1);
-            int vmax = 0, n = 0;
-            for (int q = qs.bq0 + lane; q <= qs.bq1; q += 32) vmax = std::max(vmax, visible(p, __ldg(a.q_pos + q), p.n_shared));
             const auto query0 = [&](int b) { return std::max(qs.bq0, b * a.nq); };
             const auto query1 = [&](int b) { return std::min(qs.bq1, b * a.nq + a.nq - 1); };
             // own keys of request bw + lane, 32 requests at a time
             Own mine = {0, 0u};
-            int bw = b0;
+            int bw = b0 - 32;
             const auto window = [&](int b) {
                 bw = b;
                 mine = b + lane <= b1 ? own_keys(p, query0(b + lane), query1(b + lane)) : Own{0, 0u};
             };
-            for (int b = b0; b <= b1; b += 32) {
-                window(b);
-                n += mine.tiles();
+            if (!counted) {
+                int vmax = 0, tiles = 0;
+                for (int q = qs.bq0 + lane; q <= qs.bq1; q += 32) vmax = std::max(vmax, visible(p, __ldg(a.q_pos + q), p.n_shared));
+                for (int b = b0; b <= b1; b += 32) {
+                    window(b);
+                    tiles += mine.tiles();
+                }
+                if (bw != b0) window(b0);
+                un.n.y = __reduce_max_sync(0xffffffffu, vmax);
+                un.n.x = (int)__reduce_add_sync(0xffffffffu, tiles) + (un.n.y + kPrefixKeys - 1) / kPrefixKeys;
             }
-            if (bw != b0) window(b0);
-            vmax = __reduce_max_sync(0xffffffffu, vmax);
-            const int shared = (vmax + kPrefixKeys - 1) / kPrefixKeys;
-            n = std::min((int)__reduce_add_sync(0xffffffffu, n) + shared - un.x, un.left);
+            counted = false;
+            const int vmax = un.n.y, shared = (vmax + kPrefixKeys - 1) / kPrefixKeys;
+            const int n = std::min(un.n.x - un.x, un.left);
             un.left -= std::max(n, 0);
             int x = un.x, b = b0 - 1;
             int y = x - shared;  // the tile's number among its request's own ones
@@ -853,6 +853,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 publish();
             }
         }
+        tc::cluster_wait();
     } else {
         // ------------------------------------------------------------ softmax, partial rows
         // Group wg takes the tiles of its parity; both meet where a row tile begins and ends.

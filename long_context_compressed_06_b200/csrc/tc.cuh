@@ -181,6 +181,10 @@ CSA_DEVINL uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
 CSA_DEVINL void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Its two halves, without ordering memory at cluster scope (a release there took ~900 cycles at the start
+// of attend_prefix.cu): for barriers made visible by fence_mbar_init.
+CSA_DEVINL void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+CSA_DEVINL void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 CSA_DEVINL bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
