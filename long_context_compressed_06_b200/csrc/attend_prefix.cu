@@ -472,17 +472,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         *s.abort_flag = 0;
         fence_mbar_init();
+    }
+    if (warp == kQueryWarp) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
+    __syncwarp();
+    // Both CTAs' barriers and tensor memory exist past the wait.  (An arrival waits for what its warp has
+    // on the way to memory: it comes before the counts.)
+    tc::cluster_arrive();
+    if (threadIdx.x == 0) {
         tc::prefetch_tmap(&maps.q);
         tc::prefetch_tmap(&maps.k);
         tc::prefetch_tmap(&maps.v);
     }
     if (threadIdx.x < 256) s.xch[threadIdx.x] = 0xffffffffu;  // no tile's
     count_all(p, reinterpret_cast<int2 *>(s.p));  // (P is written long after the planner has read them)
-    if (warp == kQueryWarp) tc::tmem_alloc_2sm(smem_u32(s.tmem_slot), 512);
     tc::fence_before_sync();
     __syncthreads();
-    tc::cluster_arrive();  // both CTAs' barriers exist past the wait (the planner's are its own CTA's)
-    if (warp != kPlanWarp) tc::cluster_wait();
+    if (warp != kPlanWarp) tc::cluster_wait();  // (the planner's barriers are its own CTA's)
     tc::fence_after_sync();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = *s.tmem_slot;
