@@ -1015,12 +1015,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float e[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) e[i] = exp2_ftz(fmaf(sc[x * 8 + i], rq, -mref));
+                    // l sums the weights as they are rounded: what the rounding changes in common cancels
+                    // in O / l (of a row with one key, all of it)
+                    const uint4 w = pack8(e);
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        ps[0] += e[i];
-                        ps[1] += e[i + 1];
+                    for (int i = 0; i < 4; ++i) {
+                        ps[0] += __uint_as_float(ww[i] << 16);
+                        ps[1] += __uint_as_float(ww[i] & 0xffff0000u);
                     }
-                    *reinterpret_cast<uint4 *>(prow + ((x ^ (r & 7)) << 4)) = pack8(e);
+                    *reinterpret_cast<uint4 *>(prow + ((x ^ (r & 7)) << 4)) = w;
                 }
                 l += ps[0] + ps[1];
                 tc::fence_proxy_async_smem();

@@ -893,8 +893,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                     const float p0 = exp2f(sc[i] - mref), p1 = exp2f(sc[i + 1] - mref);
-                    ps += p0 + p1;
                     pk[i / 2] = pack_bf16x2(p0, p1);
+                    // (paged: of the weights as they are rounded, see attend_prefix.cu)
+                    ps += PAGED ? __uint_as_float(pk[i / 2] << 16) + __uint_as_float(pk[i / 2] & 0xffff0000u) : p0 + p1;
                 }
                 l += ps + __shfl_xor_sync(0xffffffffu, ps, 16);
                 const int pb = (int)(g & 1);

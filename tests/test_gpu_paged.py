@@ -491,6 +491,20 @@ def test_attend_paged_empty_slots_hold_anything(cuda, kw):
     c.check(got)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(ts=[[0], [0], [-1], [0]], H=8, D=64, m=4, page=16, n_shared=0, Wn=4),
+    dict(ts=[[0]] * 40, H=128, D=128, m=4, page=16, n_shared=0, Wn=16),
+    dict(ts=[[0]] * 3, H=128, D=512, m=4, page=16, n_shared=0, Wn=16, gain=True),
+    dict(ts=[[0]] * 3, H=128, D=512, m=4, page=16, n_shared=0, Wn=16, fp8=True)])
+def test_attend_paged_one_key_is_its_value(cuda, kw):
+    """A row with one key: the weight's rounding cancels, so the output is the key's value to the bit."""
+    c = Case(**kw)
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    want = torch.where((c.pos >= 0)[..., None, None], c.ring64[:, :1, None].to(torch.bfloat16), 0.0).expand_as(got)
+    assert torch.equal(got.float(), want.float())
+
+
 def test_attend_paged_very_many_row_tiles(cuda):
     """More row tiles than the kernel counts at once."""
     c = Case(ts=[[390 + 11 * b + i for i in range(64)] for b in range(130)], H=128, D=64, m=8, page=16, n_shared=48, Wn=9)
