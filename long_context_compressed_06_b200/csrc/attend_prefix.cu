@@ -22,15 +22,18 @@
 // The price is that each SM loads 64 of a tile's 128 keys whole (its half of
 // K's rows) and all 128 keys by half their dims (its half of V's columns):
 // 128 KiB per SM and tile at D = 512, 1.33 times what one copy would be.
-// The tensor cores' operand reads (224 KiB), these loads and P share the
-// 128 B/cycle of shared memory, which bounds the kernel at D = 512.
+// At D = 512 these loads (~40 B a cycle and SM from L2, where a tile takes ~3200
+// cycles) bound the kernel, close before the tensor cores (QK 1056 + P.V 1056 cycles
+// and what they wait for); 32 row tiles of 8064 + 192 keys take 62 us with the merge.
+// At D = 128 the softmax does: ~1850 cycles a tile, a third of it exponentials.
 //
 // A gain, RoPE or a negative scale changes the query rows first, and rounding
 // them to bf16 again would cost as much accuracy as the output's own rounding
 // does (2.5e-3 instead of 2.0e-3 in all, against 64 bits).  A launch before
 // writes them as a sum of two bf16 numbers (hi + lo, 16 bits), and S gets both
 // products; lo passes through K's ring beside each piece of K, since at D = 512
-// shared memory has no room for it.
+// shared memory has no room for it (64 queries x 128 heads over 4096 entries 74 ->
+// 105 us: half more products and half more loads).
 //
 // Warps: 0 and 1 producers of K, 2 and 3 of V, 4 and 5 MMA issuers of Q K^T and of
 // P V on the pair's leader (one thread for both was busy for longer than the
