@@ -94,7 +94,10 @@ def load() -> ctypes.CDLL:
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = res
-    from . import _native as native  # (raises if it was not built)
+    try:
+        from . import _native as native
+    except ImportError as e:
+        raise RuntimeError("_native.so is not built for this torch; run `python -m long_context_compressed_06_b200.build`") from e
     native.bind(LIB_PATH)
     global _native
     _native = native
