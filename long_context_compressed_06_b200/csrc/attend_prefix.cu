@@ -1086,6 +1086,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
+// 8 floats of a table that may be aligned to 4 bytes only (`wide`: to 16)
+CSA_DEVINL void load8(const float *p, bool wide, float x[8]) {
+    if (wide) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __ldg(p + e);
+    }
+}
+
 // Query rows under a gain, the scale's sign and RoPE (channel D-64+j of the slice
 // rotates with D-32+j), as hi + lo in bf16, and their factors.  A warp per row.
 __global__ void __launch_bounds__(256)
@@ -1096,6 +1108,10 @@ __global__ void __launch_bounds__(256)
     if (row >= n_rows) return;
     const float sign = a.scale < 0.f ? -1.f : 1.f;
     const long long t = __ldg(a.q_pos + H.div(row));
+    // (4-byte loads of the gain, 16 a lane and row, took more of L1 than the rows themselves)
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.q_gain) | reinterpret_cast<uintptr_t>(a.rope_cos) |
+                        reinterpret_cast<uintptr_t>(a.rope_sin)) & 15u) == 0;
+    const bool turns = a.rope_cos && t >= 0 && t < a.rope_npos;
     const uint4 *src = reinterpret_cast<const uint4 *>(a.q) + (size_t)row * units;
     float ss = 0.f;
 #pragma unroll
@@ -1104,22 +1120,25 @@ __global__ void __launch_bounds__(256)
         if (i * 32 >= units) break;
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (u < units) unpack8(ldg16(src + u), x);
+        float gain[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+        if (a.q_gain && u < units) load8(a.q_gain + u * 8, wide, gain);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             ss = fmaf(x[e], x[e], ss);
-            x[e] *= a.q_gain && u < units ? sign * __ldg(a.q_gain + u * 8 + e) : sign;
+            x[e] *= sign * gain[e];
         }
-        if (a.rope_cos) {
+        if (turns) {  // (of the whole warp's row)
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = __shfl_xor_sync(0xffffffffu, x[e], 4);
             if (u >= units - 8 && u < units) {
                 const bool first = u < units - 4;
+                const size_t at = (size_t)t * (kRopeDim / 2) + ((u - (units - 8)) & 3) * 8;
+                float c[8], s[8];
+                load8(a.rope_cos + at, wide, c);
+                load8(a.rope_sin + at, wide, s);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 cs = rope_cs(a, t, ((u - (units - 8)) & 3) * 8 + e);
-                    x[e] = first ? x[e] * cs.x - y[e] * cs.y : x[e] * cs.x + y[e] * cs.y;
-                }
+                for (int e = 0; e < 8; ++e) x[e] = first ? x[e] * c[e] - y[e] * s[e] : x[e] * c[e] + y[e] * s[e];
             }
         }
         if (u < units) {

@@ -491,6 +491,23 @@ def test_attend_paged_empty_slots_hold_anything(cuda, kw):
     c.check(got)
 
 
+@pytest.mark.parametrize("name", ["d512_h128_nq4", "d256_h100", "part_rope"])
+def test_attend_paged_tables_aligned_to_their_elements(cuda, name):
+    """Gain and RoPE tables that start at an odd float; positions past the tables, and empty slots."""
+    kw = ROW_TILES[name] if name in ROW_TILES else dict(ROW_TILES["part_seen_512"], rope=100, gain=True)
+    c = Case(**kw)
+    before = c.run(cuda)
+    def odd(x):
+        y = torch.empty(x.numel() + 1, dtype=x.dtype, device=DEV)[1:].view(x.shape)
+        return y.copy_(x)
+    c.gain, c.rope = odd(c.gain), tuple(odd(x) for x in c.rope)
+    assert c.gain.data_ptr() % 16 == 4
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    assert torch.equal(got.view(torch.int16), before.view(torch.int16))
+    c.check(got)
+
+
 @pytest.mark.parametrize("kw", [
     dict(ts=[[0], [0], [-1], [0]], H=8, D=64, m=4, page=16, n_shared=0, Wn=4),
     dict(ts=[[0]] * 40, H=128, D=128, m=4, page=16, n_shared=0, Wn=16),
