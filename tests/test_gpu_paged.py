@@ -690,6 +690,13 @@ def test_native_plan_and_write_make_the_same_calls(cuda):
         plan[3].fill_(7)                        # outputs of one allocation, each its own
         assert all(torch.equal(a, b) for k, (a, b) in enumerate(zip(plan, results[-1])) if k != 3)
     assert all(torch.equal(a, b) for a, b in zip(*results))
+    # the outputs are tensors like any other, in inference mode too
+    for mode in (torch.inference_mode(), torch.no_grad()):
+        with mode:
+            plan = cuda.csa_plan_pages(old, new, free, table, 4, 16, 32, 81, 25)
+            plan[2].add_(1)
+            assert torch.equal(plan[2].view(5, 5).t().contiguous().t().reshape(-1) - 1, results[0][2])
+            assert plan[3].cpu().tolist() == results[0][3].tolist() and plan[0].clone().is_contiguous()
     # nothing appended, no room
     z = torch.zeros(1, dtype=torch.int32, device=DEV)
     out = cuda.csa_plan_pages(z, z, z[:0], torch.full((1, 1), -1, dtype=torch.int32, device=DEV), 4, 16, 16, 0, 0)
