@@ -130,8 +130,7 @@ struct Smem {
     uint8_t *q, *slots, *p;  // slots: K's ring, then V's; so are their barriers
     uint64_t *full, *empty, *sfull, *sempty, *pfull, *pvdone, *qland, *qready, *qempty, *vfix, *dfull, *dempty, *rbar;
     Tile *desc;  // [kDescs]
-    // [2 x 32 rows][tile parity][2 halves of the keys][32] (upper half of the row's maximum, number of
-    // the tile) in one word
+    // [2 x 32 rows][tile parity][2 halves of the keys][32] the row's maximum and the tile's tag in one word (tagged)
     uint32_t *xch;
     uint32_t *tmem_slot;
     int *abort_flag;
@@ -394,6 +393,21 @@ CSA_DEVINL float row_factor(const AttendArgs &a, float ss) {
     return fmaxf((1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
 }
 
+// A row's maximum is exchanged without its last kTagBits bits (rounded towards zero by up to 3 steps of 32
+// bits), where the tile's tag goes: a word's reader finds what it waits for or the word's use before.
+constexpr uint32_t kTagBits = 2, kTagMask = (1u << kTagBits) - 1u;
+CSA_DEVINL uint32_t tag_of(uint32_t g) { return (g >> 1) & kTagMask; }  // (a word serves every other tile)
+CSA_DEVINL float untagged(uint32_t x) { return __uint_as_float(x & ~kTagMask); }
+CSA_DEVINL uint32_t tagged(float v, uint32_t g) { return (__float_as_uint(v) & ~kTagMask) | tag_of(g); }
+// Those 3 steps are 48 log2 units below 2^28, and the weights' range has room for them.  From 2^28 on (where a
+// score's own rounding is 16 units and more) they would overflow, or be 0 under a negative maximum: there the
+// differences between scores and maximum are scaled so that a step is 16 units, and a key one step away weighs
+// 2^-16.  The factor of a maximum m: a power of two, 1 below 2^28.
+CSA_DEVINL float difference_scale(float m) {
+    const int over = (int)((__float_as_uint(m) >> 23) & 255u) - (127 + 27);
+    return __uint_as_float((uint32_t)(127 - std::max(over, 0)) << 23);
+}
+
 // the first n of 32 bits
 CSA_DEVINL uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
 
@@ -486,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::prefetch_tmap(&maps.k);
         tc::prefetch_tmap(&maps.v);
     }
-    if (threadIdx.x < 256) s.xch[threadIdx.x] = 0xffffffffu;  // no tile's
+    if (threadIdx.x < 256) s.xch[threadIdx.x] = kTagMask;  // not tile 0's or 1's
     count_all(p, reinterpret_cast<int2 *>(s.p));  // (P is written long after the planner has read them)
     tc::fence_before_sync();
     __syncthreads();
@@ -885,12 +899,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // The row's maximum in tile g, once both halves of it are there.  A poll of the words
         // themselves: an mbarrier between the two warps took ~400 cycles.
         const auto tile_max = [&](uint32_t g, float &mt) {
-            const uint32_t at = (g & 1u) * 64 + lane, tag = g & 0xffffu;
+            const uint32_t at = (g & 1u) * 64 + lane, tag = tag_of(g);
             uint64_t t0 = 0;
             for (int i = 0;; ++i) {
                 const uint32_t x = xch[at], y = xch[at + 32];
-                if (__all_sync(0xffffffffu, (x & 0xffffu) == tag && (y & 0xffffu) == tag)) {
-                    mt = fmaxf(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u));
+                if (__all_sync(0xffffffffu, (x & kTagMask) == tag && (y & kTagMask) == tag)) {
+                    mt = fmaxf(untagged(x), untagged(y));
                     return true;
                 }
                 if ((i & 63) == 63) {
@@ -973,10 +987,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     m2[1] = fmaxf(m2[1], sc[i + 1]);
                 }
                 float mt = fmaxf(m2[0], m2[1]) * rq;
-                // The row's maximum over its two threads, each rounded to 16 bits towards zero (any
-                // reference near the maximum serves, as long as all four agree).  A word is written
-                // again two tiles on: by then this tile's P.V is over, for which the partner has read
-                // it, and the other group has written the tile's between, before which it has.
+                // The row's maximum over its two threads (any reference near the maximum serves, as long
+                // as all four agree).  A word is written again two tiles on: by then this tile's P.V is
+                // over, for which the partner has read it, and the other group has written the tile's
+                // between, before which it has.
                 if (!wait(s.pvdone + b, ph ^ 1u)) break;  // (P buffer b is free, too)
                 float other;
                 if (g > g0) {
@@ -985,7 +999,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 } else if (g > 0 && !tile_max(g - 1, other)) {
                     break;
                 }
-                xch[b * 64 + hf * 32 + lane] = (__float_as_uint(mt) & 0xffff0000u) | (g & 0xffffu);
+                xch[b * 64 + hf * 32 + lane] = tagged(mt, g);
                 if (!tile_max(g, mt)) break;
                 const float m_old = m;
                 const bool mine = m != -INFINITY && mt > m + kRescaleThreshold;
@@ -1010,14 +1024,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (m_l != -INFINITY) l *= exp2f(m_l - m);
                     m_l = m;
                 }
-                const float mref = m == -INFINITY ? 0.f : m;
+                float mref = m == -INFINITY ? 0.f : m;
+                const float sized = difference_scale(mref), factor = rq * sized;
+                mref *= sized;
                 uint8_t *prow = s.p + b * kPBytes + hf * 8192 + r * 128;
                 float ps[2] = {0.f, 0.f};
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {  // 8 keys: 16 bytes
                     float e[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) e[i] = exp2_ftz(fmaf(sc[x * 8 + i], rq, -mref));
+                    for (int i = 0; i < 8; ++i) e[i] = exp2_ftz(fmaf(sc[x * 8 + i], factor, -mref));
                     // l sums the weights as they are rounded: what the rounding changes in common cancels
                     // in O / l (of a row with one key, all of it)
                     const uint4 w = pack8(e);

@@ -1,0 +1,86 @@
+"""hca_attend_paged at the ends of its inputs' range, against the formula in 64 bits: scores of any size."""
+import math
+
+import pytest
+import torch
+
+import long_context_compressed_06_b200 as csa_pkg  # noqa: F401
+from test_gpu_paged import CASES, DEV, ROW_TILES, Case
+
+pytestmark = pytest.mark.gpu
+
+
+def exact_scores(c, size, unit, seed=5):
+    """Queries +-s by head parity, s a vector of signs; keys s * size but for 8 channels that hold s * unit * (0 or 1):
+    every score is +-(size (D - 8) + unit n), n in 0..8, and exact in 32 bits, so that only the weights' and the
+    output's roundings are left of the tolerance in test_gpu_paged.py."""
+    g = torch.Generator().manual_seed(seed)
+    D, H = c.q.shape[-1], c.q.shape[2]
+    s = (torch.randint(0, 2, (D,), generator=g) * 2 - 1).to(torch.bfloat16).to(DEV)
+    c.q = (s * (1 - 2 * (torch.arange(H, device=DEV) % 2)).to(torch.bfloat16)[:, None]).expand(c.q.shape).contiguous()
+
+    def rows(old):  # unused rows stay what they are (NaN)
+        x = torch.full(old.shape, float(size), dtype=torch.bfloat16, device=DEV)
+        x[..., -8:] = unit * torch.randint(0, 2, (*old.shape[:-1], 8), generator=g).to(torch.bfloat16).to(DEV)
+        return torch.where(old.isnan(), old, x * s)
+
+    c.pool, c.ring = rows(c.pool), rows(c.ring)
+    c.pool64, c.ring64 = c.pool.double(), c.ring.double()
+    if c.gain is not None:  # (rows under a gain of 1 are the sum of two bf16 numbers exactly, too)
+        c.gain = torch.ones_like(c.gain)
+
+
+def exact_ref(c):
+    out, mag, e = c.ref()
+    return out, mag, torch.zeros_like(e)
+
+
+# log2 of the largest score at D = 128: 14.0, 14.5, 15.6, 19.4
+@pytest.mark.parametrize("size", [96, 136, 288, 4096])
+@pytest.mark.parametrize("scale", [1.0, -1.0])
+@pytest.mark.parametrize("name", ["d64_h8", "d128_h16", "d256_h64", "d512_h128", "d128_h64_nq4", "part_seen_128"])
+def test_large_scores_over_row_tiles(cuda, name, size, scale):
+    c = Case(**dict(ROW_TILES[name], scale=scale))
+    exact_scores(c, size, 1.0)
+    assert c.by_row_tiles()
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    c.check(got, exact_ref(c))
+
+
+@pytest.mark.parametrize("size", [96, 136, 288])
+@pytest.mark.parametrize("name", ["own_only", "shared_odd", "shared_512"])
+def test_large_scores_query_by_query(cuda, name, size):
+    c = Case(**dict(CASES[name], scale=1.0))
+    exact_scores(c, size, 1.0)
+    assert not c.by_row_tiles()
+    out, mag, e = c.ref()
+    # scores rounded to 32 bits here: off by 2^-24 of their size, with the factor's own rounding
+    c.check(c.run(cuda), (out, mag, e + 2.0 ** -23 * size * c.q.shape[-1]))
+
+
+# scores of 2^25 to 2^67, whose rounding to 32 bits alone moves them by more than 1.  Those below the largest are
+# `unit` = size / 4096 away or more: their weights are next to nothing, whatever their rounding makes of them.
+@pytest.mark.parametrize("size", [2.0 ** 18, 2.0 ** 22, 2.0 ** 26, 2.0 ** 60])
+@pytest.mark.parametrize("name", ["d64_h8", "d128_h16", "d256_h64", "d512_h128", "d128_h64_nq4"])
+def test_huge_scores_over_row_tiles(cuda, name, size):
+    c = Case(**dict(ROW_TILES[name], scale=1.0))
+    unit = size / 4096
+    exact_scores(c, size, unit)
+    assert c.by_row_tiles()
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    # Scores of up to z log2 units come in 32-bit steps of `step`.  A score is rounded by half a step and the reference
+    # that all are taken from cut by up to 3, the same for every key: a key `unit` below the top stays unit / step - 1
+    # steps below it at least (half a step for each of the two), each of them worth `step` units, or 16 where the kernel
+    # takes a step for 16 (from 2^28 on).  All n of them weigh at most n times that, in a channel at most its largest
+    # value.  (D = 512, the closest: unit is 2.9 steps at least.)
+    z = size * c.q.shape[-1] / math.log(2)
+    step = 2.0 ** (math.floor(math.log2(z)) - 23)
+    away = (unit / math.log(2) / step - 1) * (step if z < 2.0 ** 28 else min(step, 16.0)) * math.log(2)
+    n = c.max_pages * c.page + c.Wn
+    extra = n * math.exp(-min(away, 700.0)) * torch.full((c.q.shape[-1],), size, dtype=torch.float64, device=DEV)
+    extra[-8:] *= unit / size
+    out, mag, e = exact_ref(c)
+    assert away > 10
+    c.check(got, (out, mag + 2.0 ** 8 * extra, e))
