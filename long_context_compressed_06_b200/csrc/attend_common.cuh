@@ -63,6 +63,10 @@ CSA_DEVINL float2 rope_cs(const AttendArgs &a, long long t, int i) {
 
 int launch_attend_combine(const AttendArgs &a, cudaStream_t st);
 
+// (running max, sum) of a paged partial row as the merge takes them: a maximum of -inf is a row without keys
+// there, and a NaN score, which is in the sum, raises no maximum.  Under +inf the merged row is NaN.
+CSA_DEVINL float2 partial_ml(float m, float l) { return make_float2(l != l ? INFINITY : m, l); }
+
 // Paged attention of a batch with a shared prefix (attend_prefix.cu): the query
 // rows of the whole batch, [rows = n_bq * H][D], by tiles of 128, against tiles
 // of 128 keys.  A row tile's units are the tiles of shared entries (read through

@@ -368,7 +368,7 @@ CSA_DEVINL bool warps_meet(uint32_t bar, uint32_t &uses, const DevCtx &ctx, vola
 }
 
 // The tile's query rows as they landed: this thread's quarter of row r (units
-// q4, q4 + 4, .. of 8 dims) -> its sum of squares.
+// q4, q4 + 4, .. of 8 dims) -> its sum of squares (of an infinite element: NaN, as its normalised row is).
 template <int DP>
 CSA_DEVINL uint4 *query_unit(uint8_t *q, int r, int unit) {
     return reinterpret_cast<uint4 *>(q + (unit >> 3) * 8192 + r * 128 + (((unit & 7) ^ (r & 7)) << 4));
@@ -384,13 +384,22 @@ CSA_DEVINL float query_squares(uint8_t *q, int r, int q4) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss[e & 1] = fmaf(x[e], x[e], ss[e & 1]);
     }
-    return ss[0] + ss[1];
+    float sum = ss[0] + ss[1];
+    if (sum == INFINITY)  // or only too large for 32 bits
+#pragma unroll 1
+        for (int i = 0; i < DP / 32; ++i) {
+            float x[8];
+            unpack8(*query_unit<DP>(q, r, q4 + 4 * i), x);
+            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], 0.f, sum);
+        }
+    return sum;
 }
 
 // 1 / RMS of a row of these squares times the softmax scale (its sign is the query
-// rows'), in log2 units; above 0, so that a masked score stays -inf
+// rows'), in log2 units; above 0, so that a masked score stays -inf (a NaN stays one)
 CSA_DEVINL float row_factor(const AttendArgs &a, float ss) {
-    return fmaxf((1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
+    const float f = (1.0f / sqrtf(ss / (float)a.D + a.eps)) * fabsf(a.scale) * 1.4426950408889634f;
+    return f < 1e-37f ? 1e-37f : f;
 }
 
 // A row's maximum is exchanged without its last kTagBits bits (rounded towards zero by up to 3 steps of 32
@@ -1072,7 +1081,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
             if (q4 == 0)
                 p.ml[part * kPrefixRows + rank * 64 + r] =
-                    make_float2(m, (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]));
+                    partial_ml(m, (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]));
             if (!warps_meet(rbar, rbar_n, p.ctx, s.abort_flag)) break;
             float4 *dst = reinterpret_cast<float4 *>(p.part) + (part * 2 + rank) * (DP / 8) * 128 + tl;
 #pragma unroll 1
@@ -1168,7 +1177,7 @@ __global__ void __launch_bounds__(256)
         }
     }
     ss = warp_sum(ss);
-    if (lane == 0) rq[row] = row_factor(a, ss);
+    if (lane == 0) rq[row] = row_factor(a, ss);  // (an infinite element is Inf + NaN here: its scores are NaN)
 }
 
 // The rows of an FP8 cache that a call reads, as bf16 (exact) in the order of

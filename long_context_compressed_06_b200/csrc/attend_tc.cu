@@ -985,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (h < a.H && !direct && kh == 0)
                 a.part_ml[((size_t)it.split * a.n_bq + it.bq) * a.H + h] =
-                    it.ntiles > 0 ? make_float2(m_run, l) : make_float2(-INFINITY, 0.f);
+                    it.ntiles == 0 ? make_float2(-INFINITY, 0.f) : PAGED ? partial_ml(m_run, l) : make_float2(m_run, l);
             jt += it.ntiles;
         }
     }

@@ -1,11 +1,12 @@
-"""hca_attend_paged at the ends of its inputs' range, against the formula in 64 bits: scores of any size."""
+"""hca_attend_paged at the ends of its inputs' range, against the formula in 64 bits: scores of any size, keys that are
+not finite."""
 import math
 
 import pytest
 import torch
 
 import long_context_compressed_06_b200 as csa_pkg  # noqa: F401
-from test_gpu_paged import CASES, DEV, ROW_TILES, Case
+from test_gpu_paged import CASES, DEV, ROW_TILES, Case, dequant
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,51 @@ def test_huge_scores_over_row_tiles(cuda, name, size):
     out, mag, e = exact_ref(c)
     assert away > 10
     c.check(got, (out, mag + 2.0 ** 8 * extra, e))
+
+
+# ----------------------------------------------------------------------------- keys and queries that are not finite
+NAN, INF = float("nan"), float("inf")
+
+
+def shows_what_the_formula_does(c, got):
+    """-> where the formula's result is not finite, there the kernel's is not either."""
+    out = c.ref()[0]
+    assert not (got.isfinite() & ~out.isfinite()).any()
+    return ~out.isfinite()
+
+
+# rows of one key, and of few: a NaN score is no maximum, and must not make the row one without keys
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("kw,by_row_tiles", [
+    (CASES["one_token"], False), (CASES["no_entries"], False), (CASES["shared_odd"], False), (ROW_TILES["d128_own_only"], True),
+    (dict(ROW_TILES["part_seen_512"], Wn=1), True), (dict(ROW_TILES["part_seen_64"], Wn=1), True)])
+def test_a_key_that_is_not_finite_shows(cuda, kw, by_row_tiles, value):
+    c = Case(**kw)
+    assert c.by_row_tiles() == by_row_tiles
+    b = int(torch.where(c.pos.amax(1) >= 0, c.pos.amax(1), 2 ** 30).argmin())
+    c.ring[b, int(c.pos[b].max()) % c.ring.shape[1]] = value  # the newest token's row of the shortest request
+    c.ring64 = c.ring.double()
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    hit = shows_what_the_formula_does(c, got)
+    assert hit[b].any() and not hit[torch.arange(len(hit), device=DEV) != b].any()
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("name", ["one_token", "shared_odd", "own_rope", "shared_512", "d64_h8", "d128_h16", "d128_h64_nq4",
+                                  "d256_h64", "d512_h128", "d128_own_only", "part_seen_512", "fp8_128"])
+def test_a_query_that_is_not_finite_is_its_own_rows(cuda, name, value):
+    c = Case(**(ROW_TILES.get(name) or CASES[name]))
+    assert c.by_row_tiles() == (name in ROW_TILES)
+    clean = c.run(cuda)
+    live = (c.pos >= 0).nonzero().tolist()
+    (b0, i0), (b1, i1) = live[0], live[-1]
+    H, D = c.q.shape[2:]
+    rows = torch.zeros(c.q.shape[:3], dtype=torch.bool, device=DEV)
+    for b, i, h in ((b0, i0, 0), (b1, i1, H - 1)):
+        c.q[b, i, h, D - 3] = value
+        rows[b, i, h] = True
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    assert got[rows].isnan().all() and shows_what_the_formula_does(c, got)[rows].all()
+    assert torch.equal(got[~rows].view(torch.int16), clean[~rows].view(torch.int16))
