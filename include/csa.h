@@ -455,7 +455,10 @@ int csa_paged_write_fp8kv(const uint16_t *rows, const long long *slots, long lon
  * with everything else (RMSNorm, gain, sinks, partial RoPE, scale) as
  * csa_attend.  t < 0 (an empty slot of the batch) has no keys: its output rows
  * are zero.  Rows of the pool and of the rings outside the key sets are never
- * used, whatever they hold (unallocated pages may hold NaN).
+ * used, whatever they hold (unallocated pages may hold NaN), and a key that is
+ * not finite, like a query row that is not, shows in the rows of the queries that
+ * take it only.  Where queries of fewer than 128 heads are taken 128 rows at a time
+ * (below), those beside such a query are computed again: the call takes ms.
  *
  * n_shared: the first n_shared entries are the same pages in every row of the
  * table (a multiple of page; 0 = none), rows of empty slots too: they are read

@@ -31,7 +31,127 @@ struct MergeArgs {
     const int2 *meet;
     FastDiv H;
     int n_rows;
+    // what attend_prefix.cu worked on (see PrefixArgs): its keys, and the query rows hi + lo with their factors, if
+    // they were rewritten (lo null: a.q)
+    const uint16_t *keys;
+    long long n_shared;
+    int own_cap;
+    const uint16_t *hi, *lo;
+    const float *rq;
 };
+
+// Rows of attend_prefix.cu again, without a row tile: its P V takes the keys of all queries of a tile for all of
+// their rows, under weights of 0 where a row does not take a key, and 0 x NaN or infinity reaches the row all the
+// same.  Such rows (`bad`: NaN in these 8 dims under a sum that is none) are computed anew here, from their own
+// keys only, by the whole block: lane i of every warp has row `row` (t < 0: none) with 8 dims from d0 on, the
+// warps take the scores of 16 keys at a time in turn, the threads with `bad` their dims.  A row whose own keys make
+// it NaN (an infinity under a score of -inf) gets it again.  In 32 bits, at its leisure: 96 requests of 16 heads over
+// 16K entries take 5.8 ms instead of 43 us if one request's window holds an infinity, but nothing else gets here.
+// (Looking through the keys before P V instead, 16 KiB a tile and SM, took 9 us of every such call.)
+constexpr int kRedoEach = 4, kRedoKeys = kRedoEach * (kMergeThreads / 32);  // keys of a warp, of the block
+constexpr uint32_t kNoKey = 0xffffffffu, kRingKey = 0x80000000u;
+
+// whether queries share the row tile of this row
+CSA_DEVINL bool shares_row_tile(const MergeArgs &g, int row) {
+    const int first = row / kPrefixRows * kPrefixRows;
+    return g.H.div(first) != g.H.div(std::min(first + kPrefixRows, g.n_rows) - 1);
+}
+
+__device__ __noinline__ void redo_rows(const MergeArgs &g, int row, bool active, bool bad, int d0, float *out) {
+    const AttendArgs &a = g.a;
+    __shared__ float score[kRedoKeys][32];
+    __shared__ uint32_t place[kRedoKeys][32];  // row of the pool, the copy or (kRingKey) the rings
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int bq = active ? g.H.div(row) : 0, h = row - bq * a.H;
+    const long long t = active ? __ldg(a.q_pos + bq) : -1, b = bq / a.nq;
+    const long long entries = n_visible(t, a.m, a.N), u0 = t - a.W + 1 > 0 ? t - a.W + 1 : 0;
+    const long long n = t < 0 ? 0 : entries + (t - u0 + 1);
+    const uint16_t *hi = (g.lo ? g.hi : a.q) + (size_t)(active ? row : 0) * a.D;
+    const uint16_t *lo = g.lo ? g.lo + (size_t)(active ? row : 0) * a.D : nullptr;
+    float factor;
+    if (g.lo) {
+        factor = active ? __ldg(g.rq + row) : 0.f;
+    } else {
+        float ss = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < a.D; d += 8) {
+            float q[8];
+            unpack8(ldg16(hi + d), q);
+            for (int e = 0; e < 8; ++e) ss = fmaf(q[e], q[e], ss);
+        }
+        factor = (1.0f / sqrtf(ss / (float)a.D + a.eps)) * a.scale * 1.4426950408889634f;
+    }
+    const uint16_t *rings = g.own_cap >= 0 ? g.keys + (g.n_shared + a.n_bq / a.nq * g.own_cap) * a.D : a.win;
+    const auto values = [&](uint32_t at) { return at & kRingKey ? rings + (size_t)(at & ~kRingKey) * a.D : g.keys + (size_t)at * a.D; };
+    float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    // (every warp has the same rows, so that the loop ends for all of them together)
+    for (long long k0 = 0; __any_sync(0xffffffffu, k0 < n); k0 += kRedoKeys) {
+        __syncthreads();
+        const uint16_t *x[kRedoEach];
+#pragma unroll
+        for (int i = 0; i < kRedoEach; ++i) {
+            const long long k = k0 + kRedoEach * warp + i;
+            uint32_t at = kNoKey;
+            if (k < n && k >= entries) {
+                at = kRingKey | (uint32_t)(b * a.win_rows + (u0 + (k - entries)) % a.win_rows);
+            } else if (k < n && g.own_cap >= 0) {
+                at = (uint32_t)(k < g.n_shared ? k : g.n_shared + b * g.own_cap + (k - g.n_shared));
+            } else if (k < n) {
+                const int id = __ldg(a.table + b * a.max_pages + k / a.page);
+                if (id >= 0 && id < a.n_pages) at = (uint32_t)((long long)id * a.page + k % a.page);
+            }
+            place[kRedoEach * warp + i][lane] = at;
+            x[i] = at == kNoKey ? hi : values(at);  // (a score that is not used)
+        }
+        float s[kRedoEach] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int d = 0; d < a.D; d += 8) {
+            float q[8];
+            unpack8(ldg16(hi + d), q);
+            if (lo) {
+                float l[8];
+                unpack8(ldg16(lo + d), l);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q[e] += l[e];
+            }
+#pragma unroll
+            for (int i = 0; i < kRedoEach; ++i) {
+                float y[8];
+                unpack8(ldg16(x[i] + d), y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[i] = fmaf(q[e], y[e], s[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRedoEach; ++i) score[kRedoEach * warp + i][lane] = s[i] * factor;
+        __syncthreads();
+        if (bad)
+#pragma unroll 4
+            for (int i = 0; i < kRedoKeys; ++i) {
+                const uint32_t at = place[i][lane];
+                if (at == kNoKey) continue;
+                const float s = score[i][lane];
+                if (s > M) {
+                    const float f = exp2f(M - s);
+                    L *= f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[e] *= f;
+                    M = s;
+                }
+                const float p = s == -INFINITY ? 0.f : exp2f(s - M);
+                L += p;
+                float x[8];
+                unpack8(ldg16(values(at) + d0), x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = fmaf(p, x[e], acc[e]);
+            }
+    }
+    if (!bad) return;
+    if (a.sinks) L += exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - M);
+    const float inv = L > 0.f ? 1.0f / L : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = acc[e] * inv;
+}
 
 // A block: 32 rows x 64 dims; a warp 8 of the dims, a lane one row: two 16-byte pieces of each
 // partial, 512 contiguous bytes a load, kAtOnce partials in flight; the output goes through
@@ -40,8 +160,9 @@ struct MergeArgs {
 // Rows of two or three partials want warps, those of a dozen want loads in flight.
 // kGroups = 4, for few rows of many partials: a block 32 rows x 2 x 8 dims (those that RoPE
 // pairs), four warps a quarter of the partials each; their sums meet in shared memory.
-template <int kAtOnce, int kGroups>
-__global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_merge_kernel(const MergeArgs g) {
+// kRedo: rows of several queries share the row tiles of attend_prefix.cu (redo_rows).
+template <int kAtOnce, int kGroups, bool kRedo>
+__global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_merge_kernel(const __grid_constant__ MergeArgs g) {
     const AttendArgs &a = g.a;
     __shared__ float tile[32][65];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slab_bits = 31 - __clz(a.D / 64);  // D is 64 .. 512, a power of two
@@ -147,12 +268,23 @@ __global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_me
             }
         }
     }
+    bool bad = false;
+    if constexpr (kRedo) {
+        // (the weights in L are the row's own: NaN that is in the sums alone may come from others' keys)
+        const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+        bad = sum != sum && L == L && active && group == 0 && shares_row_tile(g, row);
+    }
     if (a.sinks && active) L += exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - M);
     const float inv = L > 0.f ? 1.0f / L : 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (group == 0) tile[lane][d0 % 64 + e] = acc[e] * inv;
-    __syncthreads();
+    if constexpr (!kRedo) {
+        __syncthreads();
+    } else if (__syncthreads_or(bad)) {
+        redo_rows(g, row, active, bad, d0, &tile[lane][d0 % 64]);
+        __syncthreads();
+    }
     // now a thread 8 dims of row threadIdx.x / 8, eight threads 128 contiguous bytes (with groups: two threads a row)
     const int r = (int)threadIdx.x / kSlices, c0 = kGroups == 1 ? (int)(threadIdx.x & 7) * 8 : sub * 8 + (int)(threadIdx.x & 1) * 32;
     if (r >= 32 || row0 + r >= g.n_rows) return;
@@ -295,6 +427,12 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
         g.part = x.part = reinterpret_cast<float *>(w + pl.part);
         g.ml = x.ml = reinterpret_cast<float2 *>(w + pl.ml);
         g.meet = x.meet = reinterpret_cast<int2 *>(w + pl.meet);
+        g.keys = x.keys;
+        g.n_shared = x.n_shared;
+        g.own_cap = x.own_cap;
+        g.hi = x.hi;
+        g.lo = x.lo;
+        g.rq = x.rq;
         rc = launch_attend_prefix(x, ctx, st);
         if (rc != CSA_OK) return rc;
     } else {
@@ -318,16 +456,16 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     cfg.numAttrs = 1;
     // partials of most rows: the splits, or the ranges of a row tile and one that both its ends share
     const int partials = pl.prefix.pairs > 0 ? pl.prefix.pairs / pl.prefix.row_tiles + 1 : pl.splits;
-    cudaError_t e;
     // groups while their blocks leave SMs idle: 32 rows x 64 dims of 74 partials 12.5 -> 10.4 us (the whole call),
     // 256 x 256 of 37 23.4 -> 20.5; but 512 x 512 of some ten 26.7 -> 28.7, 1536 x 128 41.6 -> 43.1
-    if (partials > 6 && 2 * cfg.gridDim.x <= (unsigned)num_sms()) {
-        cfg.gridDim.x *= 4;
-        e = cudaLaunchKernelEx(&cfg, attend_merge_kernel<4, 4>, g);
-    } else {
-        e = partials <= 4 ? cudaLaunchKernelEx(&cfg, attend_merge_kernel<2, 1>, g)
-                          : cudaLaunchKernelEx(&cfg, attend_merge_kernel<6, 1>, g);
-    }
+    const bool groups = partials > 6 && 2 * cfg.gridDim.x <= (unsigned)num_sms();
+    if (groups) cfg.gridDim.x *= 4;
+    // (128 heads: a row tile is one query's.  Without the second look 32 x 128 rows take 1 us less)
+    const bool redo = pl.prefix.pairs > 0 && a.H < kPrefixRows;
+    const auto launch = [&](auto kernel, auto kernel_redo) { return cudaLaunchKernelEx(&cfg, redo ? kernel_redo : kernel, g); };
+    const cudaError_t e = groups         ? launch(attend_merge_kernel<4, 4, false>, attend_merge_kernel<4, 4, true>)
+                          : partials <= 4 ? launch(attend_merge_kernel<2, 1, false>, attend_merge_kernel<2, 1, true>)
+                                          : launch(attend_merge_kernel<6, 1, false>, attend_merge_kernel<6, 1, true>);
     return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 

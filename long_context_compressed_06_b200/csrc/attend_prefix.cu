@@ -10,7 +10,9 @@
 // rarely rescaled).  A tile of 128 rows continues with the own keys of each of
 // its requests, 128 at a time, the rows of other requests masked: with H = 128
 // heads a row tile is one request and nothing is wasted, and a batch of small
-// heads shares the tile's tensor work that the mask throws away.  O, m and l of
+// heads shares the tile's tensor work that the mask throws away.  (Masked rows have
+// weights of 0; what 0 times a key that is not finite does to them the merge finds
+// and mends, attend_paged.cu.)  O, m and l of
 // a range of tiles go out in 32 bits and are merged (attend_paged.cu).
 //
 // A pair of SMs owns 128 rows (cta_group::2, M = 128): every MMA reads half of

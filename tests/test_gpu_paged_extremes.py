@@ -133,3 +133,93 @@ def test_a_query_that_is_not_finite_is_its_own_rows(cuda, name, value):
     assert cuda.csa_sync_status() == 0
     assert got[rows].isnan().all() and shows_what_the_formula_does(c, got)[rows].all()
     assert torch.equal(got[~rows].view(torch.int16), clean[~rows].view(torch.int16))
+
+
+def key_places(c, where):
+    """A key that some queries take and others do not: ("pool", page, row) or ("ring", request, row), and which
+    queries' key sets it is in, [batch][nq]."""
+    pos = c.pos.cpu().long()
+    vis = torch.where(pos >= 0, (pos + 1) // c.m, 0)
+    B = pos.shape[0]
+    if where == "shared":  # an entry of the shared pages that only some of the queries see
+        j = int(vis[(vis > 0) & (vis < c.n_shared)].min())
+        return ("pool", int(c.table[0, j // c.page]), j % c.page), vis > j
+    b = max(range(B // 3, B), key=lambda i: (int(vis[i].max()) > c.n_shared, -abs(i - B // 2)))
+    of_b = (torch.arange(B) == b)[:, None]
+    if where.endswith("entry"):
+        j = c.n_shared if where == "first_entry" else int(vis[b].max()) - 1
+        assert j >= c.n_shared and vis[b].max() > j
+        return ("pool", int(c.table[b, j // c.page]), j % c.page), of_b & (vis > j)
+    u = int(pos[b].max()) - (0 if where == "newest_token" else c.Wn // 2)
+    return ("ring", b, u % c.ring.shape[1]), of_b & (pos >= u) & (u > pos - c.Wn)
+
+
+def check_apart(cuda, c, where, value, whole):
+    clean = c.run(cuda)
+    (kind, i, r), takes = key_places(c, where)
+    assert takes.any() and not takes.all()
+    rows = getattr(c, kind)
+    assert c.fp8 or rows[i, r].isfinite().all()
+    D, H = c.q.shape[-1], c.q.shape[2]
+    rows[i, r, slice(None) if whole else slice(D // 2 + 5, D // 2 + 6)] = value
+    if c.fp8:
+        c.pool64, c.ring64 = dequant(c.pool, c.pe), dequant(c.ring, c.re)
+    else:
+        c.pool64, c.ring64 = c.pool.double(), c.ring.double()
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    takes = takes.to(DEV)
+    out, mag, e = c.ref()
+    # who takes it shows it, wherever the formula does
+    assert not out[takes].isfinite().all()
+    assert not (got[takes].isfinite() & ~out[takes].isfinite()).any()
+    # who does not take it is as right as ever, and as it was to the bit if no row beside its own in a tile of 128 does
+    x = ~takes
+    assert got[x].isfinite().all()
+    tol = 2.0 ** -8 * out[x].abs() + (2.0 ** -8 + torch.expm1(2 * e[x] * (256 if D == 512 and not c.by_row_tiles() else 1))
+                                      + 2.0 ** -10) * mag[x]
+    assert ((got[x].double() - out[x]).abs() <= tol).all()
+    row_takes = takes[:, :, None].expand(-1, -1, H).flatten()
+    if c.by_row_tiles():
+        tile_takes = torch.nn.functional.pad(row_takes, (0, -len(row_takes) % 128)).view(-1, 128).any(1)
+        row_takes = tile_takes.repeat_interleave(128)[:len(row_takes)]
+    same = (got.view(torch.int16) == clean.view(torch.int16)).flatten(0, 2).all(-1)
+    assert same[~row_takes].all()
+
+
+VALUES = [(NAN, False), (NAN, True), (INF, False), (-INF, True)]
+
+
+@pytest.mark.parametrize("value,whole", VALUES)
+@pytest.mark.parametrize("where", ["first_entry", "last_entry", "newest_token", "mid_window"])
+@pytest.mark.parametrize("name", ["d64_h8", "d64_h1", "d128_h16", "d128_h40_rope", "d128_h64_nq4", "d256_h100", "d256_h64",
+                                  "d512_h72", "d512_h128_nq4", "d128_own_only"])
+def test_a_key_reaches_only_who_takes_it_over_row_tiles(cuda, name, where, value, whole):
+    c = Case(**ROW_TILES[name])
+    assert c.by_row_tiles()
+    check_apart(cuda, c, where, value, whole)
+
+
+@pytest.mark.parametrize("value,whole", VALUES)
+@pytest.mark.parametrize("name", ["part_seen_64", "part_seen_128", "part_seen_256", "part_seen_512"])
+def test_a_shared_key_reaches_only_who_sees_it_over_row_tiles(cuda, name, value, whole):
+    c = Case(**ROW_TILES[name])
+    assert c.by_row_tiles()
+    check_apart(cuda, c, "shared", value, whole)
+
+
+@pytest.mark.parametrize("where", ["first_entry", "newest_token"])
+@pytest.mark.parametrize("name", ["fp8_128", "fp8_256_own", "fp8_512"])
+def test_an_fp8_key_reaches_only_who_takes_it_over_row_tiles(cuda, name, where):
+    c = Case(**ROW_TILES[name])
+    assert c.by_row_tiles()
+    check_apart(cuda, c, where, 0x7F, False)  # NaN
+
+
+@pytest.mark.parametrize("value,whole", VALUES)
+@pytest.mark.parametrize("name,where", [("own_only", "first_entry"), ("own_only", "newest_token"), ("shared_odd", "last_entry"),
+                                        ("shared_rope_128", "newest_token"), ("part_seen", "shared"), ("shared_256", "mid_window")])
+def test_a_key_reaches_only_who_takes_it_query_by_query(cuda, name, where, value, whole):
+    c = Case(**CASES[name])
+    assert not c.by_row_tiles()
+    check_apart(cuda, c, where, value, whole)
