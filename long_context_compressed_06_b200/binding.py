@@ -1,7 +1,8 @@
 """Thin Python binding of libcsa.so (include/csa.h), same names as the C ABI.
 
 Argument marshalling only: every step runs in the library's CUDA kernels.  The paged calls marshal their regular case
-in C++ (_native.so, built beside the library); the Python below is what they do otherwise, checks and errors included.
+in C++ if _native.so, which is built beside the library, is there for this torch; the Python below is what they do
+otherwise, checks and errors included.
 Tensors are torch CUDA tensors (PyTorch supplies device memory and the current
 stream); outputs are allocated here when not given.  If the shared library is
 missing the first call raises -- there is no fallback.
@@ -24,7 +25,7 @@ _lib = None
 
 
 class _Unbound:
-    """_native before load(): no call is regular yet."""
+    """_native before load(), and without _native.so: no call is regular."""
 
     @staticmethod
     def _none(*args):
@@ -94,13 +95,14 @@ def load() -> ctypes.CDLL:
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = res
-    try:
-        from . import _native as native
-    except ImportError as e:
-        raise RuntimeError("_native.so is not built for this torch; run `python -m long_context_compressed_06_b200.build`") from e
-    native.bind(LIB_PATH)
     global _native
-    _native = native
+    try:  # a shortcut of three calls: without it, or with one of another torch, they take the long way
+        from . import _native as native
+        if getattr(native, "torch_version", None) == torch.__version__:
+            native.bind(LIB_PATH)
+            _native = native
+    except ImportError:
+        pass
     _lib = L
     return L
 

@@ -3,7 +3,8 @@
 Each .cu under csrc/ is compiled to an object in _build/ (parallel, skipped
 when up to date) and linked into long_context_compressed_06_b200/libcsa.so
 against the shared CUDA runtime.  csrc/binding_native.cpp, the C++ side of the
-binding, is compiled with g++ against torch's headers into _native.so beside it.
+binding, is then compiled with g++ against torch's headers into _native.so beside
+it; where that cannot be done the binding does without, and a line says so.
 """
 import concurrent.futures as cf
 import glob
@@ -57,7 +58,8 @@ def build_native(force: bool = False) -> str:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.dirname(os.path.dirname(NVCC))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), "-I", os.path.join(ROOT, "include")]
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(),
+           '-DCSA_TORCH_VERSION="%s"' % torch.__version__, "-I", os.path.join(ROOT, "include")]
     for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
               sysconfig.get_paths()["include"]):
         cmd += ["-isystem", d]
@@ -73,7 +75,15 @@ def build_native(force: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    build_native(force)
+    lib = _build_lib(force, verbose)
+    try:
+        build_native(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        sys.stderr.write("_native.so is not built, the binding does without it: %s\n" % e)
+    return lib
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):

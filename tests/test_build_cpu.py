@@ -1,0 +1,45 @@
+"""What the build and the binding do where the C++ side of the binding (_native.so) is not there."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from long_context_compressed_06_b200 import build as csa_build
+
+WITHOUT = """
+import sys, types
+{block}
+import torch
+import long_context_compressed_06_b200 as csa
+from long_context_compressed_06_b200 import binding
+L = csa.load()
+assert binding._native is binding._Unbound
+assert csa.strerror(-2) and L.csa_version() >= 0
+assert csa.attend_workspace_bytes(2, 1, 128, 512, 4096) >= 0
+i = torch.zeros(4, dtype=torch.int32)
+for call in (lambda: csa.csa_plan_pages(i, i, i, i.view(2, 2), 4, 16, 16, 9, 9), lambda: csa.csa_paged_write(i, i, i),
+             lambda: csa.hca_attend_paged(i, i, i, 4, i, i, 16, 1.0)):
+    try:
+        call()
+    except TypeError:   # the long way's check: not a CUDA tensor
+        continue
+    raise SystemExit("no refusal")
+"""
+
+
+@pytest.mark.parametrize("block", [
+    "sys.modules['long_context_compressed_06_b200._native'] = None",                       # not built
+    "m = types.ModuleType('x'); m.torch_version = '1.0'; m.bind = None; "
+    "sys.modules['long_context_compressed_06_b200._native'] = m"])                        # built for another torch
+def test_binding_without_native(block):
+    csa_build.build()
+    r = subprocess.run([sys.executable, "-c", WITHOUT.format(block=block)], cwd=csa_build.ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_library_is_built_without_a_host_compiler(monkeypatch, capsys):
+    monkeypatch.setenv("CXX", "/nowhere/g++")
+    monkeypatch.setattr(csa_build, "NATIVE", csa_build.NATIVE + ".test")
+    assert csa_build.build() == csa_build.LIB and os.path.exists(csa_build.LIB)
+    assert "_native.so is not built" in capsys.readouterr().err
