@@ -46,6 +46,7 @@ def _compile(src: str, verbose: bool) -> str:
 
 
 def build_native(force: bool = False) -> str:
+    import shutil
     import sysconfig
 
     import torch
@@ -56,12 +57,13 @@ def build_native(force: bool = False) -> str:
         return NATIVE
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cuda = os.path.dirname(os.path.dirname(NVCC))
+    nvcc = shutil.which(NVCC) or NVCC  # (a path, or a name to look up)
+    cuda = [os.path.dirname(os.path.dirname(p)) for p in (nvcc, os.path.realpath(nvcc))]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(),
            '-DCSA_TORCH_VERSION="%s"' % torch.__version__, "-I", os.path.join(ROOT, "include")]
-    for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
-              sysconfig.get_paths()["include"]):
+    for d in [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]] + \
+            [os.path.join(c, "include") for c in cuda]:
         cmd += ["-isystem", d]
     cmd += [NATIVE_SRC, "-o", NATIVE + ".tmp", "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -43,3 +43,12 @@ def test_library_is_built_without_a_host_compiler(monkeypatch, capsys):
     monkeypatch.setattr(csa_build, "NATIVE", csa_build.NATIVE + ".test")
     assert csa_build.build() == csa_build.LIB and os.path.exists(csa_build.LIB)
     assert "_native.so is not built" in capsys.readouterr().err
+
+
+def test_native_is_built_with_nvcc_by_name(monkeypatch, tmp_path):
+    """NVCC may be a name that the shell finds."""
+    monkeypatch.setattr(csa_build, "NVCC", "nvcc")
+    monkeypatch.setattr(csa_build, "NATIVE", str(tmp_path / "_native.so"))
+    monkeypatch.setattr(csa_build, "BUILD", str(tmp_path))
+    monkeypatch.setenv("PATH", "/usr/local/cuda/bin" + os.pathsep + os.environ["PATH"])
+    assert os.path.exists(csa_build.build_native(force=True))
