@@ -300,8 +300,12 @@ def _workspace(nbytes: int, device, workspace):
         return None, 0
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
-    _need(workspace, workspace.dtype, "workspace")
-    return workspace, workspace.numel() * workspace.element_size()
+    # memory of this device: a view with gaps holds as many bytes from its first element on
+    n = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    if n and n <= 1 + sum((k - 1) * step for k, step in zip(workspace.shape, workspace.stride())):
+        workspace = workspace.as_strided((n,), (1,))
+    _need(workspace, getattr(workspace, "dtype", None), "workspace")
+    return workspace, n * workspace.element_size()
 
 
 def _sinks(sinks, H):
