@@ -327,8 +327,11 @@ constexpr long long kMaxCopyBytes = 1LL << 30;
 // busiest CTA (FP8: 5.6), attend_prefix.cu 0.9 to 1.45 us per unit and what its ranges' partials cost the merge.
 // E.g. at D = 512, 128 heads: 8 requests over 1024 shared entries 22 us and 24 us, 32 over 1024 42 and 36,
 // 32 over 16384 331 and 122; at D = 128, 16 heads: 16 over 1024 16 and 28, 64 over 16384 281 and 38.
+// The gather kernel reads a query's window; attend_prefix.cu goes through every row of the ring and clears those
+// outside the window one by one, ~6 us per 128 of them (32 x 128 heads over 2048 entries, rings of 2048 / 8192
+// rows: 59 / 59 us and 104 / 239; 64 x 16 heads over 4096: 92 / 92 and 120 / 366; 2 x 512 queries, 639 rows: 287 and 629).
 bool prefix_pays(long long n_bq, int H, int D, long long n_shared, long long own, int nq, const PagedPlan &gather, int W,
-                 bool fp8, const PrefixPlan &pl) {
+                 int ring_rows, bool fp8, const PrefixPlan &pl) {
     const long long HH = (H + 63) / 64, keys = n_shared + own + W;
     const long long per = ((keys + 63) / 64 + gather.splits - 1) / gather.splits;
     const long long waves = (n_bq * HH * gather.splits + num_sms() - 1) / num_sms();
@@ -337,9 +340,10 @@ bool prefix_pays(long long n_bq, int H, int D, long long n_shared, long long own
     const double requests = std::max(1.0, (double)kPrefixRows / ((double)H * nq));
     const double u = (double)((n_shared + kPrefixKeys - 1) / kPrefixKeys) + requests * (double)((own + W + 2 * kPrefixKeys - 17) / kPrefixKeys);
     const double units = u * pl.row_tiles, ranges = pl.ranges((int)std::min(units, 2e9));
+    const double outside = requests * pl.row_tiles * (double)(ring_rows - W) / kPrefixKeys;
     const double unit = D == 512 ? 1.45 : (D == 256 ? 1.1 : 0.9);
     const double t_prefix = 14.0 + (fp8 ? 2.0 : 0.0) + unit * ((units + PrefixPlan::kPartCost * pl.row_tiles) / ranges) +
-                            unit / 3 * (ranges / pl.row_tiles);
+                            unit / 3 * (ranges / pl.row_tiles) + 6.0 * outside / ranges;
     return t_prefix < t_gather;
 }
 
@@ -356,7 +360,7 @@ PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, l
     attend_tc_plan(n_bq, H, cap + W, &pl.splits, &pl.keys_per_split);
     const PrefixPlan prefix = prefix_plan(std::min(rows, 0x7fffffffLL));
     if (rows <= 0x7fffffffLL - kPrefixRows && copy <= kMaxCopyBytes && tiles <= 0x7fffffffLL / (rows / kPrefixRows + 1) &&
-        ((rewrite && D == 512) || prefix_pays(n_bq, H, D, n_shared, cap - n_shared, nq, pl, W, fp8, prefix))) {
+        ((rewrite && D == 512) || prefix_pays(n_bq, H, D, n_shared, cap - n_shared, nq, pl, W, ring_rows, fp8, prefix))) {
         pl.prefix = prefix;
         if (rewrite) {
             pl.hi = take(at, (size_t)rows * D * sizeof(uint16_t));

@@ -7,6 +7,7 @@ import torch
 
 from long_context_compressed_06_b200 import build as csa_build
 from long_context_compressed_06_b200 import workloads as W
+from test_gpu_paged import Case, spread
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -39,3 +40,14 @@ def test_status_is_the_first_call_of_a_process(cuda):
                         "import torch; assert torch.zeros(3, device='cuda').sum().item() == 0"],
                        cwd=csa_build.ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("kw,extra", [
+    (dict(ts=spread(2103, 2168, 32), H=128, D=512, m=1, page=64, n_shared=2048, Wn=128), 1920),
+    (dict(ts=spread(4103, 4160, 64), H=16, D=128, m=1, page=64, n_shared=4096, Wn=128), 8064)])
+def test_rings_much_longer_than_the_window_are_not_taken_whole(cuda, kw, extra):
+    """The kernel over row tiles goes through every row of the rings: it is not the choice where that is most of it."""
+    assert Case(**kw).by_row_tiles()
+    c = Case(**kw, ring_extra=extra)
+    assert not c.by_row_tiles()
+    c.check(c.run(cuda))
