@@ -159,27 +159,19 @@ int launch_attend_combine(const AttendArgs &a, cudaStream_t st) {
 }
 
 bool attend_tc_supported(int H, int D);
-void attend_tc_plan(long long n_bq, int H, long long max_keys, int *splits, long long *kps);
+int attend_tc_plan(long long n_bq, int H, long long max_keys);
 int launch_attend_tc(AttendArgs a, const DevCtx &ctx, cudaStream_t st, bool pdl);
 
 // Split plan of the tensor-core kernel for these shapes (one split when the
 // shapes are outside the compiled tiles: the launch then returns
 // CSA_ERR_UNSUPPORTED before using any workspace).
-static void plan_splits(long long n_bq, int H, int D, long long max_keys, int *splits, long long *kps) {
-    if (attend_tc_supported(H, D)) {
-        attend_tc_plan(n_bq, H, max_keys, splits, kps);
-    } else {
-        *splits = 1;
-        *kps = max_keys;
-    }
+static int plan_splits(long long n_bq, int H, int D, long long max_keys) {
+    return attend_tc_supported(H, D) ? attend_tc_plan(n_bq, H, max_keys) : 1;
 }
 
 size_t attend_workspace_bytes(int batch, int nq, int H, int D, long long max_keys) {
     const long long n_bq = (long long)batch * nq;
-    int splits;
-    long long kps;
-    plan_splits(n_bq, H, D, max_keys, &splits, &kps);
-    return ws_bytes_for(n_bq, H, D, splits);
+    return ws_bytes_for(n_bq, H, D, plan_splits(n_bq, H, D, max_keys));
 }
 
 int launch_attend(const uint16_t *q, const float *q_gain, const float *sinks, const float *rope_cos,
@@ -199,7 +191,7 @@ int launch_attend(const uint16_t *q, const float *q_gain, const float *sinks, co
     if (a.n_bq == 0) return CSA_OK;
     if (!attend_tc_supported(H, D)) return CSA_ERR_UNSUPPORTED;
     const long long max_keys = (dense ? N : (long long)k) + W;
-    plan_splits(a.n_bq, H, D, max_keys, &a.splits, &a.keys_per_split);
+    a.splits = plan_splits(a.n_bq, H, D, max_keys);
     const size_t need = ws_bytes_for(a.n_bq, H, D, a.splits);
     if (need > 0) {
         if (!ws || ws_bytes < need) return CSA_ERR_WORKSPACE;

@@ -50,7 +50,6 @@ struct AttendArgs {
     float *part_f;          // paged: [splits][n_bq][H][D] fp32 partial outputs, not divided, part_perm as
                             // for part_o (null: the one split's output rows are final)
     int splits;
-    long long keys_per_split;
 };
 
 // (cos, sin) of rotated pair i (< kRopeDim / 2) at position t; (1, 0) -- no

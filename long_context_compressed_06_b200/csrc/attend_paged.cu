@@ -16,7 +16,7 @@
 
 namespace csa {
 
-void attend_tc_plan(long long n_bq, int H, long long max_keys, int *splits, long long *kps);
+int attend_tc_plan(long long n_bq, int H, long long max_keys);
 int launch_attend_tc(AttendArgs a, const DevCtx &ctx, cudaStream_t st, bool pdl);
 
 namespace {
@@ -309,7 +309,6 @@ __global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_me
 struct PagedPlan {
     PrefixPlan prefix;  // pairs > 0: attend_prefix.cu
     int splits;
-    long long keys_per_split;
     size_t keys, hi, lo, rq, part, ml, meet, bytes;  // offsets
 };
 
@@ -357,7 +356,7 @@ PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, l
     // units are counted in 32 bits: shared tiles and, of each request in a row tile, own ones
     const long long tiles = n_shared / kPrefixKeys + 1 + (1 + kPrefixRows / H) * ((cap - n_shared + ring_rows) / kPrefixKeys + 2);
     size_t at = 0;
-    attend_tc_plan(n_bq, H, cap + W, &pl.splits, &pl.keys_per_split);
+    pl.splits = attend_tc_plan(n_bq, H, cap + W);
     const PrefixPlan prefix = prefix_plan(std::min(rows, 0x7fffffffLL));
     if (rows <= 0x7fffffffLL - kPrefixRows && copy <= kMaxCopyBytes && tiles <= 0x7fffffffLL / (rows / kPrefixRows + 1) &&
         ((rewrite && D == 512) || prefix_pays(n_bq, H, D, n_shared, cap - n_shared, nq, pl, W, ring_rows, fp8, prefix))) {
@@ -402,7 +401,6 @@ int launch_attend_paged(const PagedArgs &p, void *ws, size_t ws_bytes, const Dev
     if (pl.bytes > 0 && (!ws || ws_bytes < pl.bytes)) return CSA_ERR_WORKSPACE;
     char *w = static_cast<char *>(ws);
     a.splits = pl.splits;
-    a.keys_per_split = pl.keys_per_split;
     MergeArgs g = {};
     g.a = a;
     g.H = FastDiv::by((uint32_t)a.H);

@@ -100,7 +100,6 @@ struct Params {
     const float *rq;
     int2 *meet;       // [row_tiles], see PrefixArgs
     FastDiv H, nq, m, page, ring;
-    const uint16_t *keys;  // the pool's rows; linear: the copy's, see PrefixArgs
     int batch;
     int own_cap;           // linear: rows of the copy for one request's own entries
     int box;          // entries that one copy brings at most (none crosses a page): 16, 32 or 64
@@ -1242,7 +1241,6 @@ int launch_d(const PrefixArgs &x, const DevCtx &ctx, cudaStream_t st) {
     p.lo = x.lo ? 1 : 0;
     p.rq = x.rq;
     p.dependent = p.linear || p.lo;
-    p.keys = x.keys;
     p.batch = (int)(x.a.n_bq / x.a.nq);
     p.own_cap = x.own_cap;
     p.part = x.part;

@@ -1066,7 +1066,7 @@ bool attend_tc_supported(int H, int D) { return H >= 1 && H <= 128 && (D == 64 |
 // SMs, chosen to minimise the tiles of the busiest CTA (plus a small per-item
 // and per-split overhead).  The kernel deals each query's 64-key tiles to its
 // splits in balanced contiguous ranges, so the plan only needs the count.
-void attend_tc_plan(long long n_bq, int H, long long max_keys, int *splits, long long *kps) {
+int attend_tc_plan(long long n_bq, int H, long long max_keys) {
     const long long HH = (H + kHeads - 1) / kHeads;
     const long long ctas = num_sms();
     const long long tiles = (max_keys + kTileKeys - 1) / kTileKeys;
@@ -1083,8 +1083,7 @@ void attend_tc_plan(long long n_bq, int H, long long max_keys, int *splits, long
         }
         if (per <= 1) break;
     }
-    *splits = best;
-    *kps = ((tiles + best - 1) / best) * kTileKeys;
+    return best;
 }
 
 template <bool PAGED>
