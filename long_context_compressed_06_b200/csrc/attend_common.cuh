@@ -62,9 +62,17 @@ CSA_DEVINL float2 rope_cs(const AttendArgs &a, long long t, int i) {
 
 int launch_attend_combine(const AttendArgs &a, cudaStream_t st);
 
-// (running max, sum) of a paged partial row as the merge takes them: a maximum of -inf is a row without keys
-// there, and a NaN score, which is in the sum, raises no maximum.  Under +inf the merged row is NaN.
-CSA_DEVINL float2 partial_ml(float m, float l) { return make_float2(l != l ? INFINITY : m, l); }
+// (running max, sum) of a paged partial row as the merge takes them; l is kTaken at least, far below any weight, in a
+// row that has keys there.  A maximum of -inf is a row without keys, but neither a NaN score, which is in the sum, nor one of
+// -inf raises a maximum.  Under +inf the merged row is NaN; under the lowest number the partial weighs 0 beside
+// others (and 0 x inf is in its O), and alone has 0 / 0.
+constexpr float kTaken = 1e-37f, kLowest = -3.402823466e38f;
+CSA_DEVINL float2 partial_ml(float m, float l) {
+    if (l != l) return make_float2(INFINITY, l);
+    return m == -INFINITY && l > 0.f ? make_float2(kLowest, 0.f) : make_float2(m, l);
+}
+// 1 / L for a merged row: 0 of a row without keys (M = -inf)
+CSA_DEVINL float inverse_sum(float M, float L) { return L > 0.f ? 1.0f / L : (M == -INFINITY ? 0.f : __int_as_float(0x7fffffff)); }
 
 // Paged attention of a batch with a shared prefix (attend_prefix.cu): the query
 // rows of the whole batch, [rows = n_bq * H][D], by tiles of 128, against tiles

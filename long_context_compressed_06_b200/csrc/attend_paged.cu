@@ -147,8 +147,9 @@ __device__ __noinline__ void redo_rows(const MergeArgs &g, int row, bool active,
             }
     }
     if (!bad) return;
+    M = fmaxf(M, kLowest);  // (it has keys)
     if (a.sinks) L += exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - M);
-    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    const float inv = inverse_sum(M, L);
 #pragma unroll
     for (int e = 0; e < 8; ++e) out[e] = acc[e] * inv;
 }
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kMergeThreads, kAtOnce <= 2 ? 4 : 2) attend_me
         bad = sum != sum && L == L && active && group == 0 && shares_row_tile(g, row);
     }
     if (a.sinks && active) L += exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - M);
-    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    const float inv = inverse_sum(M, L);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (group == 0) tile[lane][d0 % 64 + e] = acc[e] * inv;

@@ -977,6 +977,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     mk1 = key_mask(p, d, hf * 64 + 32, rw);
                     whole = __all_sync(0xffffffffu, (mk0 & mk1) == 0xffffffffu);
                 }
+                if ((mk0 | mk1) && l == 0.f) l = kTaken;
                 if (!wait(s.sfull + sb, (g / kSBufs) & 1u)) break;
                 tc::fence_after_sync();
                 float sc[64];

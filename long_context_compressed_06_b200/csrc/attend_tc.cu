@@ -831,6 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(smem_u32(s.qready));
 
             float m_run = -INFINITY, l = 0.f;
+            bool taken = false;  // a key
             for (int j = 0; j < it.ntiles && ok; ++j) {
                 const long long g = jt + j;
                 const int sb = (int)(g & 1);
@@ -845,6 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const uint64_t vmask = s.kmask[st] >> (32 * kh);
+                taken |= PAGED && s.kmask[st] != 0;
                 tc::fence_after_sync();
                 float sc[32], sc2[32];
                 tmem_ld_half32(tmem_s + lane_base + sb * kTileKeys, sc);
@@ -928,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float L = direct
                                 ? l + ((a.sinks && h < a.H) ? exp2f(__ldg(a.sinks + h) * 1.4426950408889634f - m_run) : 0.f)
                                 : l;
-            const float inv = PAGED && !direct ? 1.0f : (L > 0.f ? 1.0f / L : 0.f);
+            const float inv = PAGED && !direct ? 1.0f : PAGED && taken ? inverse_sum(kLowest, L) : (L > 0.f ? 1.0f / L : 0.f);
             const int orow = (int)(direct ? it.bq : (long long)it.split * a.n_bq + it.bq);
             for (int c = 0; c < D; c += 64) {
                 float v[32];
@@ -985,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (h < a.H && !direct && kh == 0)
                 a.part_ml[((size_t)it.split * a.n_bq + it.bq) * a.H + h] =
-                    it.ntiles == 0 ? make_float2(-INFINITY, 0.f) : PAGED ? partial_ml(m_run, l) : make_float2(m_run, l);
+                    it.ntiles == 0 ? make_float2(-INFINITY, 0.f) : PAGED ? partial_ml(m_run, taken && l == 0.f ? kTaken : l) : make_float2(m_run, l);
             jt += it.ntiles;
         }
     }

@@ -223,3 +223,29 @@ def test_a_key_reaches_only_who_takes_it_query_by_query(cuda, name, where, value
     c = Case(**CASES[name])
     assert not c.by_row_tiles()
     check_apart(cuda, c, where, value, whole)
+
+
+# an infinite channel: heads whose query has its sign have a score of +inf, the others one of -inf, a weight of 0, and
+# 0 x inf; with no other key, or no other in the partial row, 0 / 0
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("value", [INF, -INF])
+@pytest.mark.parametrize("kw,by_row_tiles", [
+    (CASES["one_token"], False), (CASES["no_entries"], False), (dict(CASES["shared_512"], ts=[[1700], [1690], [0]], Wn=1), False),
+    (dict(CASES["own_only"], Wn=1), False), (ROW_TILES["d128_own_only"], True), (dict(ROW_TILES["part_seen_512"], Wn=1), True),
+    (dict(ROW_TILES["part_seen_64"], Wn=1), True), (dict(ROW_TILES["d512_h72"], Wn=1), True)])
+def test_scores_of_minus_infinity_are_not_rows_without_keys(cuda, kw, by_row_tiles, value, sinks):
+    c = Case(**dict(kw, sinks=sinks))
+    assert c.by_row_tiles() == by_row_tiles
+    b = int(torch.where(c.pos.amax(1) >= 0, c.pos.amax(1), 2 ** 30).argmin())
+    r = int(c.pos[b].max()) % c.ring.shape[1]
+    # every key of the query, where there are few; else its window
+    for u in range(max(0, int(c.pos[b].max()) - c.Wn + 1), int(c.pos[b].max()) + 1):
+        c.ring[b, u % c.ring.shape[1], 7] = value
+    assert c.ring[b, r, 7] == value
+    c.ring64 = c.ring.double()
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    hit = shows_what_the_formula_does(c, got)
+    assert hit[b].any()
+    rest = (torch.arange(len(hit), device=DEV) != b)
+    assert not hit[rest].any() and got[rest].isfinite().all()
