@@ -354,8 +354,10 @@ PagedPlan paged_plan(int batch, int nq, int H, int D, int page, int max_pages, l
     PagedPlan pl = {};
     const long long n_bq = (long long)batch * nq, rows = n_bq * H, cap = (long long)max_pages * page;
     const long long copy = fp8 ? (n_shared + batch * (cap - n_shared + ring_rows)) * D * (long long)sizeof(uint16_t) : 0;
-    // units are counted in 32 bits: shared tiles and, of each request in a row tile, own ones
-    const long long tiles = n_shared / kPrefixKeys + 1 + (1 + kPrefixRows / H) * ((cap - n_shared + ring_rows) / kPrefixKeys + 2);
+    // units are counted in 32 bits, with what a row tile costs beside them: shared tiles and, of each request in a row
+    // tile (one in part at either end), own ones
+    const long long tiles = PrefixPlan::kPartCost + n_shared / kPrefixKeys + 1 +
+                            (2 + kPrefixRows / H) * ((cap - n_shared + ring_rows) / kPrefixKeys + 2);
     size_t at = 0;
     pl.splits = attend_tc_plan(n_bq, H, cap + W);
     const PrefixPlan prefix = prefix_plan(std::min(rows, 0x7fffffffLL));

@@ -52,3 +52,15 @@ def test_native_is_built_with_nvcc_by_name(monkeypatch, tmp_path):
     monkeypatch.setattr(csa_build, "BUILD", str(tmp_path))
     monkeypatch.setenv("PATH", "/usr/local/cuda/bin" + os.pathsep + os.environ["PATH"])
     assert os.path.exists(csa_build.build_native(force=True))
+
+
+def test_row_tiles_whose_units_pass_32_bits_are_not_taken():
+    """A row tile of 128 rows meets three requests of 65 heads; its units are numbered in 32 bits with those of the
+    others.  Past that the call goes query by query (no workspace: one split)."""
+    import long_context_compressed_06_b200 as csa
+    csa_build.build()
+    batch = 2 ** 29 // 65  # 2^22 row tiles, 511 units each fit
+    for keys, fits in ((160 * 128, True), (172 * 128, False), (253 * 128, False)):
+        pages = (keys - 16) // 16  # own entries, and a ring of 16 rows
+        need = csa.attend_paged_workspace_bytes(batch, 1, 65, 512, 16, pages, 0, 16, 16, False, True)
+        assert (need > 0) == fits, keys
