@@ -474,6 +474,11 @@ int csa_paged_write_fp8kv(const uint16_t *rows, const long long *slots, long lon
  * rows are rounded to bf16 only where it cannot be taken (FP8 caches of more than
  * 2^30 bytes as bf16: batch times table width times D; tables and batches whose
  * tiles number 2^31).
+ * The host decides from the table's width, not from the requests' lengths, and so
+ * does an FP8 call that takes the rows together, which first writes the cache's rows
+ * as bf16: (n_shared + batch * (max_pages * page - n_shared + ring_rows)) * D * 2
+ * bytes of workspace, ~0.12 us per MiB whatever the requests hold.  A table no wider
+ * than the step needs, and rings no longer than W + nq - 1, are the fastest.
  *   q [batch][nq][H][D] bf16      pool [n_pages][page][D] bf16
  *   block_table [batch][max_pages] int32 (ids outside [0, n_pages): no entry)
  *   ring [batch][ring_rows][D] bf16     q_pos [batch][nq] int32

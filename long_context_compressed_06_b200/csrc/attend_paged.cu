@@ -327,6 +327,11 @@ constexpr long long kMaxCopyBytes = 1LL << 30;
 // busiest CTA (FP8: 5.6), attend_prefix.cu 0.9 to 1.45 us per unit and what its ranges' partials cost the merge.
 // E.g. at D = 512, 128 heads: 8 requests over 1024 shared entries 22 us and 24 us, 32 over 1024 42 and 36,
 // 32 over 16384 331 and 122; at D = 128, 16 heads: 16 over 1024 16 and 28, 64 over 16384 281 and 38.
+// The host knows the tables' width, not the requests' lengths: `own` is what the width has room for.  The copy of an
+// FP8 cache takes ~0.12 us per MiB on top (32 x 128 heads over 8192 entries, 192 own ones in tables of 192 / 16000:
+// 77 and 141 us, 354 and 344 query by query); with that in the estimate too many calls of long requests go query
+// by query, whose FP8 time it puts too low (2 x 16 heads of 256 over 65536: 66 and 88 us, 8 x 8 of 512 over 16384 102
+// and 96), so it stands without.
 // The gather kernel reads a query's window; attend_prefix.cu goes through every row of the ring and clears those
 // outside the window one by one, ~6 us per 128 of them (32 x 128 heads over 2048 entries, rings of 2048 / 8192
 // rows: 59 / 59 us and 104 / 239; 64 x 16 heads over 4096: 92 / 92 and 120 / 366; 2 x 512 queries, 639 rows: 287 and 629).

@@ -24,14 +24,18 @@
 // The price is that each SM loads 64 of a tile's 128 keys whole (its half of
 // K's rows) and all 128 keys by half their dims (its half of V's columns):
 // 128 KiB per SM and tile at D = 512, 1.33 times what one copy would be.
-// At D = 512 these loads (~40 B a cycle and SM from L2, where a tile takes ~3200
-// cycles) bound the kernel, close before the tensor cores (QK 1056 + P.V 1056 cycles
-// and what they wait for); 32 row tiles of 8064 + 192 keys take 62 us with the merge.
-// At D = 128 the softmax does: ~1850 cycles a tile, a third of it exponentials.
+// At D = 512 a tile takes ~3200 cycles, two thirds of them MMAs (QK 1056 + P.V
+// 1056); 32 row tiles of 8064 + 192 keys take 64 us with the merge.  Nothing is at
+// its limit there (tensor pipe 51 %, L2 34 %; a copy of the kernel that loaded half
+// of V took as long): it is bound by the roles' waits for one another and for their
+// instructions (1.9 warps of a quarter SM wait for one at every issue).
+// At D = 128 the softmax bounds it: ~1850 cycles a tile, a third of it exponentials.
 //
 // A gain, RoPE or a negative scale changes the query rows first, and rounding
 // them to bf16 again would cost as much accuracy as the output's own rounding
-// does (2.5e-3 instead of 2.0e-3 in all, against 64 bits).  A launch before
+// does (16 x 4 queries of 128 heads over 4096 entries, norm of the error against 64
+// bits by that of the output: 2.49e-3 instead of 1.85e-3, of which the output's
+// rounding is 1.66e-3).  A launch before
 // writes them as a sum of two bf16 numbers (hi + lo, 16 bits), and S gets both
 // products; lo passes through K's ring beside each piece of K, since at D = 512
 // shared memory has no room for it (64 queries x 128 heads over 4096 entries 74 ->

@@ -62,9 +62,9 @@ CSA_DEVINL uint4 ldg_stream(const void *p) {
 
 CSA_DEVINL uint4 ldg16(const void *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
 
-// Division of 0 <= n < 2^31 by a fixed d >= 1: n / d = (n * mul) >> (32 + shift), mul =
-// ceil(2^(31 + ceil(log2 d)) / d); 1 by itself (a runtime division is ~100 cycles on the planner's
-// and the softmax warps' serial paths).
+// Division of 0 <= n < 2^31 by a fixed d >= 1 (division by invariant multiplication, Granlund and Montgomery 1994):
+// n / d = (n * mul) >> (32 + shift), mul = ceil(2^(31 + ceil(log2 d)) / d); 1 by itself (a runtime division is ~100
+// cycles on the planner's and the softmax warps' serial paths).
 struct FastDiv {
     uint32_t d, mul, shift;
     static FastDiv by(uint32_t d) {  // on the host
@@ -178,7 +178,9 @@ CSA_DEVINL void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes, bool pred = 
 // address).  They order nothing at cluster scope by themselves: a release there
 // waits for the thread's outstanding memory operations (measured: 16 of them per
 // tile doubled the time of attend_prefix.cu's tile).  What the other CTA's
-// tensor core reads of this CTA is ordered by the proxy and tcgen05 fences before the arrival.
+// tensor core reads of this CTA is ordered by the proxy and tcgen05 fences before the arrival.  (The memory model
+// asks for cluster scope on both sides of such a hand-over.  That the fences do without it rests on what the hardware
+// does: some seven million calls of all shapes, repeated to the bit.)
 CSA_DEVINL void mbar_arrive_cluster(uint32_t bar, bool pred = true) {
     asm volatile(
         "{\n\t.reg .pred g;\n\tsetp.ne.b32 g, %1, 0;\n\t"
