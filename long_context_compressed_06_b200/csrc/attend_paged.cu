@@ -44,7 +44,7 @@ struct MergeArgs {
 // their rows, under weights of 0 where a row does not take a key, and 0 x NaN or infinity reaches the row all the
 // same.  Such rows (`bad`: NaN in these 8 dims under a sum that is none) are computed anew here, from their own
 // keys only, by the whole block: lane i of every warp has row `row` (t < 0: none) with 8 dims from d0 on, the
-// warps take the scores of 16 keys at a time in turn, the threads with `bad` their dims.  A row whose own keys make
+// warps take the scores of four keys each at a time, the threads with `bad` their dims.  A row whose own keys make
 // it NaN (an infinity under a score of -inf) gets it again.  In 32 bits, at its leisure: 96 requests of 16 heads over
 // 16K entries take 5.8 ms instead of 43 us if one request's window holds an infinity, but nothing else gets here.
 // (Looking through the keys before P V instead, 16 KiB a tile and SM, took 9 us of every such call.)
@@ -94,11 +94,15 @@ __device__ __noinline__ void redo_rows(const MergeArgs &g, int row, bool active,
             uint32_t at = kNoKey;
             if (k < n && k >= entries) {
                 at = kRingKey | (uint32_t)(b * a.win_rows + (u0 + (k - entries)) % a.win_rows);
-            } else if (k < n && g.own_cap >= 0) {
-                at = (uint32_t)(k < g.n_shared ? k : g.n_shared + b * g.own_cap + (k - g.n_shared));
             } else if (k < n) {
-                const int id = __ldg(a.table + b * a.max_pages + k / a.page);
-                if (id >= 0 && id < a.n_pages) at = (uint32_t)((long long)id * a.page + k % a.page);
+                const bool shared = k < g.n_shared;
+                const int id = __ldg(a.table + (shared ? 0 : b * a.max_pages) + k / a.page);
+                if (id < 0 || id >= a.n_pages) {  // (the copy has zeros there)
+                } else if (g.own_cap >= 0) {
+                    at = (uint32_t)(shared ? k : g.n_shared + b * g.own_cap + (k - g.n_shared));
+                } else {
+                    at = (uint32_t)((long long)id * a.page + k % a.page);
+                }
             }
             place[kRedoEach * warp + i][lane] = at;
             x[i] = at == kNoKey ? hi : values(at);  // (a score that is not used)
@@ -330,8 +334,7 @@ constexpr long long kMaxCopyBytes = 1LL << 30;
 // The host knows the tables' width, not the requests' lengths: `own` is what the width has room for.  The copy of an
 // FP8 cache takes ~0.12 us per MiB on top (32 x 128 heads over 8192 entries, 192 own ones in tables of 192 / 16000:
 // 77 and 141 us, 354 and 344 query by query); with that in the estimate too many calls of long requests go query
-// by query, whose FP8 time it puts too low (2 x 16 heads of 256 over 65536: 66 and 88 us, 8 x 8 of 512 over 16384 102
-// and 96), so it stands without.
+// by query (20 shapes where it decides: 1127 us in all with the rows together, 1258 without), so it stands without.
 // The gather kernel reads a query's window; attend_prefix.cu goes through every row of the ring and clears those
 // outside the window one by one, ~6 us per 128 of them (32 x 128 heads over 2048 entries, rings of 2048 / 8192
 // rows: 59 / 59 us and 104 / 239; 64 x 16 heads over 4096: 92 / 92 and 120 / 366; 2 x 512 queries, 639 rows: 287 and 629).

@@ -249,3 +249,35 @@ def test_scores_of_minus_infinity_are_not_rows_without_keys(cuda, kw, by_row_til
     assert hit[b].any()
     rest = (torch.arange(len(hit), device=DEV) != b)
     assert not hit[rest].any() and got[rest].isfinite().all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_beside_a_key_that_is_not_finite_leave_out_missing_pages(cuda, fp8):
+    """Keys that are all alike (values 1 to 1.4, so that an output is as large as its terms): an entry without a page
+    that counted as a row of zeros would show, 160 of some 1100."""
+    name = "fp8_128" if fp8 else "part_seen_128"
+    c = Case(**dict(ROW_TILES[name], drop=[(None, 4 * i + 1, -1) for i in range(10)], seed=9))
+    assert c.by_row_tiles()
+    g = torch.Generator().manual_seed(3)
+
+    def rows(old):
+        codes = torch.randint(0x38, 0x3C, old.shape, generator=g).to(torch.uint8).to(DEV)
+        if fp8:
+            return torch.where(old == 0x7F, old, codes)
+        return torch.where(old.isnan(), old, codes.view(torch.float8_e4m3fn).to(torch.bfloat16))
+
+    c.pool, c.ring = rows(c.pool), rows(c.ring)
+    if fp8:
+        c.pe, c.re = torch.where(c.pe == 255, c.pe, 127), torch.where(c.re == 255, c.re, 127)
+    (kind, i, r), takes = key_places(c, "newest_token")
+    getattr(c, kind)[i, r, 9] = 0x7F if fp8 else NAN
+    if fp8:
+        c.pool64, c.ring64 = dequant(c.pool, c.pe), dequant(c.ring, c.re)
+    else:
+        c.pool64, c.ring64 = c.pool.double(), c.ring.double()
+    got = c.run(cuda)
+    assert cuda.csa_sync_status() == 0
+    x = ~takes.to(DEV)
+    out, mag, e = c.ref()
+    assert got[x].isfinite().all() and (e == 0).all()
+    assert ((got[x].double() - out[x]).abs() <= 2.0 ** -8 * out[x].abs() + (2.0 ** -8 + 2.0 ** -10) * mag[x]).all()
